@@ -273,6 +273,126 @@ HIMUON_API himuon_status himuon_sign_pack(const float *o, int64_t rows, int64_t 
 HIMUON_API himuon_status himuon_sign_vote(const uint8_t *bits, int32_t workers, int64_t stride, int64_t n,
                                           himuon_dtype out_dtype, void *out, float scale, void *hip_stream);
 
+/* ---- The rest of a training step ----------------------------------------------------
+   HiMuon updates a model's matrices.  The entry points below are what stands next to it
+   in a training step: the loss with its gradient, the norm of the whole gradient with its
+   clip factor, and AdamW for every parameter that is not a matrix.  They are stateless
+   (no plan): the arrays of descriptors are read on the host during the call and may be
+   reused at once.  They enqueue only: no allocation, no wait for the GPU, so they may be
+   captured into a HIP graph (with the arguments of the capturing call).               */
+
+/* Clipped policy loss with a KL term, over `rows` sampled tokens with `vocab` logits each.
+   With z = logits / temperature, lp = z[label] - log sum_j exp z[j],
+     rho = exp(lp - old_logp) (1 where old_logp is NULL), u = rho A,
+     c = min(max(rho, 1 - clip_low), 1 + clip_high) A,
+     kl = exp(ref_logp - lp) - (ref_logp - lp) - 1 (0 where ref_logp is NULL),
+     loss = sum over rows of weight (kl_coef kl - min(u, c))
+   and, where dlogits is not NULL, with p = softmax(z) and old_logp a constant (where
+   it is NULL, too: the gradient at rho = 1),
+     dlogits[j] = grad_scale weight / temperature
+                  (-(u <= c ? u : 0) + kl_coef (1 - exp(ref_logp - lp))) ((j == label) - p[j]).
+   A row whose weight is zero or whose label is outside [0, vocab) is left out: nothing of
+   its logits, advantage or log probabilities is read, its logp is 0, its dlogits are 0 and
+   it adds nothing to the sums.  Logits of -inf have probability 0; a row with NaN or +inf
+   among its logits, or with nothing but -inf, gives NaN.                               */
+typedef struct {
+  int64_t rows, vocab;           /* >= 0, >= 1                                          */
+  int64_t ld_logits, ld_dlogits; /* leading dimensions in elements, >= vocab            */
+  const void *logits;            /* device, dtype                                       */
+  void *dlogits;                 /* device, dtype, or NULL: no gradient.  May be logits
+                                    itself (ld_dlogits == ld_logits); must not overlap it
+                                    otherwise                                           */
+  const int64_t *label;          /* device, rows                                        */
+  const float *weight;           /* device, rows                                        */
+  const float *advantage;        /* device, rows                                        */
+  const float *old_logp;         /* device, rows, or NULL                               */
+  const float *ref_logp;         /* device, rows, or NULL                               */
+  float *logp;                   /* device, rows: lp                                    */
+  float *stats;                  /* device, 4: loss, and the sums over rows of weight
+                                    times -min(u, c), kl, and [u > c] (clipped)         */
+  himuon_dtype dtype;            /* of logits and dlogits                               */
+  double clip_low, clip_high;    /* >= 0, clip_low <= 1                                 */
+  double kl_coef;                /* finite                                              */
+  double temperature;            /* in [2^-20, 2^20]                                    */
+  double grad_scale;             /* finite; multiplies dlogits only                     */
+} himuon_policy;
+
+/* Workspace bytes himuon_policy_loss needs for this call (device memory, 8-byte aligned,
+   contents immaterial). */
+HIMUON_API himuon_status himuon_policy_workspace(const himuon_policy *p, size_t *bytes);
+
+/* Enqueues the loss (and its gradient) on hip_stream.  Sums over rows and over the
+   vocabulary have a fixed order: the same call gives the same bits.  EINVAL: NULL
+   pointers with rows > 0 (stats always), bad sizes, leading dimensions, scalars or dtype,
+   a short or misaligned workspace.  EDEVICE: launch failure.                           */
+HIMUON_API himuon_status himuon_policy_loss(const himuon_policy *p, void *workspace, size_t ws_bytes,
+                                            void *hip_stream);
+
+/* One tensor of a gradient: n contiguous elements on the device. */
+typedef struct {
+  int64_t n;
+  const void *grad;
+} himuon_grad;
+
+/* Workspace bytes of himuon_grad_norm over n_tensors tensors (8-byte aligned, contents
+   immaterial). */
+HIMUON_API himuon_status himuon_grad_norm_workspace(int32_t n_tensors, size_t *bytes);
+
+/* out[0] = the 2-norm of all tensors together, out[1] = the factor that clips it:
+   min(1, max_norm / (norm + 1e-6)), or NaN where the norm is not finite in exact arithmetic
+   (an infinity or a NaN among the elements).  Squares are summed in fp64 in a fixed order, so
+   no finite gradient overflows.  out: device, two floats.  EINVAL: bad arguments
+   (max_norm is finite and >= 0), short or misaligned workspace.  EDEVICE: launch failure. */
+HIMUON_API himuon_status himuon_grad_norm(const himuon_grad *tensors, int32_t n_tensors, himuon_dtype dtype,
+                                          double max_norm, float *out, void *workspace, size_t ws_bytes,
+                                          void *hip_stream);
+
+/* Elements that share one scale of the 8-bit AdamW states. */
+#define HIMUON_ADAMW_BLOCK 256
+
+/* One parameter tensor of an AdamW step: n contiguous elements (any element alignment). */
+typedef struct {
+  int64_t n;
+  void *weight;                  /* device, weight_dtype, updated in place              */
+  const void *grad;              /* device, grad_dtype                                  */
+  void *m, *v;                   /* device, updated in place; state_bits 32: fp32, the first
+                                    and second moment.  state_bits 8: OCP e4m3 bytes, the
+                                    first moment and the square root of the second      */
+  float *m_scale, *v_scale;      /* device, ceil(n / HIMUON_ADAMW_BLOCK) each, updated in
+                                    place: element i of m holds m[i] m_scale[i / 256]
+                                    (v, v_scale likewise).  8-bit states only           */
+  double weight_decay;           /* decoupled decay of this tensor                      */
+} himuon_adamw_tensor;
+
+typedef struct {
+  himuon_dtype weight_dtype, grad_dtype;
+  int32_t state_bits;            /* 32 or 8                                             */
+  double beta1, beta2;           /* in [0, 1)                                           */
+  double eps;                    /* >= 1e-30                                            */
+} himuon_adamw_config;
+
+/* One AdamW step over all tensors (step number t >= 1), in fp32 per element:
+     g <- *grad_scale g (grad_scale: device, one float, or NULL for 1)
+     m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2
+     w <- w (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+   with w rounded to nearest even where weight_dtype is bf16.  Where *grad_scale is NaN
+   (himuon_grad_norm's factor for a gradient that is not finite) the step changes nothing.
+   8-bit states: the step computes with the fp32 moments and then stores m and r = sqrt(v)
+   by blocks of 256 elements: peak = the block's largest magnitude, scale = peak / 448, and
+   y = |x| 448 / peak rounded to one of its two e4m3 neighbours, up with the probability of
+   its distance to the lower one: the upper 16 bits of (i C + dither[k]) mod 2^32, plus one
+   half, over 2^16 (i the element's index, k = 0 and C = 0x9E3779B1 for m, k = 1 and C =
+   0x85EBCA6B for r) are added to y in units of the neighbours' gap before it is cut off.
+   Rounding to nearest would hold a moment still that moves by less than half a gap a step.
+   dither: two random numbers of the caller, new ones for each step (host memory; NULL is
+   {0, 0}).  A nonzero r is stored as 2^-9 at least, so that no weight is divided by eps
+   alone while its m is not zero; a block with peak < 2^-100 is stored as zeros.
+   EINVAL: NULL pointers with n > 0, bad sizes, scalars, dtypes or bits; two tensors
+   must not share memory (not checked).  EDEVICE: launch failure.                       */
+HIMUON_API himuon_status himuon_adamw_step(const himuon_adamw_tensor *tensors, int32_t n_tensors,
+                                           const himuon_adamw_config *cfg, int64_t t, double lr,
+                                           const float *grad_scale, const uint32_t *dither, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,6 +19,8 @@ __all__ = [
     "himuon_plan_stats", "himuon_plan_tiles", "himuon_plan_destroy", "himuon_last_error",
     "himuon_plan_runtime_counts", "himuon_runtime_counts", "himuon_step_static", "STATIC_WORKSPACE_BYTES",
     "himuon_stream_step",
+    "himuon_policy", "himuon_policy_workspace", "himuon_policy_loss", "himuon_grad", "himuon_grad_norm_workspace",
+    "himuon_grad_norm", "himuon_adamw_tensor", "himuon_adamw_config", "himuon_adamw_step", "ADAMW_BLOCK",
     "HiMuon", "CUBIC", "QUINTIC", "TILE_FULL", "F32", "BF16", "PREC_F32", "PREC_BF16",
     "PREC_BF16X3", "PREC_BF16F8", "FLAG_WRITE_UPDATE", "FLAG_IDENTITY_MAP", "library_path", "EXPORTED",
 ]
@@ -31,6 +33,7 @@ PREC_F32, PREC_BF16, PREC_BF16X3, PREC_BF16F8 = 0, 1, 2, 3
 FLAG_WRITE_UPDATE = 1
 FLAG_IDENTITY_MAP = 2
 STATIC_WORKSPACE_BYTES = 64 << 20   # HIMUON_STATIC_WORKSPACE_BYTES
+ADAMW_BLOCK = 256                   # HIMUON_ADAMW_BLOCK
 
 STATUS = {0: "HIMUON_OK", -1: "HIMUON_EINVAL", -2: "HIMUON_EBUDGET", -3: "HIMUON_ENOMEM",
           -4: "HIMUON_EDEVICE", -5: "HIMUON_EUNSUPPORTED"}
@@ -39,7 +42,8 @@ STATUS = {0: "HIMUON_OK", -1: "HIMUON_EINVAL", -2: "HIMUON_EBUDGET", -3: "HIMUON
 EXPORTED = ("himuon_plan", "himuon_workspace_size", "himuon_step", "himuon_set_tile_schedule",
             "himuon_plan_stats", "himuon_plan_tiles", "himuon_plan_destroy", "himuon_last_error",
             "himuon_plan_runtime_counts", "himuon_step_static", "himuon_stream_step", "himuon_sign_pack",
-            "himuon_sign_vote")
+            "himuon_sign_vote", "himuon_policy_workspace", "himuon_policy_loss", "himuon_grad_norm_workspace",
+            "himuon_grad_norm", "himuon_adamw_step")
 
 
 class HiMuonError(RuntimeError):
@@ -87,6 +91,31 @@ class himuon_tile(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
+class himuon_policy(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("ld_logits", ctypes.c_int64), ("ld_dlogits", ctypes.c_int64),
+                ("logits", ctypes.c_void_p), ("dlogits", ctypes.c_void_p), ("label", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("advantage", ctypes.c_void_p), ("old_logp", ctypes.c_void_p),
+                ("ref_logp", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("stats", ctypes.c_void_p),
+                ("dtype", ctypes.c_int), ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
+                ("kl_coef", ctypes.c_double), ("temperature", ctypes.c_double), ("grad_scale", ctypes.c_double)]
+
+
+class himuon_grad(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("grad", ctypes.c_void_p)]
+
+
+class himuon_adamw_tensor(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("weight", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("weight_decay", ctypes.c_double)]
+
+
+class himuon_adamw_config(ctypes.Structure):
+    _fields_ = [("weight_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int), ("state_bits", ctypes.c_int32),
+                ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double)]
+
+
 def library_path() -> str:
     return os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhimuon.so")
 
@@ -118,6 +147,14 @@ def _load() -> ctypes.CDLL:
     lib.himuon_sign_pack.argtypes = [P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, P, P]
     lib.himuon_sign_vote.argtypes = [P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                      P, ctypes.c_float, P]
+    lib.himuon_policy_workspace.argtypes = [ctypes.POINTER(himuon_policy), ctypes.POINTER(ctypes.c_size_t)]
+    lib.himuon_policy_loss.argtypes = [ctypes.POINTER(himuon_policy), P, ctypes.c_size_t, P]
+    lib.himuon_grad_norm_workspace.argtypes = [ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.himuon_grad_norm.argtypes = [ctypes.POINTER(himuon_grad), ctypes.c_int32, ctypes.c_int, ctypes.c_double,
+                                     P, P, ctypes.c_size_t, P]
+    lib.himuon_adamw_step.argtypes = [ctypes.POINTER(himuon_adamw_tensor), ctypes.c_int32,
+                                      ctypes.POINTER(himuon_adamw_config), ctypes.c_int64, ctypes.c_double, P,
+                                      ctypes.POINTER(ctypes.c_uint32), P]
     lib.himuon_last_error.argtypes = []
     lib.himuon_last_error.restype = ctypes.c_char_p
     for name in EXPORTED:
@@ -203,6 +240,37 @@ def himuon_sign_vote(bits_ptr: int, workers: int, stride: int, n: int, out_dtype
                      scale: float, stream_ptr: int) -> None:
     _check(_lib.himuon_sign_vote(bits_ptr or None, workers, stride, n, out_dtype, out_ptr or None, scale,
                                  stream_ptr or None))
+
+
+def himuon_policy_workspace(p: himuon_policy) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.himuon_policy_workspace(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+def himuon_policy_loss(p: himuon_policy, workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> None:
+    _check(_lib.himuon_policy_loss(ctypes.byref(p), workspace_ptr or None, ws_bytes, stream_ptr or None))
+
+
+def himuon_grad_norm_workspace(n_tensors: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.himuon_grad_norm_workspace(n_tensors, ctypes.byref(n)))
+    return n.value
+
+
+def himuon_grad_norm(tensors, dtype: int, max_norm: float, out_ptr: int, workspace_ptr: int, ws_bytes: int,
+                     stream_ptr: int) -> None:
+    """tensors: a ctypes array of himuon_grad."""
+    _check(_lib.himuon_grad_norm(tensors, len(tensors), dtype, max_norm, out_ptr or None, workspace_ptr or None,
+                                 ws_bytes, stream_ptr or None))
+
+
+def himuon_adamw_step(tensors, cfg: himuon_adamw_config, t: int, lr: float, grad_scale_ptr: int, dither,
+                      stream_ptr: int) -> None:
+    """tensors: a ctypes array of himuon_adamw_tensor; dither: None or two numbers in [0, 2^32)."""
+    d = None if dither is None else (ctypes.c_uint32 * 2)(*dither)
+    _check(_lib.himuon_adamw_step(tensors, len(tensors), ctypes.byref(cfg), t, lr, grad_scale_ptr or None, d,
+                                  stream_ptr or None))
 
 
 # ------------------------------------------------------------------ torch wrapper

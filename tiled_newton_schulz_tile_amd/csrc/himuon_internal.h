@@ -167,4 +167,26 @@ hipError_t launch_sign_pack(const float *o, int64_t rows, int64_t cols, int64_t 
 hipError_t launch_sign_vote(const unsigned char *bits, int workers, int64_t stride, int64_t n, bool out_bf16,
                             void *out, float scale, hipStream_t stream);
 
+// ---- AdamW and the gradient norm over many tensors (adamw.hip) -------------------
+// The constants of one AdamW step, rounded to fp32 from the caller's doubles.
+struct AdamWParams {
+  float beta1, omb1;       // beta1, 1 - beta1
+  float beta2, omb2;
+  float root_scale;        // 1 / sqrt(1 - beta2^t)
+  float eps;
+  float step;              // lr / (1 - beta1^t)
+  uint32_t dither[2];
+  const float *grad_scale; // device, or nullptr
+};
+hipError_t launch_adamw(const himuon_adamw_tensor *tensors, int32_t n_tensors, bool weight_bf16, bool grad_bf16,
+                        int state_bits, double lr, const AdamWParams &p, hipStream_t stream);
+
+size_t grad_norm_workspace(int32_t n_tensors);
+hipError_t launch_grad_norm(const himuon_grad *tensors, int32_t n_tensors, bool bf16, double max_norm, float *out,
+                            void *workspace, hipStream_t stream);
+
+// ---- clipped policy loss (policy.hip) -------------------------------------------
+size_t policy_workspace(const himuon_policy &p);
+hipError_t launch_policy(const himuon_policy &p, void *workspace, hipStream_t stream);
+
 }  // namespace himuon
