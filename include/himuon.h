@@ -334,8 +334,9 @@ typedef struct {
   const void *grad;
 } himuon_grad;
 
-/* Workspace bytes of himuon_grad_norm over n_tensors tensors (8-byte aligned, contents
-   immaterial). */
+/* Workspace bytes of himuon_grad_norm over n_tensors tensors (8-byte aligned).  Its first
+   eight bytes must be zero before its first call; every call leaves them zero.  Calls that
+   share a workspace go on one stream (or the caller orders them). */
 HIMUON_API himuon_status himuon_grad_norm_workspace(int32_t n_tensors, size_t *bytes);
 
 /* out[0] = the 2-norm of all tensors together, out[1] = the factor that clips it:
@@ -387,11 +388,24 @@ typedef struct {
    dither: two random numbers of the caller, new ones for each step (host memory; NULL is
    {0, 0}).  A nonzero r is stored as 2^-9 at least, so that no weight is divided by eps
    alone while its m is not zero; a block with peak < 2^-100 is stored as zeros.
+   table: NULL, or device memory that holds what himuon_adamw_table wrote for these tensors
+   and this config: the step is then one launch however many tensors there are; without it
+   the descriptors go in the kernel arguments, some 56 (8-bit states) or 72 tensors a launch.
    EINVAL: NULL pointers with n > 0, bad sizes, scalars, dtypes or bits; two tensors
    must not share memory (not checked).  EDEVICE: launch failure.                       */
 HIMUON_API himuon_status himuon_adamw_step(const himuon_adamw_tensor *tensors, int32_t n_tensors,
                                            const himuon_adamw_config *cfg, int64_t t, double lr,
-                                           const float *grad_scale, const uint32_t *dither, void *hip_stream);
+                                           const float *grad_scale, const uint32_t *dither, const void *table,
+                                           void *hip_stream);
+
+/* Descriptors of many tensors for the device: *bytes is 0 where one launch holds them in
+   its arguments anyway, else the size of the table.  himuon_adamw_table writes it into host
+   memory (8-byte aligned), from where the caller copies it to device memory (16-byte
+   aligned); it holds for as long as no pointer, size or weight_decay of the tensors changes. */
+HIMUON_API himuon_status himuon_adamw_table_size(const himuon_adamw_tensor *tensors, int32_t n_tensors,
+                                                 const himuon_adamw_config *cfg, size_t *bytes);
+HIMUON_API himuon_status himuon_adamw_table(const himuon_adamw_tensor *tensors, int32_t n_tensors,
+                                            const himuon_adamw_config *cfg, void *host, size_t bytes);
 
 #ifdef __cplusplus
 }

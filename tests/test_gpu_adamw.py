@@ -388,3 +388,29 @@ def test_wrapper_refusals():
         GradNorm([G]).compute(float("inf"))
     with pytest.raises(ValueError):
         GradNorm([G]).compute(1.0, out=torch.zeros(3, device=DEV))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_table_equals_arguments(bits):
+    """The descriptors in a device table (what AdamW uses for many tensors) give the bits of those in the arguments,
+    and set_grads reaches the table."""
+    _need_gpu()
+    sizes = [(37 * k) % 2111 + 1 for k in range(150)]
+    make = tensors32 if bits == 32 else tensors8
+    a, b = make(sizes, F32, F32, 8), make(sizes, F32, F32, 8)
+    opt = AdamW(a, weight_decay=0.1)
+    assert opt._table is not None
+    opt.step(1e-2, 1, dither=(7, 8))
+    stream = torch.cuda.current_stream().cuda_stream
+    opt_b = AdamW(b, weight_decay=0.1)
+    hm.himuon_adamw_step(opt_b._c, opt_b.cfg, 1, 1e-2, 0, (7, 8), 0, stream)
+    new = [torch.randn(n, generator=torch.Generator().manual_seed(n)).to(DEV) for n in sizes]
+    opt.set_grads(new)
+    opt.step(1e-2, 2, dither=(9, 10))
+    for t, g in zip(b, new):
+        t[1].copy_(g)
+    hm.himuon_adamw_step(opt_b._c, opt_b.cfg, 2, 1e-2, 0, (9, 10), 0, stream)
+    for x, y in zip(a, b):
+        for k in range(len(x)):
+            if k != 1:
+                assert torch.equal(x[k].view(torch.uint8), y[k].view(torch.uint8))

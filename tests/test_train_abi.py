@@ -57,24 +57,24 @@ def config(**kw):
 @pytest.mark.parametrize("kw", [dict(n=-1), dict(n=1 << 41), dict(weight=None), dict(grad=None), dict(m=None), dict(v=None),
                                 dict(m_scale=None), dict(v_scale=None), dict(weight_decay=float("nan"))])
 def test_adamw_refuses_tensors(kw):
-    refused(hm.himuon_adamw_step, tensors({}, kw), config(), 1, 0.1, 0, None, 0)
+    refused(hm.himuon_adamw_step, tensors({}, kw), config(), 1, 0.1, 0, None, 0, 0)
 
 
 @pytest.mark.parametrize("kw", [dict(weight_dtype=2), dict(grad_dtype=-1), dict(state_bits=16), dict(beta1=1.0),
                                 dict(beta2=-0.1), dict(beta1=float("nan")), dict(eps=0.0), dict(eps=float("inf"))])
 def test_adamw_refuses_configs(kw):
-    refused(hm.himuon_adamw_step, tensors({}), config(**kw), 1, 0.1, 0, None, 0)
+    refused(hm.himuon_adamw_step, tensors({}), config(**kw), 1, 0.1, 0, None, 0, 0)
 
 
 def test_adamw_refuses_steps():
-    refused(hm.himuon_adamw_step, tensors({}), config(), 0, 0.1, 0, None, 0)
-    refused(hm.himuon_adamw_step, tensors({}), config(), 1, float("inf"), 0, None, 0)
-    refused(hm.himuon_adamw_step, tensors(dict(n=1 << 40), dict(n=1)), config(), 1, 0.1, 0, None, 0)
+    refused(hm.himuon_adamw_step, tensors({}), config(), 0, 0.1, 0, None, 0, 0)
+    refused(hm.himuon_adamw_step, tensors({}), config(), 1, float("inf"), 0, None, 0, 0)
+    refused(hm.himuon_adamw_step, tensors(dict(n=1 << 40), dict(n=1)), config(), 1, 0.1, 0, None, 0, 0)
 
 
 def test_adamw_nothing_to_do():
-    hm.himuon_adamw_step(tensors(), config(), 1, 0.1, 0, None, 0)
-    hm.himuon_adamw_step(tensors(dict(n=0, weight=None, grad=None, m=None, v=None)), config(), 1, 0.1, 0, None, 0)
+    hm.himuon_adamw_step(tensors(), config(), 1, 0.1, 0, None, 0, 0)
+    hm.himuon_adamw_step(tensors(dict(n=0, weight=None, grad=None, m=None, v=None)), config(), 1, 0.1, 0, None, 0, 0)
 
 
 def test_grad_norm_refuses():
@@ -96,3 +96,18 @@ def test_structures_have_the_headers_sizes():
     assert ctypes.sizeof(hm.himuon_grad) == 16
     assert ctypes.sizeof(hm.himuon_adamw_tensor) == 64
     assert ctypes.sizeof(hm.himuon_adamw_config) == 16 + 24
+
+
+def test_adamw_table_refuses():
+    many = tensors(*[{}] * 100)
+    n = hm.himuon_adamw_table_size(many, config())
+    assert n > 0 and hm.himuon_adamw_table_size(tensors({}), config()) == 0
+    host = (ctypes.c_uint64 * (n // 8 + 1))()
+    at = ctypes.addressof(host)
+    hm.himuon_adamw_table(many, config(), at, n)
+    refused(hm.himuon_adamw_table, many, config(), at, n - 1)
+    refused(hm.himuon_adamw_table, many, config(), at + 4, n)
+    refused(hm.himuon_adamw_table, many, config(), 0, n)
+    refused(hm.himuon_adamw_table, tensors(dict(m=None)), config(), at, n)
+    refused(hm.himuon_adamw_table_size, tensors(dict(n=-1)), config())
+    refused(hm.himuon_adamw_step, many, config(), 1, 0.1, 0, None, FAKE + 8, 0)

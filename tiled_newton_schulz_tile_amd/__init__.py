@@ -20,7 +20,8 @@ __all__ = [
     "himuon_plan_runtime_counts", "himuon_runtime_counts", "himuon_step_static", "STATIC_WORKSPACE_BYTES",
     "himuon_stream_step",
     "himuon_policy", "himuon_policy_workspace", "himuon_policy_loss", "himuon_grad", "himuon_grad_norm_workspace",
-    "himuon_grad_norm", "himuon_adamw_tensor", "himuon_adamw_config", "himuon_adamw_step", "ADAMW_BLOCK",
+    "himuon_grad_norm", "himuon_adamw_tensor", "himuon_adamw_config", "himuon_adamw_step",
+    "himuon_adamw_table_size", "himuon_adamw_table", "ADAMW_BLOCK",
     "HiMuon", "CUBIC", "QUINTIC", "TILE_FULL", "F32", "BF16", "PREC_F32", "PREC_BF16",
     "PREC_BF16X3", "PREC_BF16F8", "FLAG_WRITE_UPDATE", "FLAG_IDENTITY_MAP", "library_path", "EXPORTED",
 ]
@@ -43,7 +44,7 @@ EXPORTED = ("himuon_plan", "himuon_workspace_size", "himuon_step", "himuon_set_t
             "himuon_plan_stats", "himuon_plan_tiles", "himuon_plan_destroy", "himuon_last_error",
             "himuon_plan_runtime_counts", "himuon_step_static", "himuon_stream_step", "himuon_sign_pack",
             "himuon_sign_vote", "himuon_policy_workspace", "himuon_policy_loss", "himuon_grad_norm_workspace",
-            "himuon_grad_norm", "himuon_adamw_step")
+            "himuon_grad_norm", "himuon_adamw_step", "himuon_adamw_table_size", "himuon_adamw_table")
 
 
 class HiMuonError(RuntimeError):
@@ -154,7 +155,11 @@ def _load() -> ctypes.CDLL:
                                      P, P, ctypes.c_size_t, P]
     lib.himuon_adamw_step.argtypes = [ctypes.POINTER(himuon_adamw_tensor), ctypes.c_int32,
                                       ctypes.POINTER(himuon_adamw_config), ctypes.c_int64, ctypes.c_double, P,
-                                      ctypes.POINTER(ctypes.c_uint32), P]
+                                      ctypes.POINTER(ctypes.c_uint32), P, P]
+    lib.himuon_adamw_table_size.argtypes = [ctypes.POINTER(himuon_adamw_tensor), ctypes.c_int32,
+                                            ctypes.POINTER(himuon_adamw_config), ctypes.POINTER(ctypes.c_size_t)]
+    lib.himuon_adamw_table.argtypes = [ctypes.POINTER(himuon_adamw_tensor), ctypes.c_int32,
+                                       ctypes.POINTER(himuon_adamw_config), P, ctypes.c_size_t]
     lib.himuon_last_error.argtypes = []
     lib.himuon_last_error.restype = ctypes.c_char_p
     for name in EXPORTED:
@@ -266,11 +271,22 @@ def himuon_grad_norm(tensors, dtype: int, max_norm: float, out_ptr: int, workspa
 
 
 def himuon_adamw_step(tensors, cfg: himuon_adamw_config, t: int, lr: float, grad_scale_ptr: int, dither,
-                      stream_ptr: int) -> None:
-    """tensors: a ctypes array of himuon_adamw_tensor; dither: None or two numbers in [0, 2^32)."""
+                      table_ptr: int, stream_ptr: int) -> None:
+    """tensors: a ctypes array of himuon_adamw_tensor; dither: None or two numbers in [0, 2^32); table_ptr: 0 or
+    the device address of the tensors' table."""
     d = None if dither is None else (ctypes.c_uint32 * 2)(*dither)
     _check(_lib.himuon_adamw_step(tensors, len(tensors), ctypes.byref(cfg), t, lr, grad_scale_ptr or None, d,
-                                  stream_ptr or None))
+                                  table_ptr or None, stream_ptr or None))
+
+
+def himuon_adamw_table_size(tensors, cfg: himuon_adamw_config) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.himuon_adamw_table_size(tensors, len(tensors), ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def himuon_adamw_table(tensors, cfg: himuon_adamw_config, host_ptr: int, size: int) -> None:
+    _check(_lib.himuon_adamw_table(tensors, len(tensors), ctypes.byref(cfg), host_ptr or None, size))
 
 
 # ------------------------------------------------------------------ torch wrapper

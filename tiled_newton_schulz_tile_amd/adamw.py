@@ -7,18 +7,41 @@ format and conventions are in include/himuon.h.
 """
 from __future__ import annotations
 
-from . import (ADAMW_BLOCK, BF16, F32, himuon_adamw_config, himuon_adamw_step, himuon_adamw_tensor, himuon_grad,
-               himuon_grad_norm, himuon_grad_norm_workspace)
+import struct
+from array import array
+
+from . import (ADAMW_BLOCK, BF16, F32, himuon_adamw_config, himuon_adamw_step, himuon_adamw_table,
+               himuon_adamw_table_size, himuon_adamw_tensor, himuon_grad, himuon_grad_norm, himuon_grad_norm_workspace)
 
 
-def _dtype(t):
-    import torch
-    return F32 if t.dtype == torch.float32 else BF16
+def _column(tensors, name, dtypes, device):
+    """(element counts, addresses) of tensors that share one dtype out of `dtypes`."""
+    dtype = tensors[0].dtype
+    if dtype not in dtypes or device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
+    for t in tensors:
+        if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+            raise ValueError(f"every {name} must be a contiguous {dtype} tensor on {device}")
+    return [t.numel() for t in tensors], [t.data_ptr() for t in tensors]
 
 
-def _check_tensor(t, name, dtypes, device):
-    if t.dtype not in dtypes or not t.is_cuda or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {' or '.join(str(d) for d in dtypes)} on {device}")
+def _stream(torch, stream, device):
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+class _on:
+    """Makes `device` the current one where it is not (the library launches on the current device)."""
+
+    def __init__(self, torch, device):
+        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
 
 
 def adamw_state(W, bits: int = 32):
@@ -53,72 +76,91 @@ class AdamW:
     with 8-bit states (adamw_state makes both).  All W share one dtype (float32 or
     bfloat16), all G share one, and all states are of one kind.  weight_decay is one number
     or one per tensor.  The tensors are referenced, not copied; set_grads replaces the
-    gradients (a training program whose gradients are new tensors each step)."""
+    gradients (a training program whose gradients are new tensors each step).  For more
+    tensors than one launch takes in its arguments the descriptors are kept on the device;
+    set_grads and the steps after it then go on one stream."""
 
     def __init__(self, tensors, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0):
         import torch
         self._torch = torch
-        self.tensors = [tuple(t) for t in tensors]
-        if not self.tensors:
+        tensors = [tuple(t) for t in tensors]
+        if not tensors:
             raise ValueError("no tensors")
-        decay = [weight_decay] * len(self.tensors) if isinstance(weight_decay, (int, float)) else list(weight_decay)
-        if len(decay) != len(self.tensors):
+        if len({len(t) for t in tensors}) != 1 or len(tensors[0]) not in (4, 6):
+            raise ValueError("every tensor is (W, G, m, v), or every one (W, G, m, r, m_scale, r_scale)")
+        decay = [weight_decay] * len(tensors) if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        if len(decay) != len(tensors):
             raise ValueError("one weight_decay per tensor")
-        first = self.tensors[0]
-        if len(first) not in (4, 6):
-            raise ValueError("a tensor is (W, G, m, v) or (W, G, m, r, m_scale, r_scale)")
-        self.bits = 32 if len(first) == 4 else 8
-        self.device = first[0].device
+        cols = list(zip(*tensors))
+        self.bits = 32 if len(cols) == 4 else 8
+        self.device = cols[0][0].device
         floats = (torch.float32, torch.bfloat16)
         state = (torch.float32,) if self.bits == 32 else (torch.float8_e4m3fn,)
-        self._c = (himuon_adamw_tensor * len(self.tensors))()
-        for c, t, wd in zip(self._c, self.tensors, decay):
-            if len(t) != len(first):
-                raise ValueError("all states must be of one kind")
-            n = t[0].numel()
-            _check_tensor(t[0], "W", floats if t is first else (first[0].dtype,), self.device)
-            _check_tensor(t[1], "G", floats if t is first else (first[1].dtype,), self.device)
-            for x in t[2:4]:
-                _check_tensor(x, "a state", state, self.device)
-            for x in t[1:4]:
-                if x.numel() != n:
-                    raise ValueError("W, G and the states must have the same number of elements")
-            for x in t[4:]:
-                _check_tensor(x, "a scale", (torch.float32,), self.device)
-                if x.numel() != -(-n // ADAMW_BLOCK):
-                    raise ValueError(f"a scale holds one value per {ADAMW_BLOCK} elements")
-            p = [x.data_ptr() for x in t]
-            c.n, c.weight, c.grad, c.m, c.v = n, p[0], p[1], p[2], p[3]
-            if self.bits == 8:
-                c.m_scale, c.v_scale = p[4], p[5]
-            c.weight_decay = wd
-        self.cfg = himuon_adamw_config(_dtype(first[0]), _dtype(first[1]), self.bits, betas[0], betas[1], eps)
+        n, w = _column(cols[0], "W", floats, self.device)
+        ptrs = [w]
+        for col, name, dtypes in zip(cols[1:4], ("G", "m", "v"), (floats, state, state)):
+            size, at = _column(col, name, dtypes, self.device)
+            if size != n:
+                raise ValueError("W, G and the states must have the same number of elements")
+            ptrs.append(at)
+        for col in cols[4:]:
+            size, at = _column(col, "scale", (torch.float32,), self.device)
+            if size != [-(-k // ADAMW_BLOCK) for k in n]:
+                raise ValueError(f"a scale holds one value per {ADAMW_BLOCK} elements")
+            ptrs.append(at)
+        if self.bits == 32:
+            ptrs += [[0] * len(n)] * 2
+        bits = [struct.unpack("q", struct.pack("d", d))[0] for d in decay]
+        self._words = array("Q")   # the C structures: n, six addresses, weight_decay
+        for row in zip(n, *ptrs, bits):
+            self._words.extend([x & (2 ** 64 - 1) for x in row])
+        self._c = (himuon_adamw_tensor * len(n)).from_buffer(self._words)
+        self._n, self._tensors = n, cols
+        dt = lambda t: F32 if t.dtype == torch.float32 else BF16  # noqa: E731
+        self.cfg = himuon_adamw_config(dt(cols[0][0]), dt(cols[1][0]), self.bits, betas[0], betas[1], eps)
+        size = himuon_adamw_table_size(self._c, self.cfg)
+        self._table = torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
+        if size:
+            host = array("Q", bytes(-(-size // 8) * 8))
+            himuon_adamw_table(self._c, self.cfg, host.buffer_info()[0], size)
+            self._table.copy_(torch.frombuffer(host, dtype=torch.uint8)[:size])   # done when it returns
 
-    def set_grads(self, grads) -> None:
+    @property
+    def tensors(self):
+        return list(zip(*self._tensors))
+
+    def set_grads(self, grads, stream=None) -> None:
         """Replaces the gradients from the next step on (same dtype and sizes)."""
-        grads = list(grads)
-        if len(grads) != len(self.tensors):
+        torch = self._torch
+        grads = tuple(grads)
+        if len(grads) != len(self._n):
             raise ValueError("one gradient per tensor")
-        for t, g in zip(self.tensors, grads):
-            _check_tensor(g, "G", (t[1].dtype,), self.device)
-            if g.numel() != t[0].numel():
-                raise ValueError("a gradient must have its weight's number of elements")
-        for k, (c, g) in enumerate(zip(self._c, grads)):
-            c.grad = g.data_ptr()
-            self.tensors[k] = (self.tensors[k][0], g, *self.tensors[k][2:])
+        size, at = _column(grads, "G", (self._tensors[1][0].dtype,), self.device)
+        if size != self._n:
+            raise ValueError("a gradient must have its weight's number of elements")
+        self._tensors[1] = grads
+        for c, p in zip(self._c, at):
+            c.grad = p
+        if self._table is not None:
+            host = torch.empty(self._table.numel() + 7, dtype=torch.uint8, pin_memory=True)
+            himuon_adamw_table(self._c, self.cfg, host.data_ptr(), host.numel())
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+                self._table.copy_(host[:self._table.numel()], non_blocking=True)
 
     def step(self, lr: float, t: int, scale=None, dither=None, stream=None) -> None:
         """Step number t >= 1.  scale: None or a float32 CUDA tensor whose first element multiplies
         the gradients (GradNorm's factor; NaN leaves everything unchanged).  dither: two random
         numbers in [0, 2^32), new ones each step, for 8-bit states."""
         torch = self._torch
+        at = 0
         if scale is not None:
             if scale.dtype != torch.float32 or scale.device != self.device or scale.numel() < 1:
                 raise ValueError(f"scale must be a float32 tensor on {self.device}")
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        with torch.cuda.device(self.device):
-            himuon_adamw_step(self._c, self.cfg, t, lr, scale.data_ptr() if scale is not None else 0, dither,
-                              s.cuda_stream)
+            at = scale.data_ptr()
+        with _on(torch, self.device):
+            himuon_adamw_step(self._c, self.cfg, t, lr, at, dither,
+                              self._table.data_ptr() if self._table is not None else 0,
+                              _stream(torch, stream, self.device))
 
 
 class GradNorm:
@@ -127,39 +169,44 @@ class GradNorm:
     def __init__(self, grads):
         import torch
         self._torch = torch
-        grads = list(grads)
+        grads = tuple(grads)
         if not grads:
             raise ValueError("no tensors")
         self.device = grads[0].device
-        self._dt = grads[0].dtype
-        self._c = (himuon_grad * len(grads))()
+        self._dtypes = (torch.float32, torch.bfloat16)
+        self._c = None
+        self._n = len(grads)
         self.set_grads(grads)
-        self._ws = torch.empty(himuon_grad_norm_workspace(len(grads)), dtype=torch.uint8, device=self.device)
+        self._dtypes = (grads[0].dtype,)
+        self._dt = F32 if grads[0].dtype == torch.float32 else BF16
+        self._ws = torch.zeros(himuon_grad_norm_workspace(len(grads)), dtype=torch.uint8, device=self.device)
+        torch.cuda.current_stream(self.device).synchronize()   # the zeros are there for a call on any stream
 
     def set_grads(self, grads) -> None:
         """Replaces the tensors (as many as before, of the same dtype)."""
-        torch = self._torch
-        grads = list(grads)
-        if len(grads) != len(self._c):
+        grads = tuple(grads)
+        if len(grads) != self._n:
             raise ValueError("as many gradients as before")
-        for g in grads:
-            _check_tensor(g, "a gradient", (self._dt,) if self._dt in (torch.float32, torch.bfloat16) else
-                          (torch.float32, torch.bfloat16), self.device)
-        self.grads = grads
-        for c, g in zip(self._c, grads):
-            c.n, c.grad = g.numel(), g.data_ptr()
+        n, at = _column(grads, "gradient", self._dtypes, self.device)
+        words = array("Q")
+        for row in zip(n, at):
+            words.extend(row)
+        self._words, self.grads = words, grads
+        self._c = (himuon_grad * len(n)).from_buffer(words)
 
     def compute(self, max_norm: float, out=None, stream=None):
         """A float32 CUDA tensor (norm, factor): the 2-norm over all tensors and min(1, max_norm / (norm + 1e-6)),
-        NaN where the gradient is not finite.  out: a tensor of two elements to write to instead of a new one.
-        Calls of one GradNorm share its workspace: they go on one stream, or the caller orders them."""
+        NaN where the gradient is not finite.  out: a tensor of two elements to write to instead of a new one
+        (allocated on the current stream).  Calls of one GradNorm share its workspace: they go on one stream, or
+        the caller orders them."""
         torch = self._torch
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        with torch.cuda.device(self.device), torch.cuda.stream(s):
-            if out is None:
-                out = torch.empty(2, dtype=torch.float32, device=self.device)
-            elif out.dtype != torch.float32 or out.shape != (2,) or out.device != self.device or not out.is_contiguous():
-                raise ValueError(f"out must be a contiguous float32 tensor of two elements on {self.device}")
-            himuon_grad_norm(self._c, _dtype(self.grads[0]), max_norm, out.data_ptr(), self._ws.data_ptr(),
-                             self._ws.numel(), s.cuda_stream)
+        if out is None:
+            out = torch.empty(2, dtype=torch.float32, device=self.device)
+            if stream is not None:
+                out.record_stream(stream)
+        elif out.dtype != torch.float32 or out.shape != (2,) or out.device != self.device or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous float32 tensor of two elements on {self.device}")
+        with _on(torch, self.device):
+            himuon_grad_norm(self._c, self._dt, max_norm, out.data_ptr(), self._ws.data_ptr(), self._ws.numel(),
+                             _stream(torch, stream, self.device))
         return out

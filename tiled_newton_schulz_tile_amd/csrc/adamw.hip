@@ -1,10 +1,11 @@
-// AdamW over many tensors in few launches, with fp32 or 8-bit states, and the norm of many
+// AdamW over many tensors in one launch, with fp32 or 8-bit states, and the norm of many
 // gradients.  Both are streams: every element of every tensor crosses HBM once.
 //
-// A launch covers up to kTensors tensors, whose descriptors travel in the kernel arguments
-// (so a call needs no table in device memory, no upload and no wait, and pointers may
-// change from step to step).  Every tensor is cut into chunks of kChunk elements, and a
-// block finds the tensor of its chunk by bisection of the first-chunk table.
+// The tensors' descriptors travel in the kernel arguments while they fit (so a call needs
+// no table in device memory, no upload and no wait, and pointers may change from step to
+// step), or in a table in device memory that the caller uploads once.  Every tensor is cut
+// into chunks of 1024 or 4096 elements; a block finds the tensor of its chunk with one load
+// per lane of the first-chunk table and a ballot.
 //
 // Tensors may start at any element (views of a flattened bucket do): vectors are declared
 // with the alignment of one element and the hardware takes unaligned global accesses.
@@ -19,10 +20,10 @@ namespace {
 using namespace dev;
 
 constexpr int THREADS = 256;
-constexpr int64_t kChunk = 4096;
 
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef unsigned short u16x4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned short u16x8u __attribute__((ext_vector_type(8), aligned(2)));
 typedef unsigned u32u __attribute__((aligned(1)));
 
 __device__ __forceinline__ float load1(const float *p, int64_t i) { return gmem(p)[i]; }
@@ -66,15 +67,14 @@ __device__ __forceinline__ void store_upto4(T *p, int64_t i, int n, f32x4 x) {
 }
 
 // ------------------------------------------------------------------ tables in arguments
-// 8-bit entries hold two scale pointers more; both tables stay under 4 KB with the rest of
-// the arguments.
+// One tensor.  8-bit entries hold two scale pointers more.
 template <int BITS>
 struct Entry {
   void *w;
   const void *g;
   void *m, *v;
   int64_t n;
-  float decay;   // 1 - lr weight_decay
+  float weight_decay;
 };
 template <>
 struct Entry<8> {
@@ -83,40 +83,58 @@ struct Entry<8> {
   void *m, *v;
   float *ms, *vs;
   int64_t n;
-  float decay;
+  float weight_decay;
 };
 template <int BITS>
-constexpr int kTensors = BITS == 8 ? 58 : 74;
+constexpr int kTensors = BITS == 8 ? 56 : 72;
 
 template <int BITS>
-struct AdamWTable {
-  int32_t n;
+struct ArgTable {
+  int32_t n, shift;                    // tensors; log2 of a chunk's elements
   int32_t first[kTensors<BITS> + 1];   // first chunk of each tensor; [n]: all chunks
   Entry<BITS> t[kTensors<BITS>];
+  __device__ __forceinline__ const int32_t *firsts() const { return first; }
+  __device__ __forceinline__ const Entry<BITS> *entries() const { return t; }
 };
-static_assert(sizeof(AdamWTable<32>) + sizeof(AdamWParams) <= 4096, "kernel arguments");
-static_assert(sizeof(AdamWTable<8>) + sizeof(AdamWParams) <= 4096, "kernel arguments");
+static_assert(sizeof(ArgTable<32>) + sizeof(AdamWParams) <= 4096, "kernel arguments");
+static_assert(sizeof(ArgTable<8>) + sizeof(AdamWParams) <= 4096, "kernel arguments");
 
-constexpr int kNormTensors = 200;
+// The same in device memory: n + 1 first chunks, then the entries at entry_offset(n).
+size_t entry_offset(int64_t n) { return ((size_t)(n + 1) * sizeof(int32_t) + 15) / 16 * 16; }
+template <int BITS>
+struct DeviceTable {
+  int32_t n, shift;
+  const int32_t *first;
+  const Entry<BITS> *t;
+  __device__ __forceinline__ const int32_t *firsts() const { return first; }
+  __device__ __forceinline__ const Entry<BITS> *entries() const { return t; }
+};
+
+constexpr int kNormTensors = 198;
 struct NormTable {
-  int32_t n;
+  int32_t n, shift;
   int32_t first[kNormTensors + 1];
   int64_t size[kNormTensors];
   const void *g[kNormTensors];
 };
 static_assert(sizeof(NormTable) + 64 <= 4096, "kernel arguments");
 
+// Chunks are small while the tensors together are (a call of a few hundred thousand
+// elements has to spread over 256 CUs, and each thread of a small chunk has one vector of
+// every operand in flight and is done), and large once the blocks would be many.
+constexpr int kSmallShift = 10, kLargeShift = 12;
+constexpr int64_t kSmallTotal = (int64_t)4 << 20;
+
 // The tensor that chunk c belongs to: the last one whose first chunk is <= c.  (Tensors
 // without elements are not in the table.)
-template <class TABLE>
-__device__ __forceinline__ int tensor_of(const TABLE &tab, int c) {
-  int lo = 0, hi = tab.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (tab.first[mid] <= c) lo = mid;
-    else hi = mid;
+__device__ __forceinline__ int tensor_of(const int32_t *first, int n, int c) {
+  const int lane = threadIdx.x & 63;
+  int count = 0;
+  for (int k = 0; k < n; k += 64) {
+    const bool le = k + lane < n && first[k + lane] <= c;
+    count += __builtin_popcountll(__ballot(le));
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(count - 1);
 }
 
 // ------------------------------------------------------------------ AdamW
@@ -130,25 +148,26 @@ __device__ __forceinline__ float adamw(float w, float g, float &m, float &v, flo
   return __builtin_fmaf(w, decay, -p.step * (m * __builtin_amdgcn_rcpf(den)));
 }
 
-template <typename W, typename G>
-__global__ __launch_bounds__(THREADS) void adamw32_kernel(AdamWTable<32> tab, AdamWParams p) {
+template <typename W, typename G, class TABLE>
+__global__ __launch_bounds__(THREADS) void adamw32_kernel(TABLE tab, AdamWParams p) {
   const float scale = p.grad_scale ? *gmem(p.grad_scale) : 1.f;
-  if (scale != scale) return;   // the gradient was not finite: nothing changes
-  const int c = blockIdx.x, ti = tensor_of(tab, c);
-  const Entry<32> &t = tab.t[ti];
+  const int c = blockIdx.x, ti = tensor_of(tab.firsts(), tab.n, c);
+  const Entry<32> &t = tab.entries()[ti];
   W *w = reinterpret_cast<W *>(t.w);
   const G *g = reinterpret_cast<const G *>(t.g);
   float *m = reinterpret_cast<float *>(t.m), *v = reinterpret_cast<float *>(t.v);
-  const int64_t base = (int64_t)(c - tab.first[ti]) * kChunk;
-  const int64_t end = t.n < base + kChunk ? t.n : base + kChunk;
+  const float decay = 1.f - p.lr * t.weight_decay;
+  const int64_t base = (int64_t)(c - tab.firsts()[ti]) << tab.shift;
+  const int64_t end = t.n - base < (1 << tab.shift) ? t.n : base + (1 << tab.shift);
   for (int64_t i = base + 4 * threadIdx.x; i < end; i += 4 * THREADS) {
     const int n = end - i < 4 ? (int)(end - i) : 4;
     const f32x4 gv = load_upto4(g, i, n);
     f32x4 mv = load_upto4(m, i, n), vv = load_upto4(v, i, n), wv = load_upto4(w, i, n);
+    if (scale != scale) return;   // the gradient was not finite: nothing changes
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float mm = mv[e], vq = vv[e], root;
-      wv[e] = adamw(wv[e], gv[e] * scale, mm, vq, root, t.decay, p);
+      wv[e] = adamw(wv[e], gv[e] * scale, mm, vq, root, decay, p);
       mv[e] = mm;
       vv[e] = vq;
     }
@@ -228,17 +247,17 @@ __device__ __forceinline__ f32x4 load_codes(const unsigned char *p, int64_t i, i
   return unpack_e4m3x4(word);
 }
 
-template <typename W, typename G>
-__global__ __launch_bounds__(THREADS) void adamw8_kernel(AdamWTable<8> tab, AdamWParams p) {
+template <typename W, typename G, class TABLE>
+__global__ __launch_bounds__(THREADS) void adamw8_kernel(TABLE tab, AdamWParams p) {
   const float scale = p.grad_scale ? *gmem(p.grad_scale) : 1.f;
-  if (scale != scale) return;   // the gradient was not finite: nothing changes
-  const int c = blockIdx.x, ti = tensor_of(tab, c);
-  const Entry<8> &t = tab.t[ti];
+  const int c = blockIdx.x, ti = tensor_of(tab.firsts(), tab.n, c);
+  const Entry<8> &t = tab.entries()[ti];
   W *w = reinterpret_cast<W *>(t.w);
   const G *g = reinterpret_cast<const G *>(t.g);
   unsigned char *m = reinterpret_cast<unsigned char *>(t.m), *r = reinterpret_cast<unsigned char *>(t.v);
-  const int64_t base = (int64_t)(c - tab.first[ti]) * kChunk;
-  const int64_t end = t.n < base + kChunk ? t.n : base + kChunk;
+  const float decay = 1.f - p.lr * t.weight_decay;
+  const int64_t base = (int64_t)(c - tab.firsts()[ti]) << tab.shift;
+  const int64_t end = t.n - base < (1 << tab.shift) ? t.n : base + (1 << tab.shift);
   const int lane = threadIdx.x & 63;
   // a wave takes whole blocks: every lane stays in the loop until its wave's block is done
   for (int64_t b = base + (int64_t)(threadIdx.x >> 6) * kBlock; b < end; b += THREADS / 64 * kBlock) {
@@ -248,11 +267,12 @@ __global__ __launch_bounds__(THREADS) void adamw8_kernel(AdamWTable<8> tab, Adam
     const float m_unit = *gmem(ms), r_unit = *gmem(vs);
     const f32x4 gv = load_upto4(g, i, n);
     f32x4 mv = load_codes(m, i, n), rv = load_codes(r, i, n), wv = load_upto4(w, i, n);
+    if (scale != scale) return;   // the gradient was not finite: nothing changes
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float r0 = rv[e] * r_unit;
       float mm = mv[e] * m_unit, vq = r0 * r0, root;
-      wv[e] = adamw(wv[e], gv[e] * scale, mm, vq, root, t.decay, p);
+      wv[e] = adamw(wv[e], gv[e] * scale, mm, vq, root, decay, p);
       // lanes beyond the tensor's end hold zeros throughout
       mv[e] = mm;
       rv[e] = root;
@@ -264,50 +284,97 @@ __global__ __launch_bounds__(THREADS) void adamw8_kernel(AdamWTable<8> tab, Adam
   }
 }
 
-template <int BITS, typename W, typename G>
-void launch_table(const AdamWTable<BITS> &tab, const AdamWParams &p, hipStream_t stream) {
-  const dim3 grid((unsigned)tab.first[tab.n]);
+template <int BITS, typename W, typename G, class TABLE>
+void launch_typed(const TABLE &tab, unsigned chunks, const AdamWParams &p, hipStream_t stream) {
   if constexpr (BITS == 32)
-    hipLaunchKernelGGL((adamw32_kernel<W, G>), grid, dim3(THREADS), 0, stream, tab, p);
+    hipLaunchKernelGGL((adamw32_kernel<W, G, TABLE>), dim3(chunks), dim3(THREADS), 0, stream, tab, p);
   else
-    hipLaunchKernelGGL((adamw8_kernel<W, G>), grid, dim3(THREADS), 0, stream, tab, p);
+    hipLaunchKernelGGL((adamw8_kernel<W, G, TABLE>), dim3(chunks), dim3(THREADS), 0, stream, tab, p);
+}
+template <int BITS, class TABLE>
+hipError_t launch_table(const TABLE &tab, int64_t chunks, bool weight_bf16, bool grad_bf16, const AdamWParams &p,
+                        hipStream_t stream) {
+  const unsigned c = (unsigned)chunks;
+  if (weight_bf16)
+    grad_bf16 ? launch_typed<BITS, __bf16, __bf16>(tab, c, p, stream) : launch_typed<BITS, __bf16, float>(tab, c, p, stream);
+  else
+    grad_bf16 ? launch_typed<BITS, float, __bf16>(tab, c, p, stream) : launch_typed<BITS, float, float>(tab, c, p, stream);
+  return hipGetLastError();
+}
+
+template <class TENSOR>
+int shift_of(const TENSOR *tensors, int32_t n_tensors) {
+  int64_t total = 0;
+  for (int32_t k = 0; k < n_tensors; ++k) total += tensors[k].n;
+  return total <= kSmallTotal ? kSmallShift : kLargeShift;
+}
+int64_t chunks_of(int64_t n, int shift) { return (n + ((int64_t)1 << shift) - 1) >> shift; }
+
+template <int BITS>
+void fill_entry(Entry<BITS> &t, const himuon_adamw_tensor &x) {
+  t.w = x.weight;
+  t.g = x.grad;
+  t.m = x.m;
+  t.v = x.v;
+  if constexpr (BITS == 8) {
+    t.ms = x.m_scale;
+    t.vs = x.v_scale;
+  }
+  t.n = x.n;
+  t.weight_decay = (float)x.weight_decay;
+}
+
+template <int BITS>
+void fill_table(const himuon_adamw_tensor *tensors, int32_t n_tensors, char *host) {
+  const int shift = shift_of(tensors, n_tensors);
+  int32_t *first = reinterpret_cast<int32_t *>(host);
+  Entry<BITS> *t = reinterpret_cast<Entry<BITS> *>(host + entry_offset(n_tensors));
+  int64_t at = 0;   // < 2^29: 2^40 elements in all and 2^24 tensors at most
+  int32_t n = 0;
+  for (int32_t k = 0; k < n_tensors; ++k) {
+    if (tensors[k].n == 0) continue;
+    first[n] = (int32_t)at;
+    fill_entry<BITS>(t[n], tensors[k]);
+    at += chunks_of(tensors[k].n, shift);
+    ++n;
+  }
+  first[n] = (int32_t)at;
 }
 
 template <int BITS>
 hipError_t launch_adamw_bits(const himuon_adamw_tensor *tensors, int32_t n_tensors, bool weight_bf16, bool grad_bf16,
-                             double lr, const AdamWParams &p, hipStream_t stream) {
-  AdamWTable<BITS> tab;
+                             const AdamWParams &p, const void *table, hipStream_t stream) {
+  const int shift = shift_of(tensors, n_tensors);
+  if (table) {
+    DeviceTable<BITS> tab{0, shift, reinterpret_cast<const int32_t *>(table),
+                          reinterpret_cast<const Entry<BITS> *>(reinterpret_cast<const char *>(table) +
+                                                                entry_offset(n_tensors))};
+    int64_t chunks = 0;
+    for (int32_t k = 0; k < n_tensors; ++k) {
+      tab.n += tensors[k].n > 0;
+      chunks += chunks_of(tensors[k].n, shift);
+    }
+    if (chunks == 0) return hipSuccess;
+    return launch_table<BITS>(tab, chunks, weight_bf16, grad_bf16, p, stream);
+  }
+  ArgTable<BITS> tab;
   tab.n = 0;
+  tab.shift = shift;
   tab.first[0] = 0;
   auto flush = [&]() -> hipError_t {
     if (tab.n == 0) return hipSuccess;
-    if (weight_bf16)
-      grad_bf16 ? launch_table<BITS, __bf16, __bf16>(tab, p, stream) : launch_table<BITS, __bf16, float>(tab, p, stream);
-    else
-      grad_bf16 ? launch_table<BITS, float, __bf16>(tab, p, stream) : launch_table<BITS, float, float>(tab, p, stream);
+    hipError_t e = launch_table<BITS>(tab, tab.first[tab.n], weight_bf16, grad_bf16, p, stream);
     tab.n = 0;
-    return hipGetLastError();
+    return e;
   };
   for (int32_t k = 0; k < n_tensors; ++k) {
-    const himuon_adamw_tensor &x = tensors[k];
-    if (x.n == 0) continue;
-    const int64_t chunks = (x.n + kChunk - 1) / kChunk;   // of all tensors: < 2^29 (n is 2^40 in all at most)
+    if (tensors[k].n == 0) continue;
     if (tab.n == kTensors<BITS>) {
       hipError_t e = flush();
       if (e != hipSuccess) return e;
     }
-    Entry<BITS> &t = tab.t[tab.n];
-    t.w = x.weight;
-    t.g = x.grad;
-    t.m = x.m;
-    t.v = x.v;
-    if constexpr (BITS == 8) {
-      t.ms = x.m_scale;
-      t.vs = x.v_scale;
-    }
-    t.n = x.n;
-    t.decay = (float)(1.0 - lr * x.weight_decay);
-    tab.first[tab.n + 1] = (int32_t)(tab.first[tab.n] + chunks);
+    fill_entry<BITS>(tab.t[tab.n], tensors[k]);
+    tab.first[tab.n + 1] = (int32_t)(tab.first[tab.n] + chunks_of(tensors[k].n, shift));
     ++tab.n;
   }
   return flush();
@@ -330,31 +397,60 @@ __device__ __forceinline__ double block_sum(double x, double *lds) {
   return s;
 }
 
+// 16 bytes of a gradient: squares into the sum
+__device__ __forceinline__ void add_squares(const float *p, double &sum) {
+  const f32x4 x = load4(p, 0);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum = __builtin_fma((double)x[e], (double)x[e], sum);
+}
+__device__ __forceinline__ void add_squares(const __bf16 *p, double &sum) {
+  const u16x8u h = *reinterpret_cast<const GLOBAL_AS u16x8u *>(gmem(p));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double x = (double)bf16_bits_to_f32(h[e]);
+    sum = __builtin_fma(x, x, sum);
+  }
+}
+
+// Each block leaves one partial sum; the last block to finish (the ticket says which) joins
+// all of them, those of the call's earlier launches among them, in a fixed order.
 template <typename G>
-__global__ __launch_bounds__(THREADS) void grad_norm_kernel(NormTable tab, double *part) {
+__global__ __launch_bounds__(THREADS) void grad_norm_kernel(NormTable tab, double *part, int64_t before, bool last,
+                                                            unsigned *ticket, double max_norm, float *out) {
   __shared__ double lds[THREADS / 64];
+  __shared__ bool joins;
+  constexpr int N = 16 / sizeof(G);
   double sum = 0;
   const int chunks = tab.first[tab.n];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int ti = tensor_of(tab, c);
+    const int ti = tensor_of(tab.first, tab.n, c);
     const G *g = reinterpret_cast<const G *>(tab.g[ti]);
-    const int64_t base = (int64_t)(c - tab.first[ti]) * kChunk, size = tab.size[ti];
-    const int64_t end = size < base + kChunk ? size : base + kChunk;
-    for (int64_t i = base + 4 * threadIdx.x; i < end; i += 4 * THREADS) {
-      const f32x4 x = load_upto4(g, i, end - i < 4 ? (int)(end - i) : 4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum = __builtin_fma((double)x[e], (double)x[e], sum);
+    const int64_t base = (int64_t)(c - tab.first[ti]) << tab.shift, size = tab.size[ti];
+    const int64_t end = size - base < (1 << tab.shift) ? size : base + (1 << tab.shift);
+#pragma unroll 4
+    for (int64_t i = base + N * threadIdx.x; i + N <= end; i += N * THREADS) add_squares(g + i, sum);
+    const int64_t rest = base + (end - base) / N * N + threadIdx.x;
+    if (rest < end) {
+      const double x = (double)load1(g, rest);
+      sum = __builtin_fma(x, x, sum);
     }
   }
   sum = block_sum(sum, lds);
-  if (threadIdx.x == 0) gmem(part)[blockIdx.x] = sum;
-}
-
-__global__ __launch_bounds__(1024) void grad_norm_join_kernel(const double *part, int64_t n, double max_norm,
-                                                              float *out) {
-  __shared__ double lds[16];
-  double sum = 0;
-  for (int64_t i = threadIdx.x; i < n; i += 1024) sum += gmem(part)[i];
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(&part[before + blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (last) {
+      // (the count wraps to zero with the last block, so that the next call finds it as this one did)
+      joins = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+      if (joins) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  if (!last) return;
+  __syncthreads();
+  if (!joins) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  sum = 0;
+  for (int64_t i = threadIdx.x; i < before + gridDim.x; i += THREADS)
+    sum += __hip_atomic_load(&part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   sum = block_sum(sum, lds);
   if (threadIdx.x != 0) return;
   const double norm = __builtin_sqrt(sum);
@@ -366,50 +462,61 @@ __global__ __launch_bounds__(1024) void grad_norm_join_kernel(const double *part
 }  // namespace
 
 hipError_t launch_adamw(const himuon_adamw_tensor *tensors, int32_t n_tensors, bool weight_bf16, bool grad_bf16,
-                        int state_bits, double lr, const AdamWParams &p, hipStream_t stream) {
-  return state_bits == 8 ? launch_adamw_bits<8>(tensors, n_tensors, weight_bf16, grad_bf16, lr, p, stream)
-                         : launch_adamw_bits<32>(tensors, n_tensors, weight_bf16, grad_bf16, lr, p, stream);
+                        int state_bits, const AdamWParams &p, const void *table, hipStream_t stream) {
+  return state_bits == 8 ? launch_adamw_bits<8>(tensors, n_tensors, weight_bf16, grad_bf16, p, table, stream)
+                         : launch_adamw_bits<32>(tensors, n_tensors, weight_bf16, grad_bf16, p, table, stream);
 }
 
-// One partial sum per block, kNormTensors tensors a launch.
+size_t adamw_table_size(int32_t n_tensors, int state_bits) {
+  return entry_offset(n_tensors) + (size_t)n_tensors * (state_bits == 8 ? sizeof(Entry<8>) : sizeof(Entry<32>));
+}
+void adamw_table(const himuon_adamw_tensor *tensors, int32_t n_tensors, int state_bits, void *host) {
+  if (state_bits == 8)
+    fill_table<8>(tensors, n_tensors, reinterpret_cast<char *>(host));
+  else
+    fill_table<32>(tensors, n_tensors, reinterpret_cast<char *>(host));
+}
+int adamw_arg_tensors(int state_bits) { return state_bits == 8 ? kTensors<8> : kTensors<32>; }
+
+// The ticket, then one partial sum per block and kNormTensors tensors a launch.
 size_t grad_norm_workspace(int32_t n_tensors) {
-  return ((size_t)n_tensors / kNormTensors + 1) * kNormBlocks * sizeof(double);
+  return ((size_t)n_tensors / kNormTensors + 1) * kNormBlocks * sizeof(double) + 8;
 }
 
 hipError_t launch_grad_norm(const himuon_grad *tensors, int32_t n_tensors, bool bf16, double max_norm, float *out,
                             void *workspace, hipStream_t stream) {
-  double *part = reinterpret_cast<double *>(workspace);
+  unsigned *ticket = reinterpret_cast<unsigned *>(workspace);
+  double *part = reinterpret_cast<double *>(workspace) + 1;
   int64_t parts = 0;
   NormTable tab;
   tab.n = 0;
+  tab.shift = shift_of(tensors, n_tensors) + 2;
   tab.first[0] = 0;
-  auto flush = [&]() -> hipError_t {
-    if (tab.n == 0) return hipSuccess;
-    const int grid = tab.first[tab.n] < kNormBlocks ? tab.first[tab.n] : kNormBlocks;
+  auto flush = [&](bool last) -> hipError_t {
+    const int chunks = tab.first[tab.n];   // none: the last block has nothing to add of its own
+    const int grid = chunks < 1 ? 1 : chunks < kNormBlocks ? chunks : kNormBlocks;
     if (bf16)
-      hipLaunchKernelGGL(grad_norm_kernel<__bf16>, dim3(grid), dim3(THREADS), 0, stream, tab, part + parts);
+      hipLaunchKernelGGL(grad_norm_kernel<__bf16>, dim3(grid), dim3(THREADS), 0, stream, tab, part, parts, last, ticket,
+                         max_norm, out);
     else
-      hipLaunchKernelGGL(grad_norm_kernel<float>, dim3(grid), dim3(THREADS), 0, stream, tab, part + parts);
+      hipLaunchKernelGGL(grad_norm_kernel<float>, dim3(grid), dim3(THREADS), 0, stream, tab, part, parts, last, ticket,
+                         max_norm, out);
     parts += grid;
     tab.n = 0;
     return hipGetLastError();
   };
   for (int32_t k = 0; k < n_tensors; ++k) {
     if (tensors[k].n == 0) continue;
-    const int64_t chunks = (tensors[k].n + kChunk - 1) / kChunk;
     if (tab.n == kNormTensors) {
-      hipError_t e = flush();
+      hipError_t e = flush(false);
       if (e != hipSuccess) return e;
     }
     tab.g[tab.n] = tensors[k].grad;
     tab.size[tab.n] = tensors[k].n;
-    tab.first[tab.n + 1] = (int32_t)(tab.first[tab.n] + chunks);
+    tab.first[tab.n + 1] = (int32_t)(tab.first[tab.n] + chunks_of(tensors[k].n, tab.shift));
     ++tab.n;
   }
-  hipError_t e = flush();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(grad_norm_join_kernel, dim3(1), dim3(1024), 0, stream, part, parts, max_norm, out);
-  return hipGetLastError();
+  return flush(true);
 }
 
 }  // namespace himuon

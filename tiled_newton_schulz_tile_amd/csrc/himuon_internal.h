@@ -175,11 +175,17 @@ struct AdamWParams {
   float root_scale;        // 1 / sqrt(1 - beta2^t)
   float eps;
   float step;              // lr / (1 - beta1^t)
+  float lr;
   uint32_t dither[2];
   const float *grad_scale; // device, or nullptr
 };
+// table: nullptr (descriptors in the kernel arguments, adamw_arg_tensors() a launch), or
+// device memory with what adamw_table wrote for these tensors (one launch).
 hipError_t launch_adamw(const himuon_adamw_tensor *tensors, int32_t n_tensors, bool weight_bf16, bool grad_bf16,
-                        int state_bits, double lr, const AdamWParams &p, hipStream_t stream);
+                        int state_bits, const AdamWParams &p, const void *table, hipStream_t stream);
+size_t adamw_table_size(int32_t n_tensors, int state_bits);
+void adamw_table(const himuon_adamw_tensor *tensors, int32_t n_tensors, int state_bits, void *host);
+int adamw_arg_tensors(int state_bits);
 
 size_t grad_norm_workspace(int32_t n_tensors);
 hipError_t launch_grad_norm(const himuon_grad *tensors, int32_t n_tensors, bool bf16, double max_norm, float *out,

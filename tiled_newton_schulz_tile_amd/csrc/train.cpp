@@ -21,6 +21,7 @@ bool is_dtype(himuon_dtype d) { return d == HIMUON_F32 || d == HIMUON_BF16; }
 
 // A tensor's bytes have to be addressable; its size is otherwise free.
 constexpr int64_t kMostElements = (int64_t)1 << 40;
+constexpr int32_t kMostTensors = 1 << 24;
 
 himuon_status check_workspace(const void *ws, size_t have, size_t need) {
   if (need == 0) return HIMUON_OK;
@@ -43,6 +44,26 @@ himuon_status check_policy(const himuon_policy *p) {
     return bad("clip_low must be in [0, 1] and clip_high finite and >= 0");
   if (!std::isfinite(p->kl_coef) || !std::isfinite(p->grad_scale)) return bad("kl_coef and grad_scale must be finite");
   if (!(p->temperature >= 0x1p-20 && p->temperature <= 0x1p20)) return bad("temperature must be in [2^-20, 2^20]");
+  return HIMUON_OK;
+}
+
+himuon_status check_adamw(const himuon_adamw_tensor *tensors, int32_t n_tensors, const himuon_adamw_config *cfg) {
+  if (n_tensors < 0 || (n_tensors > 0 && !tensors) || !cfg) return bad("bad argument");
+  if (n_tensors > kMostTensors) return bad("more than 2^24 tensors");
+  if (!is_dtype(cfg->weight_dtype) || !is_dtype(cfg->grad_dtype)) return bad("dtype");
+  if (cfg->state_bits != 32 && cfg->state_bits != 8) return bad("state_bits must be 32 or 8");
+  if (!(cfg->beta1 >= 0 && cfg->beta1 < 1 && cfg->beta2 >= 0 && cfg->beta2 < 1)) return bad("betas must be in [0, 1)");
+  if (!(cfg->eps >= 1e-30 && std::isfinite((float)cfg->eps))) return bad("eps must be finite and >= 1e-30");
+  int64_t total = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const himuon_adamw_tensor &x = tensors[i];
+    if (x.n < 0 || x.n > kMostElements - total) return bad("n must be >= 0, 2^40 in all at most");
+    total += x.n;
+    if (!std::isfinite((float)x.weight_decay)) return bad("weight_decay must be finite");
+    if (x.n == 0) continue;
+    if (!x.weight || !x.grad || !x.m || !x.v) return bad("NULL pointer");
+    if (cfg->state_bits == 8 && (!x.m_scale || !x.v_scale)) return bad("8-bit states need their scales");
+  }
   return HIMUON_OK;
 }
 
@@ -74,7 +95,7 @@ HIMUON_API himuon_status himuon_policy_loss(const himuon_policy *p, void *worksp
 }
 
 HIMUON_API himuon_status himuon_grad_norm_workspace(int32_t n_tensors, size_t *bytes) try {
-  if (!bytes || n_tensors < 0) return bad("bad argument");
+  if (!bytes || n_tensors < 0 || n_tensors > kMostTensors) return bad("bad argument");
   *bytes = himuon::grad_norm_workspace(n_tensors);
   return HIMUON_OK;
 } catch (...) {
@@ -85,6 +106,7 @@ HIMUON_API himuon_status himuon_grad_norm(const himuon_grad *tensors, int32_t n_
                                           double max_norm, float *out, void *workspace, size_t ws_bytes,
                                           void *hip_stream) try {
   if (n_tensors < 0 || (n_tensors > 0 && !tensors) || !out) return bad("bad argument");
+  if (n_tensors > kMostTensors) return bad("more than 2^24 tensors");
   if (!is_dtype(dtype)) return bad("dtype");
   if (!std::isfinite(max_norm) || max_norm < 0) return bad("max_norm must be finite and >= 0");
   int64_t total = 0;
@@ -102,26 +124,39 @@ HIMUON_API himuon_status himuon_grad_norm(const himuon_grad *tensors, int32_t n_
   return HIMUON_ENOMEM;
 }
 
+HIMUON_API himuon_status himuon_adamw_table_size(const himuon_adamw_tensor *tensors, int32_t n_tensors,
+                                                 const himuon_adamw_config *cfg, size_t *bytes) try {
+  if (!bytes) return bad("NULL argument");
+  himuon_status s = check_adamw(tensors, n_tensors, cfg);
+  if (s != HIMUON_OK) return s;
+  *bytes = n_tensors > himuon::adamw_arg_tensors(cfg->state_bits) ? himuon::adamw_table_size(n_tensors, cfg->state_bits)
+                                                                  : 0;
+  return HIMUON_OK;
+} catch (...) {
+  return HIMUON_ENOMEM;
+}
+
+HIMUON_API himuon_status himuon_adamw_table(const himuon_adamw_tensor *tensors, int32_t n_tensors,
+                                            const himuon_adamw_config *cfg, void *host, size_t bytes) try {
+  himuon_status s = check_adamw(tensors, n_tensors, cfg);
+  if (s != HIMUON_OK) return s;
+  if (!host || bytes < himuon::adamw_table_size(n_tensors, cfg->state_bits)) return bad("table too small");
+  if (reinterpret_cast<uintptr_t>(host) % 8) return bad("table must be 8-byte aligned");
+  himuon::adamw_table(tensors, n_tensors, cfg->state_bits, host);
+  return HIMUON_OK;
+} catch (...) {
+  return HIMUON_ENOMEM;
+}
+
 HIMUON_API himuon_status himuon_adamw_step(const himuon_adamw_tensor *tensors, int32_t n_tensors,
                                            const himuon_adamw_config *cfg, int64_t t, double lr,
-                                           const float *grad_scale, const uint32_t *dither, void *hip_stream) try {
-  if (n_tensors < 0 || (n_tensors > 0 && !tensors) || !cfg) return bad("bad argument");
-  if (!is_dtype(cfg->weight_dtype) || !is_dtype(cfg->grad_dtype)) return bad("dtype");
-  if (cfg->state_bits != 32 && cfg->state_bits != 8) return bad("state_bits must be 32 or 8");
-  if (!(cfg->beta1 >= 0 && cfg->beta1 < 1 && cfg->beta2 >= 0 && cfg->beta2 < 1)) return bad("betas must be in [0, 1)");
-  if (!(cfg->eps >= 1e-30 && std::isfinite((float)cfg->eps))) return bad("eps must be finite and >= 1e-30");
+                                           const float *grad_scale, const uint32_t *dither, const void *table,
+                                           void *hip_stream) try {
+  himuon_status s = check_adamw(tensors, n_tensors, cfg);
+  if (s != HIMUON_OK) return s;
   if (t < 1) return bad("t must be >= 1");
   if (!std::isfinite((float)lr)) return bad("lr must be finite");
-  int64_t total = 0;
-  for (int32_t i = 0; i < n_tensors; ++i) {
-    const himuon_adamw_tensor &x = tensors[i];
-    if (x.n < 0 || x.n > kMostElements - total) return bad("n must be >= 0, 2^40 in all at most");
-    total += x.n;
-    if (!std::isfinite((float)x.weight_decay)) return bad("weight_decay must be finite");
-    if (x.n == 0) continue;
-    if (!x.weight || !x.grad || !x.m || !x.v) return bad("NULL pointer");
-    if (cfg->state_bits == 8 && (!x.m_scale || !x.v_scale)) return bad("8-bit states need their scales");
-  }
+  if (reinterpret_cast<uintptr_t>(table) % 16) return bad("table must be 16-byte aligned");
   himuon::AdamWParams p{};
   p.beta1 = (float)cfg->beta1;
   p.omb1 = (float)(1.0 - cfg->beta1);
@@ -131,11 +166,12 @@ HIMUON_API himuon_status himuon_adamw_step(const himuon_adamw_tensor *tensors, i
   p.root_scale = (float)(1.0 / std::sqrt(bias2));
   p.eps = (float)cfg->eps;
   p.step = (float)(lr / bias1);
+  p.lr = (float)lr;
   p.dither[0] = dither ? dither[0] : 0;
   p.dither[1] = dither ? dither[1] : 0;
   p.grad_scale = grad_scale;
   return launched(himuon::launch_adamw(tensors, n_tensors, cfg->weight_dtype == HIMUON_BF16,
-                                       cfg->grad_dtype == HIMUON_BF16, cfg->state_bits, lr, p,
+                                       cfg->grad_dtype == HIMUON_BF16, cfg->state_bits, p, table,
                                        reinterpret_cast<hipStream_t>(hip_stream)),
                   "AdamW step launch");
 } catch (...) {

@@ -9,6 +9,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 from . import BF16, F32, himuon_policy, himuon_policy_loss, himuon_policy_workspace
+from .adamw import _on, _stream
 
 
 class PolicyLoss(NamedTuple):
@@ -30,7 +31,7 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
     [0, V) is left out.  old_logp None: the ratio is 1; ref_logp None: no KL term.  clip: the pair (low, high).
     dlogits: True allocates the gradient, False or None computes the forward pass alone, a tensor of logits' shape
     and dtype receives it (`logits` itself: in place).  Everything runs on `stream` (the current stream by default);
-    the outputs and the workspace that the call allocates belong to that stream."""
+    stats, logp and the workspace share one allocation of the call."""
     import torch
     if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or not logits.is_cuda:
         raise ValueError("logits must be a 2-D float32 or bfloat16 CUDA tensor")
@@ -38,42 +39,47 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
     if V < 1:
         raise ValueError("logits must have at least one column")
     dev = logits.device
-
-    def ld_of(t, name):
-        if (V > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < V):
-            raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
-        return t.stride(0) if N > 1 else V
-
-    def row(t, dtype, name):
+    ld = _leading(logits, "logits", N, V)
+    rows = [0, 0, 0, 0, 0]
+    for k, (t, dtype, name) in enumerate(((label, torch.int64, "label"), (weight, torch.float32, "weight"),
+                                          (advantage, torch.float32, "advantage"), (old_logp, torch.float32, "old_logp"),
+                                          (ref_logp, torch.float32, "ref_logp"))):
         if t is None:
-            return 0
-        if t.shape != (N,) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+            if k < 3:
+                raise ValueError(f"{name} is needed")
+            continue
+        if t.dtype is not dtype or t.device != dev or t.dim() != 1 or t.numel() != N or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of {N} elements on {dev}")
-        return t.data_ptr()
+        rows[k] = t.data_ptr()
+    if dlogits is True:
+        dlogits = torch.empty(N, V, dtype=logits.dtype, device=dev)
+    elif dlogits is False:
+        dlogits = None
+    elif dlogits is not None and (dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype or
+                                  dlogits.device != dev):
+        raise ValueError("dlogits must have the shape, dtype and device of logits")
+    p = himuon_policy(N, V, ld, _leading(dlogits, "dlogits", N, V) if dlogits is not None else 0, logits.data_ptr(),
+                      dlogits.data_ptr() if dlogits is not None else None, *rows, None, None,
+                      F32 if logits.dtype is torch.float32 else BF16, clip[0], clip[1], kl_coef, temperature, grad_scale)
+    need = himuon_policy_workspace(p)
+    buf = torch.empty(4 + need // 4 + N, dtype=torch.float32, device=dev)   # stats, workspace (whole words), logp
+    base = buf.data_ptr()
+    p.stats, p.logp = base, base + 16 + need
+    if stream is not None:
+        for t in (buf, dlogits):
+            if t is not None:
+                t.record_stream(stream)
+    with _on(torch, dev):
+        himuon_policy_loss(p, base + 16, need, _stream(torch, stream, dev))
+    return PolicyLoss(buf[:4], buf[4 + need // 4:], dlogits)
 
-    ld = ld_of(logits, "logits")
-    for t, name in ((label, "label"), (weight, "weight"), (advantage, "advantage")):
-        if t is None:
-            raise ValueError(f"{name} is needed")
-    ptrs = (row(label, torch.int64, "label"), row(weight, torch.float32, "weight"),
-            row(advantage, torch.float32, "advantage"), row(old_logp, torch.float32, "old_logp"),
-            row(ref_logp, torch.float32, "ref_logp"))
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev), torch.cuda.stream(s):
-        if dlogits is True:
-            dlogits = torch.empty(N, V, dtype=logits.dtype, device=dev)
-        elif dlogits is False:
-            dlogits = None
-        if dlogits is not None and (dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or
-                                    dlogits.device != dev):
-            raise ValueError("dlogits must have the shape, dtype and device of logits")
-        logp = torch.empty(N, dtype=torch.float32, device=dev)
-        stats = torch.empty(4, dtype=torch.float32, device=dev)
-        p = himuon_policy(N, V, ld, ld_of(dlogits, "dlogits") if dlogits is not None else 0, logits.data_ptr(),
-                          dlogits.data_ptr() if dlogits is not None else None, *ptrs, logp.data_ptr(),
-                          stats.data_ptr(), F32 if logits.dtype == torch.float32 else BF16, clip[0], clip[1], kl_coef,
-                          temperature, grad_scale)
-        n = himuon_policy_workspace(p)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        himuon_policy_loss(p, ws.data_ptr(), n, s.cuda_stream)
-    return PolicyLoss(stats, logp, dlogits)
+
+def _leading(t, name, N, V):
+    if N <= 1:
+        if V > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit column stride")
+        return V
+    rows, cols = t.stride()
+    if (V > 1 and cols != 1) or rows < V:
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return rows
