@@ -25,23 +25,15 @@ def _column(tensors, name, dtypes, device):
     return [t.numel() for t in tensors], [t.data_ptr() for t in tensors]
 
 
-def _stream(torch, stream, device):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-
-
-class _on:
-    """Makes `device` the current one where it is not (the library launches on the current device)."""
-
-    def __init__(self, torch, device):
-        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _launch(torch, device, stream, call, *args):
+    """call(*args, stream) with `device` the current one, as the library needs it.  The current stream is asked for
+    by its raw handle: a call of a few microseconds should not spend two on a Stream object."""
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() == device.index:
+        call(*args, s)
+    else:
+        with torch.cuda.device(device):
+            call(*args, s)
 
 
 def adamw_state(W, bits: int = 32):
@@ -157,10 +149,8 @@ class AdamW:
             if scale.dtype != torch.float32 or scale.device != self.device or scale.numel() < 1:
                 raise ValueError(f"scale must be a float32 tensor on {self.device}")
             at = scale.data_ptr()
-        with _on(torch, self.device):
-            himuon_adamw_step(self._c, self.cfg, t, lr, at, dither,
-                              self._table.data_ptr() if self._table is not None else 0,
-                              _stream(torch, stream, self.device))
+        _launch(torch, self.device, stream, himuon_adamw_step, self._c, self.cfg, t, lr, at, dither,
+                self._table.data_ptr() if self._table is not None else 0)
 
 
 class GradNorm:
@@ -206,7 +196,6 @@ class GradNorm:
                 out.record_stream(stream)
         elif out.dtype != torch.float32 or out.shape != (2,) or out.device != self.device or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous float32 tensor of two elements on {self.device}")
-        with _on(torch, self.device):
-            himuon_grad_norm(self._c, self._dt, max_norm, out.data_ptr(), self._ws.data_ptr(), self._ws.numel(),
-                             _stream(torch, stream, self.device))
+        _launch(torch, self.device, stream, himuon_grad_norm, self._c, self._dt, max_norm, out.data_ptr(),
+                self._ws.data_ptr(), self._ws.numel())
         return out

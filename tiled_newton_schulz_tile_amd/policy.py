@@ -9,7 +9,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 from . import BF16, F32, himuon_policy, himuon_policy_loss, himuon_policy_workspace
-from .adamw import _on, _stream
+from .adamw import _launch
 
 
 class PolicyLoss(NamedTuple):
@@ -40,17 +40,11 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
         raise ValueError("logits must have at least one column")
     dev = logits.device
     ld = _leading(logits, "logits", N, V)
-    rows = [0, 0, 0, 0, 0]
-    for k, (t, dtype, name) in enumerate(((label, torch.int64, "label"), (weight, torch.float32, "weight"),
-                                          (advantage, torch.float32, "advantage"), (old_logp, torch.float32, "old_logp"),
-                                          (ref_logp, torch.float32, "ref_logp"))):
-        if t is None:
-            if k < 3:
-                raise ValueError(f"{name} is needed")
-            continue
-        if t.dtype is not dtype or t.device != dev or t.dim() != 1 or t.numel() != N or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {N} elements on {dev}")
-        rows[k] = t.data_ptr()
+    f32 = torch.float32
+    rows = (_row(label, torch.int64, N, dev, "label"), _row(weight, f32, N, dev, "weight"),
+            _row(advantage, f32, N, dev, "advantage"),
+            0 if old_logp is None else _row(old_logp, f32, N, dev, "old_logp"),
+            0 if ref_logp is None else _row(ref_logp, f32, N, dev, "ref_logp"))
     if dlogits is True:
         dlogits = torch.empty(N, V, dtype=logits.dtype, device=dev)
     elif dlogits is False:
@@ -69,9 +63,14 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
         for t in (buf, dlogits):
             if t is not None:
                 t.record_stream(stream)
-    with _on(torch, dev):
-        himuon_policy_loss(p, base + 16, need, _stream(torch, stream, dev))
+    _launch(torch, dev, stream, himuon_policy_loss, p, base + 16, need)
     return PolicyLoss(buf[:4], buf[4 + need // 4:], dlogits)
+
+
+def _row(t, dtype, N, dev, name):
+    if t is None or t.dtype is not dtype or t.device != dev or t.dim() != 1 or t.numel() != N or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {N} elements on {dev}")
+    return t.data_ptr()
 
 
 def _leading(t, name, N, V):
