@@ -317,7 +317,7 @@ typedef struct {
   double grad_scale;             /* finite; multiplies dlogits only                     */
 } himuon_policy;
 
-/* Workspace bytes himuon_policy_loss needs for this call (device memory, 8-byte aligned,
+/* Workspace bytes himuon_policy_loss needs for this call (device memory, 16-byte aligned,
    contents immaterial). */
 HIMUON_API himuon_status himuon_policy_workspace(const himuon_policy *p, size_t *bytes);
 
@@ -334,7 +334,7 @@ typedef struct {
   const void *grad;
 } himuon_grad;
 
-/* Workspace bytes of himuon_grad_norm over n_tensors tensors (8-byte aligned).  Its first
+/* Workspace bytes of himuon_grad_norm over n_tensors tensors (16-byte aligned).  Its first
    eight bytes must be zero before its first call; every call leaves them zero.  Calls that
    share a workspace go on one stream (or the caller orders them). */
 HIMUON_API himuon_status himuon_grad_norm_workspace(int32_t n_tensors, size_t *bytes);

@@ -282,3 +282,50 @@ def test_policy_wrapper_refusals():
                 dict(temperature=0.0), dict(temperature=float("inf")), dict(grad_scale=float("nan"))]:
         with pytest.raises(hm.HiMuonError):
             policy_loss(z, label, weight, adv, old, **bad)
+
+
+@pytest.mark.parametrize("V", [255, 1024, 2049, 4097, 8192, 16385, 32768, 32777, 50257, 65537, 131071, 131080, 150001])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_policy_more_rows_than_are_split(V, dtype):
+    """More rows than the path that cuts rows into spans takes: every size of row that a block holds in registers,
+    and rows past it; forward alone, with the gradient, and in place."""
+    _need_gpu()
+    logits, rest = make(133, V, dtype, V, pad=1, masked=0.9)
+    label, weight, adv, old, ref = rest
+    weight[132] = 0.5
+    kw = dict(clip=(0.2, 0.28), kl_coef=0.05, temperature=1.2)
+    got = policy_loss(logits, label, weight, adv, old, ref, **kw)
+    check(logits, rest, got, dtype, **kw)
+    fwd = policy_loss(logits, label, weight, adv, old, ref, dlogits=False, **kw)
+    check(logits, rest, fwd, dtype, **kw)
+    z = logits.clone()
+    policy_loss(z, label, weight, adv, old, ref, dlogits=z, **kw)
+    assert torch.equal(z, got.dlogits)
+
+
+@pytest.mark.parametrize("V", [3000, 40000, 140001])
+def test_policy_extreme_rows_among_many(V):
+    """Rows of -inf, of the lowest value, with NaN or +inf, on the paths for many rows."""
+    _need_gpu()
+    logits, rest = make(140, V, torch.float32, 5, masked=0.9)
+    label, weight, adv, old, ref = rest
+    weight[:8] = 1.0
+    old[:8], ref[:8] = -3.0, -3.5
+    label[:8] = 1
+    logits[0, V // 3:] = float("-inf")
+    logits[1, V // 3:] = torch.finfo(torch.float32).min
+    logits[2] = torch.finfo(torch.float32).min          # every token masked alike: a uniform row
+    logits[3] = float("-inf")
+    logits[3, 1] = -5.0
+    got = policy_loss(logits, label, weight, adv, old, ref)
+    assert abs(float(got.logp[2]) + np.log(V)) <= 2.0 ** -21 * np.log(V) + 2.0 ** -24 * (V / 512 + 24)
+    assert float(got.logp[3]) == 0
+    logits[2].zero_()
+    again = policy_loss(logits, label, weight, adv, old, ref)
+    assert torch.equal(got.logp, again.logp) and torch.equal(got.dlogits, again.dlogits)
+    check(logits, rest, got, torch.float32)
+    logits[4, 7], logits[5, V - 1] = float("nan"), float("inf")
+    logits[6] = float("-inf")
+    got = policy_loss(logits, label, weight, adv, old, ref)
+    assert torch.isnan(got.logp[4:7]).all() and torch.isfinite(got.logp[:4]).all()
+    assert torch.isnan(got.dlogits[4:7]).any(1).all() and torch.isfinite(got.dlogits[:4]).all()

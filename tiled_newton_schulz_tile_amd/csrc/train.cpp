@@ -26,7 +26,7 @@ constexpr int32_t kMostTensors = 1 << 24;
 himuon_status check_workspace(const void *ws, size_t have, size_t need) {
   if (need == 0) return HIMUON_OK;
   if (!ws || have < need) return bad("workspace smaller than the workspace query says");
-  if (reinterpret_cast<uintptr_t>(ws) % 8) return bad("workspace must be 8-byte aligned");
+  if (reinterpret_cast<uintptr_t>(ws) % 16) return bad("workspace must be 16-byte aligned");
   return HIMUON_OK;
 }
 
