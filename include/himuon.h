@@ -378,7 +378,11 @@ typedef struct {
      w <- w (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
    with w rounded to nearest even where weight_dtype is bf16.  Where *grad_scale is NaN
    (himuon_grad_norm's factor for a gradient that is not finite) the step changes nothing.
-   8-bit states: the step computes with the fp32 moments and then stores m and r = sqrt(v)
+   8-bit states: moments and codes are computed in fp32 with every operation rounded on its
+   own, in the order of these formulas ((1 - beta2) g first, then times g; r^2 before its
+   product with beta2; 448 / peak as the rounded reciprocal times 448), so that any other
+   computation in that order gives the same states bit for bit.  The weight takes the fp32
+   moments; then the step stores m and r = sqrt(v)
    by blocks of 256 elements: peak = the block's largest magnitude, scale = peak / 448, and
    y = |x| 448 / peak rounded to one of its two e4m3 neighbours, up with the probability of
    its distance to the lower one: the upper 16 bits of (i C + dither[k]) mod 2^32, plus one

@@ -414,3 +414,38 @@ def test_adamw_table_equals_arguments(bits):
         for k in range(len(x)):
             if k != 1:
                 assert torch.equal(x[k].view(torch.uint8), y[k].view(torch.uint8))
+
+
+@pytest.mark.parametrize("gt", [F32, BF16])
+def test_adamw8_states_are_those_of_the_formulas_in_fp32(gt):
+    """The 8-bit states bit for bit: numpy float32 operations (each correctly rounded) in the documented order."""
+    _need_gpu()
+    f = np.float32
+    sizes = [1, 255, 256, 5001, 70000]
+    ts = tensors8(sizes, F32, gt, 77)
+    opt = AdamW(ts, betas=(0.9, 0.999))
+    scale = torch.tensor([0.37], device=DEV)
+    table = T.e4m3_values().astype(f)
+    for t, dither in ((1, (11, 0xFEDCBA98)), (2, (0x9ABCDEF0, 5))):
+        before = [[x.clone() for x in q] for q in ts]
+        opt.step(1e-3, t, scale=scale, dither=dither)
+        for b, a in zip(before, ts):
+            n = b[0].numel()
+            g = b[1].float().cpu().numpy() * f(0.37)
+            m_unit, r_unit = (np.repeat(x.cpu().numpy(), T.BLOCK)[:n] for x in b[4:])
+            m = table[b[2].view(torch.uint8).cpu().numpy()] * m_unit
+            r = table[b[3].view(torch.uint8).cpu().numpy()] * r_unit
+            m = f(0.9) * m + f(1 - 0.9) * g
+            r = np.sqrt(f(0.999) * (r * r) + f(1 - 0.999) * g * g)
+            for k, x in enumerate((m, r)):
+                i = np.arange(n, dtype=np.uint64)
+                d = ((i * T.MULT[k] + dither[k]) % 2 ** 32 >> np.uint64(16)).astype(np.uint32) << np.uint32(4) | np.uint32(8)
+                pad = np.zeros(-n % T.BLOCK, f)
+                peak = np.abs(np.concatenate([x, pad])).reshape(-1, T.BLOCK).max(1)
+                inv = np.repeat(f(1) / peak * f(448), T.BLOCK)[:n]
+                y = np.abs(x) * inv
+                low = np.where(y < f(2 ** -6), f(2 ** -6), f(0))
+                y = (((y + low).view(np.uint32) + d) & np.uint32(0xFFF00000)).view(f) - low
+                y = np.clip(y, f(2 ** -9) if k else f(0), f(448)) * np.sign(x)
+                assert np.array_equal(table[a[2 + k].view(torch.uint8).cpu().numpy()], y)
+                assert np.array_equal(a[4 + k].cpu().numpy(), peak * f(1 / 448))
