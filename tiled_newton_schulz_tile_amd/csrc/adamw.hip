@@ -4,7 +4,7 @@
 // The tensors' descriptors travel in the kernel arguments while they fit (so a call needs
 // no table in device memory, no upload and no wait, and pointers may change from step to
 // step), or in a table in device memory that the caller uploads once.  Every tensor is cut
-// into chunks of 1024 or 4096 elements; a block finds the tensor of its chunk with one load
+// into chunks of 1024 elements; a block finds the tensor of its chunk with one load
 // per lane of the first-chunk table and a ballot.
 //
 // Tensors may start at any element (views of a flattened bucket do): vectors are declared
@@ -34,33 +34,50 @@ __device__ __forceinline__ void store1(float *p, int64_t i, float x) { gmem(p)[i
 __device__ __forceinline__ void store1(__bf16 *p, int64_t i, float x) {
   gmem(reinterpret_cast<unsigned short *>(p))[i] = to_bf16_bits(x);
 }
-__device__ __forceinline__ f32x4 load4(const float *p, int64_t i) {
-  return *reinterpret_cast<const GLOBAL_AS f32x4u *>(gmem(p + i));
+// NT: past the caches (non-temporal)
+template <bool NT, class V>
+__device__ __forceinline__ V load_as(const GLOBAL_AS V *p) {
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  return *p;
 }
+template <bool NT, class V>
+__device__ __forceinline__ void store_as(GLOBAL_AS V *p, V x) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(x, p);
+  else
+    *p = x;
+}
+template <bool NT>
+__device__ __forceinline__ f32x4 load4(const float *p, int64_t i) {
+  return load_as<NT>(reinterpret_cast<const GLOBAL_AS f32x4u *>(gmem(p + i)));
+}
+template <bool NT>
 __device__ __forceinline__ f32x4 load4(const __bf16 *p, int64_t i) {
-  const u16x4u h = *reinterpret_cast<const GLOBAL_AS u16x4u *>(gmem(p + i));
+  const u16x4u h = load_as<NT>(reinterpret_cast<const GLOBAL_AS u16x4u *>(gmem(p + i)));
   return f32x4{bf16_bits_to_f32(h[0]), bf16_bits_to_f32(h[1]), bf16_bits_to_f32(h[2]), bf16_bits_to_f32(h[3])};
 }
+template <bool NT>
 __device__ __forceinline__ void store4(float *p, int64_t i, f32x4 x) {
-  *reinterpret_cast<GLOBAL_AS f32x4u *>(gmem(p + i)) = x;
+  store_as<NT>(reinterpret_cast<GLOBAL_AS f32x4u *>(gmem(p + i)), (f32x4u)x);
 }
+template <bool NT>
 __device__ __forceinline__ void store4(__bf16 *p, int64_t i, f32x4 x) {
-  *reinterpret_cast<GLOBAL_AS u16x4u *>(gmem(p + i)) =
-      u16x4u{to_bf16_bits(x[0]), to_bf16_bits(x[1]), to_bf16_bits(x[2]), to_bf16_bits(x[3])};
+  store_as<NT>(reinterpret_cast<GLOBAL_AS u16x4u *>(gmem(p + i)),
+               u16x4u{to_bf16_bits(x[0]), to_bf16_bits(x[1]), to_bf16_bits(x[2]), to_bf16_bits(x[3])});
 }
-// n (1..4) elements from i on; what lies beyond them reads as zero and is not written
-template <class T>
+// n (0..4) elements from i on; what lies beyond them reads as zero and is not written
+template <bool NT, class T>
 __device__ __forceinline__ f32x4 load_upto4(const T *p, int64_t i, int n) {
-  if (n >= 4) return load4(p, i);
+  if (n >= 4) return load4<NT>(p, i);
   f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < 3; ++e)
     if (e < n) x[e] = load1(p, i + e);
   return x;
 }
-template <class T>
+template <bool NT, class T>
 __device__ __forceinline__ void store_upto4(T *p, int64_t i, int n, f32x4 x) {
-  if (n >= 4) return store4(p, i, x);
+  if (n >= 4) return store4<NT>(p, i, x);
 #pragma unroll
   for (int e = 0; e < 3; ++e)
     if (e < n) store1(p, i + e, x[e]);
@@ -90,7 +107,7 @@ constexpr int kTensors = BITS == 8 ? 56 : 72;
 
 template <int BITS>
 struct ArgTable {
-  int32_t n, shift;                    // tensors; log2 of a chunk's elements
+  int32_t n;
   int32_t first[kTensors<BITS> + 1];   // first chunk of each tensor; [n]: all chunks
   Entry<BITS> t[kTensors<BITS>];
   __device__ __forceinline__ const int32_t *firsts() const { return first; }
@@ -103,7 +120,7 @@ static_assert(sizeof(ArgTable<8>) + sizeof(AdamWParams) <= 4096, "kernel argumen
 size_t entry_offset(int64_t n) { return ((size_t)(n + 1) * sizeof(int32_t) + 15) / 16 * 16; }
 template <int BITS>
 struct DeviceTable {
-  int32_t n, shift;
+  int32_t n;
   const int32_t *first;
   const Entry<BITS> *t;
   __device__ __forceinline__ const int32_t *firsts() const { return first; }
@@ -119,11 +136,11 @@ struct NormTable {
 };
 static_assert(sizeof(NormTable) + 64 <= 4096, "kernel arguments");
 
-// Chunks are small while the tensors together are (a call of a few hundred thousand
-// elements has to spread over 256 CUs, and each thread of a small chunk has one vector of
-// every operand in flight and is done), and large once the blocks would be many.
-constexpr int kSmallShift = 10, kLargeShift = 12;
-constexpr int64_t kSmallTotal = (int64_t)4 << 20;
+// A chunk is one vector of four elements a thread: every load of a block is in flight at once
+// and nothing loops.  Chunks of 4096 took 3 % (fp32 states) and 6 % (8-bit) longer on 262 M
+// elements, and leave CUs idle in a call of a few hundred thousand.
+constexpr int kChunkShift = 10;
+static_assert(1 << kChunkShift == 4 * THREADS, "four elements a thread");
 
 // The tensor that chunk c belongs to: the last one whose first chunk is <= c.  (Tensors
 // without elements are not in the table.)
@@ -145,7 +162,7 @@ __device__ __forceinline__ float new_weight(float w, float m, float root, float 
   return __builtin_fmaf(w, decay, -p.step * (m * __builtin_amdgcn_rcpf(den)));
 }
 
-template <typename W, typename G, class TABLE>
+template <typename W, typename G, bool NT, class TABLE>
 __global__ __launch_bounds__(THREADS) void adamw32_kernel(TABLE tab, AdamWParams p) {
   const float scale = p.grad_scale ? *gmem(p.grad_scale) : 1.f;
   const int c = blockIdx.x, ti = tensor_of(tab.firsts(), tab.n, c);
@@ -154,24 +171,22 @@ __global__ __launch_bounds__(THREADS) void adamw32_kernel(TABLE tab, AdamWParams
   const G *g = reinterpret_cast<const G *>(t.g);
   float *m = reinterpret_cast<float *>(t.m), *v = reinterpret_cast<float *>(t.v);
   const float decay = 1.f - p.lr * t.weight_decay;
-  const int64_t base = (int64_t)(c - tab.firsts()[ti]) << tab.shift;
-  const int64_t end = t.n - base < (1 << tab.shift) ? t.n : base + (1 << tab.shift);
-  for (int64_t i = base + 4 * threadIdx.x; i < end; i += 4 * THREADS) {
-    const int n = end - i < 4 ? (int)(end - i) : 4;
-    const f32x4 gv = load_upto4(g, i, n);
-    f32x4 mv = load_upto4(m, i, n), vv = load_upto4(v, i, n), wv = load_upto4(w, i, n);
-    if (scale != scale) return;   // the gradient was not finite: nothing changes
+  const int64_t i = ((int64_t)(c - tab.firsts()[ti]) << kChunkShift) + 4 * threadIdx.x;
+  if (i >= t.n) return;
+  const int n = t.n - i < 4 ? (int)(t.n - i) : 4;
+  const f32x4 gv = load_upto4<NT>(g, i, n);
+  f32x4 mv = load_upto4<NT>(m, i, n), vv = load_upto4<NT>(v, i, n), wv = load_upto4<NT>(w, i, n);
+  if (scale != scale) return;   // the gradient was not finite: nothing changes
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = gv[e] * scale;
-      mv[e] = __builtin_fmaf(p.beta1, mv[e], p.omb1 * x);
-      vv[e] = __builtin_fmaf(p.beta2, vv[e], p.omb2 * x * x);
-      wv[e] = new_weight(wv[e], mv[e], __builtin_amdgcn_sqrtf(vv[e]), decay, p);
-    }
-    store_upto4(m, i, n, mv);
-    store_upto4(v, i, n, vv);
-    store_upto4(w, i, n, wv);
+  for (int e = 0; e < 4; ++e) {
+    const float x = gv[e] * scale;
+    mv[e] = __builtin_fmaf(p.beta1, mv[e], p.omb1 * x);
+    vv[e] = __builtin_fmaf(p.beta2, vv[e], p.omb2 * x * x);
+    wv[e] = new_weight(wv[e], mv[e], __builtin_amdgcn_sqrtf(vv[e]), decay, p);
   }
+  store_upto4<NT>(m, i, n, mv);
+  store_upto4<NT>(v, i, n, vv);
+  store_upto4<NT>(w, i, n, wv);
 }
 
 // ---- 8-bit states
@@ -183,6 +198,7 @@ __global__ __launch_bounds__(THREADS) void adamw32_kernel(TABLE tab, AdamWParams
 // bits.  262 M elements, fp32 weights, bf16 gradients: 697 us (5.3 TB/s); with fused
 // multiply-adds and the hardware's root 674 us on the same card, in fp64 772 us.
 constexpr int kBlock = HIMUON_ADAMW_BLOCK;
+static_assert(kBlock == 4 * 64, "a wave holds one block");
 constexpr unsigned kStepM = 0x9E3779B1u, kStepR = 0x85EBCA6Bu;   // of the dither sequences
 
 __device__ __forceinline__ f32x4 unpack_e4m3x4(unsigned x) {
@@ -264,7 +280,7 @@ __device__ __forceinline__ void store_codes(unsigned char *p, int64_t i, int n, 
 }
 __device__ __forceinline__ float scale_of(float peak) { return peak < 0x1p-100f ? 0.f : peak * (1.f / 448.f); }
 
-template <typename W, typename G, class TABLE>
+template <typename W, typename G, bool NT, class TABLE>
 __global__ __launch_bounds__(THREADS) void adamw8_kernel(TABLE tab, AdamWParams p) {
   const float scale = p.grad_scale ? *gmem(p.grad_scale) : 1.f;
   const int c = blockIdx.x, ti = tensor_of(tab.firsts(), tab.n, c);
@@ -273,66 +289,71 @@ __global__ __launch_bounds__(THREADS) void adamw8_kernel(TABLE tab, AdamWParams 
   const G *g = reinterpret_cast<const G *>(t.g);
   unsigned char *m = reinterpret_cast<unsigned char *>(t.m), *r = reinterpret_cast<unsigned char *>(t.v);
   const float decay = 1.f - p.lr * t.weight_decay;
-  const int64_t base = (int64_t)(c - tab.firsts()[ti]) << tab.shift;
-  const int64_t end = t.n - base < (1 << tab.shift) ? t.n : base + (1 << tab.shift);
+  // a wave takes one whole block: lanes beyond the tensor's end stay, for the reductions
   const int lane = threadIdx.x & 63;
-  // a wave takes whole blocks: every lane stays in the loop until its wave's block is done
-  for (int64_t b = base + (int64_t)(threadIdx.x >> 6) * kBlock; b < end; b += THREADS / 64 * kBlock) {
-    const int64_t i = b + 4 * lane;
-    const int n = end - i >= 4 ? 4 : (end > i ? (int)(end - i) : 0);
-    float *ms = t.ms + b / kBlock, *vs = t.vs + b / kBlock;
-    const float m_unit = *gmem(ms), r_unit = *gmem(vs);
-    const f32x4 gv = load_upto4(g, i, n);
-    const unsigned m_word = load_codes(m, i, n), r_word = load_codes(r, i, n);
-    f32x4 wv = load_upto4(w, i, n);
-    if (scale != scale) return;   // the gradient was not finite: nothing changes
-    f32x4 mv = unpack_e4m3x4(m_word), rv = unpack_e4m3x4(r_word);   // zeros beyond the tensor's end, throughout
-    {
+  const int64_t b = ((int64_t)(c - tab.firsts()[ti]) << kChunkShift) + (threadIdx.x >> 6) * kBlock;
+  if (b >= t.n) return;
+  const int64_t i = b + 4 * lane;
+  const int n = t.n - i >= 4 ? 4 : (t.n > i ? (int)(t.n - i) : 0);
+  float *ms = t.ms + b / kBlock, *vs = t.vs + b / kBlock;
+  const float m_unit = *gmem(ms), r_unit = *gmem(vs);
+  const f32x4 gv = load_upto4<NT>(g, i, n);
+  const unsigned m_word = load_codes(m, i, n), r_word = load_codes(r, i, n);
+  f32x4 wv = load_upto4<NT>(w, i, n);
+  if (scale != scale) return;   // the gradient was not finite: nothing changes
+  f32x4 mv = unpack_e4m3x4(m_word), rv = unpack_e4m3x4(r_word);   // zeros beyond the tensor's end, throughout
+  {
 #pragma clang fp contract(off)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = gv[e] * scale, r0 = rv[e] * r_unit;
-        mv[e] = p.beta1 * (mv[e] * m_unit) + p.omb1 * x;
-        rv[e] = __builtin_sqrtf(p.beta2 * (r0 * r0) + p.omb2 * x * x);
-      }
+    for (int e = 0; e < 4; ++e) {
+      const float x = gv[e] * scale, r0 = rv[e] * r_unit;
+      mv[e] = p.beta1 * (mv[e] * m_unit) + p.omb1 * x;
+      rv[e] = __builtin_sqrtf(p.beta2 * (r0 * r0) + p.omb2 * x * x);
     }
+  }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) wv[e] = new_weight(wv[e], mv[e], rv[e], decay, p);
-    store_upto4(w, i, n, wv);
-    const float m_peak = wave_peak(mv), r_peak = wave_peak(rv);
-    store_codes(m, i, n, codes_of<false>(mv, m_peak, (unsigned)i * kStepM + p.dither[0], kStepM));
-    store_codes(r, i, n, codes_of<true>(rv, r_peak, (unsigned)i * kStepR + p.dither[1], kStepR));
-    if (lane == 0) {
-      *gmem(ms) = scale_of(m_peak);
-      *gmem(vs) = scale_of(r_peak);
-    }
+  for (int e = 0; e < 4; ++e) wv[e] = new_weight(wv[e], mv[e], rv[e], decay, p);
+  store_upto4<NT>(w, i, n, wv);
+  const float m_peak = wave_peak(mv), r_peak = wave_peak(rv);
+  store_codes(m, i, n, codes_of<false>(mv, m_peak, (unsigned)i * kStepM + p.dither[0], kStepM));
+  store_codes(r, i, n, codes_of<true>(rv, r_peak, (unsigned)i * kStepR + p.dither[1], kStepR));
+  if (lane == 0) {
+    *gmem(ms) = scale_of(m_peak);
+    *gmem(vs) = scale_of(r_peak);
   }
 }
 
+// A call that moves more than this goes past the caches: nothing of it is left there when the
+// next step comes, and its lines do not have to push others out.  Bytes of a call, cached
+// against non-temporal: 114 MB (8-bit states) 33.1 / 40.8 us, 250 MB (bf16, fp32 states)
+// 55.1 / 50.3 us, 3.7 GB 677 / 664 us, 6.8 GB 1231 / 1134 us.
+constexpr double kCachedBytes = 128e6;
+
 template <int BITS, typename W, typename G, class TABLE>
-void launch_typed(const TABLE &tab, unsigned chunks, const AdamWParams &p, hipStream_t stream) {
-  if constexpr (BITS == 32)
-    hipLaunchKernelGGL((adamw32_kernel<W, G, TABLE>), dim3(chunks), dim3(THREADS), 0, stream, tab, p);
-  else
-    hipLaunchKernelGGL((adamw8_kernel<W, G, TABLE>), dim3(chunks), dim3(THREADS), 0, stream, tab, p);
+void launch_typed(const TABLE &tab, unsigned chunks, bool nt, const AdamWParams &p, hipStream_t stream) {
+  const dim3 grid(chunks), block(THREADS);
+  if constexpr (BITS == 32) {
+    if (nt) hipLaunchKernelGGL((adamw32_kernel<W, G, true, TABLE>), grid, block, 0, stream, tab, p);
+    else hipLaunchKernelGGL((adamw32_kernel<W, G, false, TABLE>), grid, block, 0, stream, tab, p);
+  } else {
+    if (nt) hipLaunchKernelGGL((adamw8_kernel<W, G, true, TABLE>), grid, block, 0, stream, tab, p);
+    else hipLaunchKernelGGL((adamw8_kernel<W, G, false, TABLE>), grid, block, 0, stream, tab, p);
+  }
 }
+// How a call is launched: its types, and whether it goes past the caches.
+struct Kind {
+  bool weight_bf16, grad_bf16, nt;
+};
 template <int BITS, class TABLE>
-hipError_t launch_table(const TABLE &tab, int64_t chunks, bool weight_bf16, bool grad_bf16, const AdamWParams &p,
-                        hipStream_t stream) {
+hipError_t launch_table(const TABLE &tab, int64_t chunks, Kind k, const AdamWParams &p, hipStream_t stream) {
   const unsigned c = (unsigned)chunks;
-  if (weight_bf16)
-    grad_bf16 ? launch_typed<BITS, __bf16, __bf16>(tab, c, p, stream) : launch_typed<BITS, __bf16, float>(tab, c, p, stream);
-  else
-    grad_bf16 ? launch_typed<BITS, float, __bf16>(tab, c, p, stream) : launch_typed<BITS, float, float>(tab, c, p, stream);
+  if (k.weight_bf16 && k.grad_bf16) launch_typed<BITS, __bf16, __bf16>(tab, c, k.nt, p, stream);
+  else if (k.weight_bf16) launch_typed<BITS, __bf16, float>(tab, c, k.nt, p, stream);
+  else if (k.grad_bf16) launch_typed<BITS, float, __bf16>(tab, c, k.nt, p, stream);
+  else launch_typed<BITS, float, float>(tab, c, k.nt, p, stream);
   return hipGetLastError();
 }
 
-template <class TENSOR>
-int shift_of(const TENSOR *tensors, int32_t n_tensors) {
-  int64_t total = 0;
-  for (int32_t k = 0; k < n_tensors; ++k) total += tensors[k].n;
-  return total <= kSmallTotal ? kSmallShift : kLargeShift;
-}
 int64_t chunks_of(int64_t n, int shift) { return (n + ((int64_t)1 << shift) - 1) >> shift; }
 
 template <int BITS>
@@ -351,16 +372,15 @@ void fill_entry(Entry<BITS> &t, const himuon_adamw_tensor &x) {
 
 template <int BITS>
 void fill_table(const himuon_adamw_tensor *tensors, int32_t n_tensors, char *host) {
-  const int shift = shift_of(tensors, n_tensors);
   int32_t *first = reinterpret_cast<int32_t *>(host);
   Entry<BITS> *t = reinterpret_cast<Entry<BITS> *>(host + entry_offset(n_tensors));
-  int64_t at = 0;   // < 2^29: 2^40 elements in all and 2^24 tensors at most
+  int64_t at = 0;   // < 2^31: 2^40 elements in all and 2^24 tensors at most
   int32_t n = 0;
   for (int32_t k = 0; k < n_tensors; ++k) {
     if (tensors[k].n == 0) continue;
     first[n] = (int32_t)at;
     fill_entry<BITS>(t[n], tensors[k]);
-    at += chunks_of(tensors[k].n, shift);
+    at += chunks_of(tensors[k].n, kChunkShift);
     ++n;
   }
   first[n] = (int32_t)at;
@@ -369,26 +389,28 @@ void fill_table(const himuon_adamw_tensor *tensors, int32_t n_tensors, char *hos
 template <int BITS>
 hipError_t launch_adamw_bits(const himuon_adamw_tensor *tensors, int32_t n_tensors, bool weight_bf16, bool grad_bf16,
                              const AdamWParams &p, const void *table, hipStream_t stream) {
-  const int shift = shift_of(tensors, n_tensors);
+  int64_t total = 0;
+  for (int32_t k = 0; k < n_tensors; ++k) total += tensors[k].n;
+  const double each = (weight_bf16 ? 4 : 8) + (grad_bf16 ? 2 : 4) + (BITS == 8 ? 4 : 16);
+  const Kind kind = {weight_bf16, grad_bf16, (double)total * each > kCachedBytes};
   if (table) {
-    DeviceTable<BITS> tab{0, shift, reinterpret_cast<const int32_t *>(table),
+    DeviceTable<BITS> tab{0, reinterpret_cast<const int32_t *>(table),
                           reinterpret_cast<const Entry<BITS> *>(reinterpret_cast<const char *>(table) +
                                                                 entry_offset(n_tensors))};
     int64_t chunks = 0;
     for (int32_t k = 0; k < n_tensors; ++k) {
       tab.n += tensors[k].n > 0;
-      chunks += chunks_of(tensors[k].n, shift);
+      chunks += chunks_of(tensors[k].n, kChunkShift);
     }
     if (chunks == 0) return hipSuccess;
-    return launch_table<BITS>(tab, chunks, weight_bf16, grad_bf16, p, stream);
+    return launch_table<BITS>(tab, chunks, kind, p, stream);
   }
   ArgTable<BITS> tab;
   tab.n = 0;
-  tab.shift = shift;
   tab.first[0] = 0;
   auto flush = [&]() -> hipError_t {
     if (tab.n == 0) return hipSuccess;
-    hipError_t e = launch_table<BITS>(tab, tab.first[tab.n], weight_bf16, grad_bf16, p, stream);
+    hipError_t e = launch_table<BITS>(tab, tab.first[tab.n], kind, p, stream);
     tab.n = 0;
     return e;
   };
@@ -399,14 +421,18 @@ hipError_t launch_adamw_bits(const himuon_adamw_tensor *tensors, int32_t n_tenso
       if (e != hipSuccess) return e;
     }
     fill_entry<BITS>(tab.t[tab.n], tensors[k]);
-    tab.first[tab.n + 1] = (int32_t)(tab.first[tab.n] + chunks_of(tensors[k].n, shift));
+    tab.first[tab.n + 1] = (int32_t)(tab.first[tab.n] + chunks_of(tensors[k].n, kChunkShift));
     ++tab.n;
   }
   return flush();
 }
 
 // ------------------------------------------------------------------ gradient norm
-constexpr int kNormBlocks = 2048;   // blocks of a launch at most; each leaves one partial sum
+// 512 blocks of 512 threads at most, two a CU, each with four vectors a thread in flight.
+// Every block ends with a release at device scope, which writes its L2 back and is paid one
+// after the other: 1.07 G bf16 elements took 430 us in 2048 blocks of 256 threads and 715 us
+// in 8192; 1024 blocks 377 us, these 356 us (6.0 TB/s).
+constexpr int kNormThreads = 512, kNormBlocks = 512;   // each block leaves one partial sum
 
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
@@ -422,14 +448,14 @@ __device__ __forceinline__ double block_sum(double x, double *lds) {
   return s;
 }
 
-// 16 bytes of a gradient: squares into the sum
-__device__ __forceinline__ void add_squares(const float *p, double &sum) {
-  const f32x4 x = load4(p, 0);
+// 16 bytes of a gradient, and its squares into a sum
+__device__ __forceinline__ f32x4 load_vec(const float *p) { return load4<false>(p, 0); }
+__device__ __forceinline__ u16x8u load_vec(const __bf16 *p) { return *reinterpret_cast<const GLOBAL_AS u16x8u *>(gmem(p)); }
+__device__ __forceinline__ void add_squares(f32x4 x, double &sum) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) sum = __builtin_fma((double)x[e], (double)x[e], sum);
 }
-__device__ __forceinline__ void add_squares(const __bf16 *p, double &sum) {
-  const u16x8u h = *reinterpret_cast<const GLOBAL_AS u16x8u *>(gmem(p));
+__device__ __forceinline__ void add_squares(u16x8u h, double &sum) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const double x = (double)bf16_bits_to_f32(h[e]);
@@ -440,27 +466,34 @@ __device__ __forceinline__ void add_squares(const __bf16 *p, double &sum) {
 // Each block leaves one partial sum; the last block to finish (the ticket says which) joins
 // all of them, those of the call's earlier launches among them, in a fixed order.
 template <typename G>
-__global__ __launch_bounds__(THREADS) void grad_norm_kernel(NormTable tab, double *part, int64_t before, bool last,
+__global__ __launch_bounds__(kNormThreads) void grad_norm_kernel(NormTable tab, double *part, int64_t before, bool last,
                                                             unsigned *ticket, double max_norm, float *out) {
-  __shared__ double lds[THREADS / 64];
+  __shared__ double lds[kNormThreads / 64];
   __shared__ bool joins;
-  constexpr int N = 16 / sizeof(G);
-  double sum = 0;
+  constexpr int N = 16 / sizeof(G), STEP = N * kNormThreads;
+  double sum = 0, more[3] = {0, 0, 0};
   const int chunks = tab.first[tab.n];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int ti = tensor_of(tab.first, tab.n, c);
     const G *g = reinterpret_cast<const G *>(tab.g[ti]);
     const int64_t base = (int64_t)(c - tab.first[ti]) << tab.shift, size = tab.size[ti];
     const int64_t end = size - base < (1 << tab.shift) ? size : base + (1 << tab.shift);
-#pragma unroll 4
-    for (int64_t i = base + N * threadIdx.x; i + N <= end; i += N * THREADS) add_squares(g + i, sum);
+    int64_t i = base + N * threadIdx.x;
+    for (; i + 3 * STEP + N <= end; i += 4 * STEP) {
+      const auto a = load_vec(g + i), b = load_vec(g + i + STEP), d = load_vec(g + i + 2 * STEP), e = load_vec(g + i + 3 * STEP);
+      add_squares(a, sum);
+      add_squares(b, more[0]);
+      add_squares(d, more[1]);
+      add_squares(e, more[2]);
+    }
+    for (; i + N <= end; i += STEP) add_squares(load_vec(g + i), sum);
     const int64_t rest = base + (end - base) / N * N + threadIdx.x;
     if (rest < end) {
       const double x = (double)load1(g, rest);
       sum = __builtin_fma(x, x, sum);
     }
   }
-  sum = block_sum(sum, lds);
+  sum = block_sum(sum + more[0] + (more[1] + more[2]), lds);
   if (threadIdx.x == 0) {
     __hip_atomic_store(&part[before + blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (last) {
@@ -474,7 +507,7 @@ __global__ __launch_bounds__(THREADS) void grad_norm_kernel(NormTable tab, doubl
   if (!joins) return;
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   sum = 0;
-  for (int64_t i = threadIdx.x; i < before + gridDim.x; i += THREADS)
+  for (int64_t i = threadIdx.x; i < before + gridDim.x; i += kNormThreads)
     sum += __hip_atomic_load(&part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   sum = block_sum(sum, lds);
   if (threadIdx.x != 0) return;
@@ -503,6 +536,15 @@ void adamw_table(const himuon_adamw_tensor *tensors, int32_t n_tensors, int stat
 }
 int adamw_arg_tensors(int state_bits) { return state_bits == 8 ? kTensors<8> : kTensors<32>; }
 
+// Chunks of the norm are long, for a block more costs its release (above): 4 M fp32 elements
+// in 4 tensors take 16.1 us in chunks of 2^12, 11.8 in 2^14 and 9.9 in 2^16, 16 M bf16 ones
+// 24.0, 19.9 and 14.4; 1 M in one tensor 9.9, 6.3 and 7.0.
+int norm_shift_of(const himuon_grad *tensors, int32_t n_tensors) {
+  int64_t total = 0;
+  for (int32_t k = 0; k < n_tensors; ++k) total += tensors[k].n;
+  return total <= ((int64_t)2 << 20) ? 14 : 16;
+}
+
 // The ticket, then one partial sum per block and kNormTensors tensors a launch.
 size_t grad_norm_workspace(int32_t n_tensors) {
   return ((size_t)n_tensors / kNormTensors + 1) * kNormBlocks * sizeof(double) + 8;
@@ -515,16 +557,16 @@ hipError_t launch_grad_norm(const himuon_grad *tensors, int32_t n_tensors, bool 
   int64_t parts = 0;
   NormTable tab;
   tab.n = 0;
-  tab.shift = shift_of(tensors, n_tensors) + 2;
+  tab.shift = norm_shift_of(tensors, n_tensors);
   tab.first[0] = 0;
   auto flush = [&](bool last) -> hipError_t {
     const int chunks = tab.first[tab.n];   // none: the last block has nothing to add of its own
     const int grid = chunks < 1 ? 1 : chunks < kNormBlocks ? chunks : kNormBlocks;
     if (bf16)
-      hipLaunchKernelGGL(grad_norm_kernel<__bf16>, dim3(grid), dim3(THREADS), 0, stream, tab, part, parts, last, ticket,
+      hipLaunchKernelGGL(grad_norm_kernel<__bf16>, dim3(grid), dim3(kNormThreads), 0, stream, tab, part, parts, last, ticket,
                          max_norm, out);
     else
-      hipLaunchKernelGGL(grad_norm_kernel<float>, dim3(grid), dim3(THREADS), 0, stream, tab, part, parts, last, ticket,
+      hipLaunchKernelGGL(grad_norm_kernel<float>, dim3(grid), dim3(kNormThreads), 0, stream, tab, part, parts, last, ticket,
                          max_norm, out);
     parts += grid;
     tab.n = 0;
