@@ -34,36 +34,34 @@ __device__ __forceinline__ void store1(float *p, int64_t i, float x) { gmem(p)[i
 __device__ __forceinline__ void store1(__bf16 *p, int64_t i, float x) {
   gmem(reinterpret_cast<unsigned short *>(p))[i] = to_bf16_bits(x);
 }
-// NT: past the caches (non-temporal)
-template <bool NT, class V>
-__device__ __forceinline__ V load_as(const GLOBAL_AS V *p) {
-  if constexpr (NT) return __builtin_nontemporal_load(p);
-  return *p;
-}
-template <bool NT, class V>
-__device__ __forceinline__ void store_as(GLOBAL_AS V *p, V x) {
-  if constexpr (NT)
-    __builtin_nontemporal_store(x, p);
-  else
-    *p = x;
-}
+// NT: past the caches (non-temporal).  (Not through a template on the vector type: deduction
+// would drop its alignment.)
 template <bool NT>
 __device__ __forceinline__ f32x4 load4(const float *p, int64_t i) {
-  return load_as<NT>(reinterpret_cast<const GLOBAL_AS f32x4u *>(gmem(p + i)));
+  const GLOBAL_AS f32x4u *q = reinterpret_cast<const GLOBAL_AS f32x4u *>(gmem(p + i));
+  if constexpr (NT) return __builtin_nontemporal_load(q);
+  return *q;
 }
 template <bool NT>
 __device__ __forceinline__ f32x4 load4(const __bf16 *p, int64_t i) {
-  const u16x4u h = load_as<NT>(reinterpret_cast<const GLOBAL_AS u16x4u *>(gmem(p + i)));
+  const GLOBAL_AS u16x4u *q = reinterpret_cast<const GLOBAL_AS u16x4u *>(gmem(p + i));
+  u16x4 h;
+  if constexpr (NT) h = __builtin_nontemporal_load(q);
+  else h = *q;
   return f32x4{bf16_bits_to_f32(h[0]), bf16_bits_to_f32(h[1]), bf16_bits_to_f32(h[2]), bf16_bits_to_f32(h[3])};
 }
 template <bool NT>
 __device__ __forceinline__ void store4(float *p, int64_t i, f32x4 x) {
-  store_as<NT>(reinterpret_cast<GLOBAL_AS f32x4u *>(gmem(p + i)), (f32x4u)x);
+  GLOBAL_AS f32x4u *q = reinterpret_cast<GLOBAL_AS f32x4u *>(gmem(p + i));
+  if constexpr (NT) __builtin_nontemporal_store(x, q);
+  else *q = x;
 }
 template <bool NT>
 __device__ __forceinline__ void store4(__bf16 *p, int64_t i, f32x4 x) {
-  store_as<NT>(reinterpret_cast<GLOBAL_AS u16x4u *>(gmem(p + i)),
-               u16x4u{to_bf16_bits(x[0]), to_bf16_bits(x[1]), to_bf16_bits(x[2]), to_bf16_bits(x[3])});
+  GLOBAL_AS u16x4u *q = reinterpret_cast<GLOBAL_AS u16x4u *>(gmem(p + i));
+  const u16x4 h = {to_bf16_bits(x[0]), to_bf16_bits(x[1]), to_bf16_bits(x[2]), to_bf16_bits(x[3])};
+  if constexpr (NT) __builtin_nontemporal_store(h, q);
+  else *q = h;
 }
 // n (0..4) elements from i on; what lies beyond them reads as zero and is not written
 template <bool NT, class T>
@@ -249,16 +247,33 @@ __device__ __forceinline__ unsigned dithered(float x, float inv, unsigned seq) {
   if constexpr (ROOT) return x > 0.f ? (unsigned)min(max(code, 1), 126) : 0u;
   return (unsigned)min(code, 126) | (word_of(x) >> 24 & 0x80u);
 }
-// The codes of a wave's block of 256 elements, four consecutive ones per lane.
+// The codes of four consecutive elements; inv = 448 / peak, 0 for a block that is held as zeros.
 template <bool ROOT>
-__device__ __forceinline__ unsigned codes_of(f32x4 x, float peak, unsigned seq, unsigned step) {
-#pragma clang fp contract(off)
-  if (!(peak >= 0x1p-100f)) return 0;   // (uniform over the wave; a NaN peak leaves a NaN scale)
-  const float inv = 1.f / peak * 448.f;
+__device__ __forceinline__ unsigned codes_of(f32x4 x, float inv, unsigned seq, unsigned step) {
   unsigned word = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) word |= dithered<ROOT>(x[e], inv, seq + e * step) << (8 * e);
-  return word;
+  return inv > 0.f ? word : 0u;   // (uniform over the wave; a NaN peak leaves a NaN scale and codes of zero)
+}
+// 448 / peak for both moments of a wave's block, as the rounded reciprocal times 448: one
+// division for the two, on even lanes the one and on odd lanes the other.
+__device__ __forceinline__ void inverses(float m_peak, float r_peak, float &m_inv, float &r_inv) {
+#pragma clang fp contract(off)
+  const float peak = threadIdx.x & 1 ? r_peak : m_peak;
+  const float inv = peak >= 0x1p-100f ? 1.f / peak * 448.f : 0.f;
+  m_inv = __builtin_bit_cast(float, __builtin_amdgcn_readlane((int)word_of(inv), 0));
+  r_inv = __builtin_bit_cast(float, __builtin_amdgcn_readlane((int)word_of(inv), 1));
+}
+
+// sqrt(v) rounded to nearest, for v = 0 or v >= 2^-96: the hardware's root s is within an ulp,
+// and v against s (s - ulp) and s (s + ulp), which lie on the midpoints' squares but for a
+// quarter of an ulp^2, says whether a neighbour is nearer.
+__device__ __forceinline__ float rounded_sqrt(float v) {
+  const float s = __builtin_amdgcn_sqrtf(v);
+  const float below = __builtin_bit_cast(float, word_of(s) - 1u), above = __builtin_bit_cast(float, word_of(s) + 1u);
+  float r = __builtin_fmaf(-below, s, v) <= 0.f ? below : s;
+  r = __builtin_fmaf(-above, s, v) > 0.f ? above : r;
+  return v < __builtin_inff() ? r : s;   // (a NaN takes s too)
 }
 
 __device__ __forceinline__ unsigned load_codes(const unsigned char *p, int64_t i, int n) {
@@ -280,47 +295,67 @@ __device__ __forceinline__ void store_codes(unsigned char *p, int64_t i, int n, 
 }
 __device__ __forceinline__ float scale_of(float peak) { return peak < 0x1p-100f ? 0.f : peak * (1.f / 448.f); }
 
-template <typename W, typename G, bool NT, class TABLE>
-__global__ __launch_bounds__(THREADS) void adamw8_kernel(TABLE tab, AdamWParams p) {
-  const float scale = p.grad_scale ? *gmem(p.grad_scale) : 1.f;
-  const int c = blockIdx.x, ti = tensor_of(tab.firsts(), tab.n, c);
-  const Entry<8> &t = tab.entries()[ti];
+// A wave's block of 256 elements from b on, four consecutive ones per lane; WHOLE: all of them
+// exist, else lanes beyond the tensor's end hold zeros throughout and stay for the reductions.
+template <typename W, typename G, bool NT, bool WHOLE>
+__device__ __forceinline__ void adamw8_block(const Entry<8> &t, int64_t b, float scale, const AdamWParams &p) {
   W *w = reinterpret_cast<W *>(t.w);
   const G *g = reinterpret_cast<const G *>(t.g);
   unsigned char *m = reinterpret_cast<unsigned char *>(t.m), *r = reinterpret_cast<unsigned char *>(t.v);
-  const float decay = 1.f - p.lr * t.weight_decay;
-  // a wave takes one whole block: lanes beyond the tensor's end stay, for the reductions
   const int lane = threadIdx.x & 63;
-  const int64_t b = ((int64_t)(c - tab.firsts()[ti]) << kChunkShift) + (threadIdx.x >> 6) * kBlock;
-  if (b >= t.n) return;
   const int64_t i = b + 4 * lane;
-  const int n = t.n - i >= 4 ? 4 : (t.n > i ? (int)(t.n - i) : 0);
+  const int n = WHOLE || t.n - i >= 4 ? 4 : (t.n > i ? (int)(t.n - i) : 0);
   float *ms = t.ms + b / kBlock, *vs = t.vs + b / kBlock;
   const float m_unit = *gmem(ms), r_unit = *gmem(vs);
   const f32x4 gv = load_upto4<NT>(g, i, n);
   const unsigned m_word = load_codes(m, i, n), r_word = load_codes(r, i, n);
   f32x4 wv = load_upto4<NT>(w, i, n);
   if (scale != scale) return;   // the gradient was not finite: nothing changes
-  f32x4 mv = unpack_e4m3x4(m_word), rv = unpack_e4m3x4(r_word);   // zeros beyond the tensor's end, throughout
+  f32x4 mv = unpack_e4m3x4(m_word), rv = unpack_e4m3x4(r_word);
   {
 #pragma clang fp contract(off)
+    bool tiny = false;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float x = gv[e] * scale, r0 = rv[e] * r_unit;
       mv[e] = p.beta1 * (mv[e] * m_unit) + p.omb1 * x;
-      rv[e] = __builtin_sqrtf(p.beta2 * (r0 * r0) + p.omb2 * x * x);
+      rv[e] = p.beta2 * (r0 * r0) + p.omb2 * x * x;
+      tiny |= rv[e] < 0x1p-96f && rv[e] > 0.f;
+    }
+    if (__builtin_expect(__ballot(tiny) == 0, 1)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rv[e] = rounded_sqrt(rv[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rv[e] = __builtin_sqrtf(rv[e]);
     }
   }
+  const float decay = 1.f - p.lr * t.weight_decay;
 #pragma unroll
   for (int e = 0; e < 4; ++e) wv[e] = new_weight(wv[e], mv[e], rv[e], decay, p);
   store_upto4<NT>(w, i, n, wv);
   const float m_peak = wave_peak(mv), r_peak = wave_peak(rv);
-  store_codes(m, i, n, codes_of<false>(mv, m_peak, (unsigned)i * kStepM + p.dither[0], kStepM));
-  store_codes(r, i, n, codes_of<true>(rv, r_peak, (unsigned)i * kStepR + p.dither[1], kStepR));
+  float m_inv, r_inv;
+  inverses(m_peak, r_peak, m_inv, r_inv);
+  store_codes(m, i, n, codes_of<false>(mv, m_inv, (unsigned)i * kStepM + p.dither[0], kStepM));
+  store_codes(r, i, n, codes_of<true>(rv, r_inv, (unsigned)i * kStepR + p.dither[1], kStepR));
   if (lane == 0) {
     *gmem(ms) = scale_of(m_peak);
     *gmem(vs) = scale_of(r_peak);
   }
+}
+
+template <typename W, typename G, bool NT, class TABLE>
+__global__ __launch_bounds__(THREADS) void adamw8_kernel(TABLE tab, AdamWParams p) {
+  const float scale = p.grad_scale ? *gmem(p.grad_scale) : 1.f;
+  const int c = blockIdx.x, ti = tensor_of(tab.firsts(), tab.n, c);
+  const Entry<8> &t = tab.entries()[ti];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t b = ((int64_t)(c - tab.firsts()[ti]) << kChunkShift) + wave * kBlock;
+  if (b + kBlock <= t.n)
+    adamw8_block<W, G, NT, true>(t, b, scale, p);
+  else if (b < t.n)
+    adamw8_block<W, G, NT, false>(t, b, scale, p);
 }
 
 // A call that moves more than this goes past the caches: nothing of it is left there when the
