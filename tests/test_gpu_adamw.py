@@ -449,3 +449,24 @@ def test_adamw8_states_are_those_of_the_formulas_in_fp32(gt):
                 y = np.clip(y, f(2 ** -9) if k else f(0), f(448)) * np.sign(x)
                 assert np.array_equal(table[a[2 + k].view(torch.uint8).cpu().numpy()], y)
                 assert np.array_equal(a[4 + k].cpu().numpy(), peak * f(1 / 448))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("wt,gt", [(F32, F32), (F32, BF16), (BF16, BF16), (BF16, F32)])
+def test_adamw_large_call_equals_small_calls(bits, wt, gt):
+    """A call of many bytes (which goes past the caches) gives the bits of calls on its tensors one by one."""
+    _need_gpu()
+    g = torch.Generator(device=DEV).manual_seed(3)
+    sizes = [4_000_003, 3, 4_000_000, 3_999_744]
+    a = []
+    for n in sizes:
+        W = torch.randn(n, device=DEV, generator=g).to(wt)
+        a.append((W, torch.randn(n, device=DEV, generator=g).to(gt), *adamw_state(W, bits)))
+    b = [tuple(x.clone() for x in t) for t in a]
+    for t in (1, 2):
+        AdamW(a, weight_decay=0.1).step(1e-2, t, dither=(t, 5))
+        for x in b:
+            AdamW([x], weight_decay=0.1).step(1e-2, t, dither=(t, 5))
+    for x, y in zip(a, b):
+        for s, u in zip(x, y):
+            assert torch.equal(s.view(torch.uint8), u.view(torch.uint8))

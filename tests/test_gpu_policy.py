@@ -329,3 +329,24 @@ def test_policy_extreme_rows_among_many(V):
     got = policy_loss(logits, label, weight, adv, old, ref)
     assert torch.isnan(got.logp[4:7]).all() and torch.isfinite(got.logp[:4]).all()
     assert torch.isnan(got.dlogits[4:7]).any(1).all() and torch.isfinite(got.dlogits[:4]).all()
+
+
+@pytest.mark.parametrize("V", [1001, 20000, 128256, 140001])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_policy_large_gradient_equals_its_parts(V, dtype):
+    """A gradient past the caches' size has the bits of the same rows in smaller calls."""
+    _need_gpu()
+    N = max(400, (40 << 20) // (V * 2))
+    logits, rest = make(400, V, dtype, 12)
+    logits = logits.repeat(-(-N // 400), 1)[:N]
+    rest = [t.repeat(-(-N // 400))[:N] for t in rest]
+    label, weight, adv, old, ref = rest
+    got = policy_loss(logits, label, weight, adv, old, ref, kl_coef=0.1)
+    n = 140
+    part = policy_loss(logits[:n], *(t[:n] for t in rest), kl_coef=0.1)
+    assert torch.equal(part.logp, got.logp[:n]) and torch.equal(part.dlogits, got.dlogits[:n])
+    fwd = policy_loss(logits, label, weight, adv, old, ref, kl_coef=0.1, dlogits=False)
+    assert torch.equal(fwd.stats, got.stats) or V > 65536   # (long rows are summed in another order without a gradient)
+    reps = N // 400
+    for k in range(1, reps):
+        assert torch.equal(got.dlogits[400 * k:400 * (k + 1)], got.dlogits[:400])

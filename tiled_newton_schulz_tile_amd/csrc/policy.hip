@@ -27,11 +27,14 @@ struct Vec<float> {
   static __device__ __forceinline__ u32x4 load(const float *p) {
     return *reinterpret_cast<const GLOBAL_AS u32x4a4 *>(gmem(p));
   }
+  template <bool NT>
   static __device__ __forceinline__ void store(float *p, const float (&x)[4]) {
     u32x4 v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = __builtin_bit_cast(unsigned, x[e]);
-    *reinterpret_cast<GLOBAL_AS u32x4a4 *>(gmem(p)) = v;
+    GLOBAL_AS u32x4a4 *q = reinterpret_cast<GLOBAL_AS u32x4a4 *>(gmem(p));
+    if constexpr (NT) __builtin_nontemporal_store(v, q);
+    else *q = v;
   }
   static __device__ __forceinline__ void unpack(u32x4 v, float (&x)[4]) {
 #pragma unroll
@@ -50,9 +53,12 @@ struct Vec<__bf16> {
   static __device__ __forceinline__ u32x4 load(const __bf16 *p) {
     return *reinterpret_cast<const GLOBAL_AS u32x4a2 *>(gmem(reinterpret_cast<const unsigned short *>(p)));
   }
+  template <bool NT>
   static __device__ __forceinline__ void store(__bf16 *p, const float (&x)[8]) {
-    *reinterpret_cast<GLOBAL_AS u32x4a2 *>(gmem(reinterpret_cast<unsigned short *>(p))) =
-        u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    const u32x4 v = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    GLOBAL_AS u32x4a2 *q = reinterpret_cast<GLOBAL_AS u32x4a2 *>(gmem(reinterpret_cast<unsigned short *>(p)));
+    if constexpr (NT) __builtin_nontemporal_store(v, q);
+    else *q = v;
   }
   static __device__ __forceinline__ void unpack(u32x4 v, float (&x)[8]) {
 #pragma unroll
@@ -205,7 +211,7 @@ __device__ __forceinline__ float sum_of(u32x4 v, float k, float ref) {
   return s;
 }
 // A vector of the gradient: coef ((j == label) - p_j), f = -coef / sum.
-template <class T>
+template <class T, bool NT>
 __device__ __forceinline__ void gradient(T *p, u32x4 v, float k, float ref, float f, float coef, int label_at) {
   float x[Vec<T>::N];
   Vec<T>::unpack(v, x);
@@ -216,24 +222,29 @@ __device__ __forceinline__ void gradient(T *p, u32x4 v, float k, float ref, floa
     for (int e = 0; e < Vec<T>::N; ++e)
       if (e == label_at) x[e] += coef;
   }
-  Vec<T>::store(p, x);
+  Vec<T>::template store<NT>(p, x);
 }
 
-template <class T, int THR>
+template <class T, int THR, bool NT>
 __device__ __forceinline__ void zero_row(T *dz, int V) {
   constexpr int N = Vec<T>::N;
   const float zero[N] = {};
   const int whole = V / N * N;
-  for (int j = threadIdx.x * N; j < whole; j += THR * N) Vec<T>::store(dz + j, zero);
+  for (int j = threadIdx.x * N; j < whole; j += THR * N) Vec<T>::template store<NT>(dz + j, zero);
   if (whole + (int)threadIdx.x < V) Vec<T>::store1(dz + whole + threadIdx.x, 0.f);
 }
+
+// What a kernel writes besides a row's terms: nothing, the gradient, or the gradient past the
+// caches.
+enum { kForward = 0, kGradient = 1, kGradientNT = 2 };
 
 // One block per row, the row in registers: K vectors of 16 bytes a thread, and one element
 // of the row's last V % N on the first threads.  The row is read once and the gradient
 // written once; -inf stands in for what lies beyond the row.
-template <typename T, int THR, int K, bool GRAD>
+template <typename T, int THR, int K, int OUT>
 __global__ __launch_bounds__(THR) void policy_row_kernel(const T *logits, T *dlogits, PolicyParams p) {
   constexpr int N = Vec<T>::N;
+  constexpr bool GRAD = OUT != kForward, NT = OUT == kGradientNT;
   __shared__ Softmax lds[THR / 64];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, V = p.vocab, vecs = V / N, rest = vecs * N + tid;
@@ -242,7 +253,7 @@ __global__ __launch_bounds__(THR) void policy_row_kernel(const T *logits, T *dlo
   const RowIn r = row_in(z, row, p);
   if (r.label < 0) {
     if (tid == 0) write_terms(0.f, f32x4{0.f, 0.f, 0.f, 0.f}, row, p);
-    if constexpr (GRAD) zero_row<T, THR>(dz, V);
+    if constexpr (GRAD) zero_row<T, THR, NT>(dz, V);
     return;
   }
   u32x4 v[K];
@@ -272,7 +283,7 @@ __global__ __launch_bounds__(THR) void policy_row_kernel(const T *logits, T *dlo
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int j = (tid + i * THR) * N;
-      if (tid + i * THR < vecs) gradient(dz + j, v[i], p.k, s.ref, f, coef, r.label - j);
+      if (tid + i * THR < vecs) gradient<T, NT>(dz + j, v[i], p.k, s.ref, f, coef, r.label - j);
     }
     if (rest < V) Vec<T>::store1(dz + rest, f * pow2(tail, p.k, s.ref) + (rest == r.label ? coef : 0.f));
   }
@@ -285,11 +296,12 @@ __global__ __launch_bounds__(THR) void policy_row_kernel(const T *logits, T *dlo
 // out: gradient 212 us held (4.35 TB/s of what has to move), 263 us with every vector read
 // twice; forward 90 us held, 78 us streamed.
 constexpr int kLongThreads = 1024;
-template <bool GRAD>
-constexpr int kLongK = GRAD ? 16 : 0;
-template <typename T, bool GRAD>
+template <int OUT>
+constexpr int kLongK = OUT != kForward ? 16 : 0;
+template <typename T, int OUT>
 __global__ __launch_bounds__(kLongThreads) void policy_long_kernel(const T *logits, T *dlogits, PolicyParams p) {
-  constexpr int N = Vec<T>::N, THR = kLongThreads, K = kLongK<GRAD>;
+  constexpr int N = Vec<T>::N, THR = kLongThreads, K = kLongK<OUT>;
+  constexpr bool GRAD = OUT != kForward, NT = OUT == kGradientNT;
   __shared__ Softmax lds[THR / 64];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, V = p.vocab, vecs = V / N, rest = vecs * N + tid;
@@ -298,7 +310,7 @@ __global__ __launch_bounds__(kLongThreads) void policy_long_kernel(const T *logi
   const RowIn r = row_in(z, row, p);
   if (r.label < 0) {
     if (tid == 0) write_terms(0.f, f32x4{0.f, 0.f, 0.f, 0.f}, row, p);
-    if constexpr (GRAD) zero_row<T, THR>(dz, V);
+    if constexpr (GRAD) zero_row<T, THR, NT>(dz, V);
     return;
   }
   u32x4 v[K > 0 ? K : 1];
@@ -330,11 +342,11 @@ __global__ __launch_bounds__(kLongThreads) void policy_long_kernel(const T *logi
   if constexpr (GRAD) {
     const float f = -coef / s.sum;
     for (at -= THR; at >= K * THR; at -= THR)
-      gradient(dz + (int64_t)at * N, Vec<T>::load(z + (int64_t)at * N), p.k, s.ref, f, coef, r.label - at * N);
+      gradient<T, NT>(dz + (int64_t)at * N, Vec<T>::load(z + (int64_t)at * N), p.k, s.ref, f, coef, r.label - at * N);
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int j = (tid + i * THR) * N;
-      gradient(dz + j, v[i], p.k, s.ref, f, coef, r.label - j);
+      gradient<T, NT>(dz + j, v[i], p.k, s.ref, f, coef, r.label - j);
     }
     if (rest < V) Vec<T>::store1(dz + rest, f * pow2(tail, p.k, s.ref) + (rest == r.label ? coef : 0.f));
   }
@@ -504,7 +516,7 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_finish_kernel(const 
 #pragma unroll
     for (int i = 0; i < kSpanK; ++i) {
       const int at = v0 + tid + i * THR;
-      if (at < vecs) Vec<T>::store(dz + (int64_t)at * N, zero);
+      if (at < vecs) Vec<T>::template store<false>(dz + (int64_t)at * N, zero);
     }
     if (has_rest) Vec<T>::store1(dz + rest, 0.f);
     return;
@@ -522,7 +534,7 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_finish_kernel(const 
 #pragma unroll
   for (int i = 0; i < kSpanK; ++i) {
     const int at = v0 + tid + i * THR;
-    if (at < vecs) gradient(dz + (int64_t)at * N, v[i], p.k, s.ref, f, coef, r.label - at * N);
+    if (at < vecs) gradient<T, false>(dz + (int64_t)at * N, v[i], p.k, s.ref, f, coef, r.label - at * N);
   }
   if (has_rest) Vec<T>::store1(dz + rest, f * pow2(tail, p.k, s.ref) + (rest == r.label ? coef : 0.f));
 }
@@ -535,12 +547,24 @@ bool few_rows(int64_t rows, int64_t vecs) {
   return rows > 0 && ((rows <= 64 && vecs >= 256) || (rows <= 128 && vecs >= 2048));
 }
 
+// A gradient that the L2s together (32 MB) cannot hold goes past them: 4096 x 128256 bf16 356 /
+// 339 us, 256 x 128256 33 / 28 us, 1000 x 128256 fp32 213 / 195 us.  A smaller one stays for
+// whoever reads it next.
+constexpr double kL2Bytes = 32e6;
+
 template <typename T, int THR, int K>
-void launch_rows(const T *z, T *dz, unsigned rows, const PolicyParams &p, hipStream_t stream) {
-  if (dz)
-    hipLaunchKernelGGL((policy_row_kernel<T, THR, K, true>), dim3(rows), dim3(THR), 0, stream, z, dz, p);
-  else
-    hipLaunchKernelGGL((policy_row_kernel<T, THR, K, false>), dim3(rows), dim3(THR), 0, stream, z, nullptr, p);
+void launch_rows(const T *z, T *dz, unsigned rows, int out, const PolicyParams &p, hipStream_t stream) {
+  const dim3 grid(rows), block(THR);
+  if (out == kForward) hipLaunchKernelGGL((policy_row_kernel<T, THR, K, kForward>), grid, block, 0, stream, z, dz, p);
+  else if (out == kGradient) hipLaunchKernelGGL((policy_row_kernel<T, THR, K, kGradient>), grid, block, 0, stream, z, dz, p);
+  else hipLaunchKernelGGL((policy_row_kernel<T, THR, K, kGradientNT>), grid, block, 0, stream, z, dz, p);
+}
+template <typename T>
+void launch_long_rows(const T *z, T *dz, unsigned rows, int out, const PolicyParams &p, hipStream_t stream) {
+  const dim3 grid(rows), block(kLongThreads);
+  if (out == kForward) hipLaunchKernelGGL((policy_long_kernel<T, kForward>), grid, block, 0, stream, z, dz, p);
+  else if (out == kGradient) hipLaunchKernelGGL((policy_long_kernel<T, kGradient>), grid, block, 0, stream, z, dz, p);
+  else hipLaunchKernelGGL((policy_long_kernel<T, kGradientNT>), grid, block, 0, stream, z, dz, p);
 }
 
 template <typename T>
@@ -558,6 +582,7 @@ hipError_t launch_policy_t(const himuon_policy &c, const PolicyParams &p, hipStr
                        stream, z, dz, p, (int32_t)rows, (int32_t)spans, c.stats);
     return hipGetLastError();
   }
+  const int out = !dz ? kForward : (double)c.rows * c.vocab * sizeof(T) > kL2Bytes ? kGradientNT : kGradient;
   // (a grid's x extent holds 2^31 - 1 blocks; rows beyond go into further launches)
   constexpr int64_t kRows = (int64_t)1 << 30;
   for (int64_t r = 0; r < c.rows; r += kRows) {
@@ -572,16 +597,13 @@ hipError_t launch_policy_t(const himuon_policy &c, const PolicyParams &p, hipStr
     q.part += r;
     const T *zr = z + r * c.ld_logits;
     T *dr = dz ? dz + r * c.ld_dlogits : nullptr;
-    if (vecs <= 64 * 4) launch_rows<T, 64, 4>(zr, dr, rows, q, stream);
-    else if (vecs <= 256 * 4) launch_rows<T, 256, 4>(zr, dr, rows, q, stream);
-    else if (vecs <= 512 * 4) launch_rows<T, 512, 4>(zr, dr, rows, q, stream);
-    else if (vecs <= 512 * 8) launch_rows<T, 512, 8>(zr, dr, rows, q, stream);
-    else if (vecs <= 1024 * 8) launch_rows<T, 1024, 8>(zr, dr, rows, q, stream);
-    else if (vecs <= 1024 * 16) launch_rows<T, 1024, 16>(zr, dr, rows, q, stream);
-    else if (dr)
-      hipLaunchKernelGGL((policy_long_kernel<T, true>), dim3(rows), dim3(kLongThreads), 0, stream, zr, dr, q);
-    else
-      hipLaunchKernelGGL((policy_long_kernel<T, false>), dim3(rows), dim3(kLongThreads), 0, stream, zr, nullptr, q);
+    if (vecs <= 64 * 4) launch_rows<T, 64, 4>(zr, dr, rows, out, q, stream);
+    else if (vecs <= 256 * 4) launch_rows<T, 256, 4>(zr, dr, rows, out, q, stream);
+    else if (vecs <= 512 * 4) launch_rows<T, 512, 4>(zr, dr, rows, out, q, stream);
+    else if (vecs <= 512 * 8) launch_rows<T, 512, 8>(zr, dr, rows, out, q, stream);
+    else if (vecs <= 1024 * 8) launch_rows<T, 1024, 8>(zr, dr, rows, out, q, stream);
+    else if (vecs <= 1024 * 16) launch_rows<T, 1024, 16>(zr, dr, rows, out, q, stream);
+    else launch_long_rows<T>(zr, dr, rows, out, q, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
