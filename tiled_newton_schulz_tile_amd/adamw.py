@@ -107,7 +107,7 @@ class AdamW:
         for row in zip(n, *ptrs, bits):
             self._words.extend([x & (2 ** 64 - 1) for x in row])
         self._c = (himuon_adamw_tensor * len(n)).from_buffer(self._words)
-        self._n, self._tensors = n, cols
+        self._n, self._tensors, self._grad_dtype = n, cols, cols[1][0].dtype
         dt = lambda t: F32 if t.dtype == torch.float32 else BF16  # noqa: E731
         self.cfg = himuon_adamw_config(dt(cols[0][0]), dt(cols[1][0]), self.bits, betas[0], betas[1], eps)
         size = himuon_adamw_table_size(self._c, self.cfg)
@@ -127,7 +127,7 @@ class AdamW:
         grads = tuple(grads)
         if len(grads) != len(self._n):
             raise ValueError("one gradient per tensor")
-        size, at = _column(grads, "G", (self._tensors[1][0].dtype,), self.device)
+        size, at = _column(grads, "G", (self._grad_dtype,), self.device)
         if size != self._n:
             raise ValueError("a gradient must have its weight's number of elements")
         self._tensors[1] = grads
@@ -138,6 +138,11 @@ class AdamW:
             himuon_adamw_table(self._c, self.cfg, host.data_ptr(), host.numel())
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
                 self._table.copy_(host[:self._table.numel()], non_blocking=True)
+
+    def drop_grads(self) -> None:
+        """Forgets the gradients, so that their memory may go; set_grads gives the next step's, unless those are at
+        the same addresses."""
+        self._tensors[1] = (None,) * len(self._n)
 
     def step(self, lr: float, t: int, scale=None, dither=None, stream=None) -> None:
         """Step number t >= 1.  scale: None or a float32 CUDA tensor whose first element multiplies

@@ -5,7 +5,8 @@
 dense weights and names runtime tile-size schedules among what the tiling allows.
 Which parameters count as such matrices, and what updates the rest, is not on the
 pages; the convention here: every 2-D parameter goes through HiMuon, every other
-parameter through a plain torch optimizer (AdamW unless one is given).  A parameter
+parameter through a plain torch optimizer (AdamW unless one is given; AdamWOptimizer below
+is this library's own, one launch over all of them, with 32-bit or 8-bit states).  A parameter
 group can opt out with ``use_himuon=False``.  HiMuon parameters that share a learning
 rate share one plan (one launch per kernel covers all of their layers); groups with
 their own ``lr`` get a plan each, and the step reads every group's current ``lr``, so
@@ -20,10 +21,12 @@ pass, while the plan holds device pointers).
 from __future__ import annotations
 
 import bisect
+import random
 
 import torch
 
 from . import HiMuon, PREC_BF16X3, QUINTIC
+from .adamw import AdamW, adamw_state
 
 
 class TileSchedule:
@@ -132,7 +135,13 @@ class HiMuonOptimizer(torch.optim.Optimizer):
             self._grads.append(grads)
 
     @torch.no_grad()
-    def step(self, closure=None):
+    def step(self, closure=None, grad_scale=None):
+        """grad_scale: None, or a float32 CUDA tensor whose first element multiplies every gradient (the clip
+        factor of adamw.GradNorm), read on the device.  Where it is NaN (a gradient that is not finite) the HiMuon
+        gradients count as zero and an AdamWOptimizer fallback skips its step.  Other fallbacks take unscaled
+        gradients, so a grad_scale with them is refused."""
+        if grad_scale is not None and self.fallback is not None and not isinstance(self.fallback, AdamWOptimizer):
+            raise ValueError("grad_scale needs an AdamWOptimizer fallback")
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -148,11 +157,17 @@ class HiMuonOptimizer(torch.optim.Optimizer):
             for p, g in zip(grp["params"], grads):
                 if p.grad is None:
                     g.zero_()
-                else:
+                elif grad_scale is None:
                     g.copy_(p.grad)
+                else:
+                    factor = grad_scale.flatten()[:1]
+                    g.copy_(torch.where(factor.isnan(), 0.0, p.grad.flatten() * factor).view(p.grad.shape))
             eng.step(float(grp["lr"]))
         if self.fallback is not None:
-            self.fallback.step()
+            if grad_scale is None:
+                self.fallback.step()
+            else:
+                self.fallback.step(grad_scale=grad_scale)
         for grp in self.param_groups:
             grp["step_count"] = self.step_count + 1
         return loss
@@ -195,3 +210,92 @@ class HiMuonOptimizer(torch.optim.Optimizer):
                 eng.close()
             self._engines = None
             self._grads = None
+
+
+class AdamWOptimizer(torch.optim.Optimizer):
+    """AdamW on this library's kernels (adamw.AdamW): every parameter of a group in one launch.
+
+    Parameters are contiguous float32 or bfloat16 CUDA tensors; lr, betas, eps and
+    weight_decay are per group as in torch.  state_bits: 32 (float32 moments) or 8 (e4m3
+    values with a scale per 256 elements; `seed` starts the random numbers of their
+    rounding).  A parameter's state is ``state[p]["adamw"]``, the tensors that
+    adamw.adamw_state makes; its step count starts with its first gradient."""
+
+    def __init__(self, params, lr: float = 3e-4, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                 state_bits: int = 32, seed: int = 0):
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
+        for g in self.param_groups:
+            for p in g["params"]:
+                if p.dtype not in (torch.float32, torch.bfloat16) or not p.is_cuda or not p.is_contiguous():
+                    raise ValueError("parameters must be contiguous float32 or bfloat16 CUDA tensors")
+        self.state_bits = state_bits
+        self._random = random.Random(seed)
+        self._engines = {}
+
+    def _engine(self, key, params, group):
+        """The AdamW over these parameters, kept while they and the group's constants stay the same."""
+        held = self._engines.get(key)
+        constants = (group["betas"], group["eps"], group["weight_decay"])
+        same = held is not None and held[1] == constants and len(held[2]) == len(params) and \
+            all(a is b for a, b in zip(held[2], params))
+        grads = [p.grad if p.grad.is_contiguous() else p.grad.contiguous() for p in params]
+        if not same:
+            held = (AdamW([(p.data, g, *self.state[p]["adamw"]) for p, g in zip(params, grads)], group["betas"],
+                          group["eps"], group["weight_decay"]), constants, list(params))
+            self._engines[key] = held
+        elif any(g.data_ptr() != c.grad for g, c in zip(grads, held[0]._c)):
+            held[0].set_grads(grads)
+        return held[0]
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale=None):
+        """grad_scale: None, or a float32 CUDA tensor whose first element multiplies the gradients; NaN leaves
+        parameters and states as they are."""
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for k, group in enumerate(self.param_groups):
+            calls = {}
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                st = self.state[p]
+                if "adamw" not in st:
+                    st["step"], st["adamw"] = 0, adamw_state(p, self.state_bits)
+                st["step"] += 1
+                calls.setdefault((k, p.device.index, p.dtype, p.grad.dtype, st["step"]), []).append(p)
+            for (*key, t), params in calls.items():
+                # parameters that joined late have a step count, and an engine, of their own
+                key = (*key, tuple(map(id, params)) if len(calls) > 1 else None)
+                dither = [self._random.getrandbits(32) for _ in range(2)] if self.state_bits == 8 else None
+                engine = self._engine(key, params, group)
+                engine.step(float(group["lr"]), t, scale=grad_scale, dither=dither)
+                engine.drop_grads()
+        return loss
+
+    def state_dict(self):
+        sd = super().state_dict()
+        sd["random"] = self._random.getstate()
+        return sd
+
+    def load_state_dict(self, state_dict):
+        """Restores states bit for bit (torch would cast them to the parameters' dtype) and the random numbers."""
+        state_dict = dict(state_dict)
+        rng = state_dict.pop("random", None)
+        held = state_dict["state"]
+        super().load_state_dict({**state_dict, "state": {}})
+        for saved, group in zip(state_dict["param_groups"], self.param_groups):
+            for i, p in zip(saved["params"], group["params"]):
+                st = held.get(i)
+                if not st:
+                    continue
+                kept = tuple(x.to(p.device, copy=True) for x in st["adamw"])
+                if len(kept) != (2 if self.state_bits == 32 else 4) or kept[0].shape != p.shape:
+                    raise ValueError("the saved states are of another kind or shape")
+                self.state[p] = {"step": int(st["step"]), "adamw": kept}
+        if rng is not None:
+            self._random.setstate((rng[0], tuple(rng[1]), rng[2]))
+        self._engines = {}
