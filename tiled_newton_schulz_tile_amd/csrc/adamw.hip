@@ -223,28 +223,24 @@ __device__ __forceinline__ unsigned wave_max(unsigned x) {
 
 // Largest magnitude of a wave's values, compared as bit patterns, so that a NaN is larger than
 // everything and stays.
+template <bool ROOT>
 __device__ __forceinline__ float wave_peak(f32x4 x) {
   unsigned k = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) k = max(k, word_of(x[e]) & 0x7fffffffu);   // (by value: a bit cast of x[e] itself takes x[0])
-  return __builtin_bit_cast(float, wave_max(k));
+  for (int e = 0; e < 4; ++e) k = max(k, word_of(x[e]) & (ROOT ? 0xffffffffu : 0x7fffffffu));   // (word_of takes
+  return __builtin_bit_cast(float, wave_max(k));   // a copy: a bit cast of x[e] itself would be that of x[0])
 }
 // The e4m3 code of x in units of the block's scale, rounded to a neighbouring value as the
-// dither says.  Three mantissa bits are kept; a dither of 16 bits and a half, added at the top
-// of the bits that are cut, carries up with the probability of the distance to the lower
-// neighbour.  Below 2^-6 the values are 2^-9 apart, as they are from 2^-6 to 2^-5, so such
-// magnitudes are rounded with 2^-6 added.  The exponent and the kept bits then are the code,
-// but for a constant.
+// dither says.  y 2^-120 is an fp32 number whose exponent field, three mantissa bits on, is the
+// e4m3 code of y: fp32's subnormals start at 2^-126 as e4m3's do at 2^-6, with 20 bits more.  A
+// dither of 16 bits and a half, added at the top of the 20 bits that are cut, carries up with
+// the probability of the distance to the lower neighbour.
 // ROOT: x is a root, not negative; one that is not zero gets the smallest code at least.
 template <bool ROOT>
 __device__ __forceinline__ unsigned dithered(float x, float inv, unsigned seq) {
-#pragma clang fp contract(off)
-  float y = __builtin_fabsf(x) * inv;
-  const bool low = y < 0x1p-6f;
-  y += low ? 0x1p-6f : 0.f;
-  const unsigned cut = (word_of(y) + ((seq >> 16) << 4 | 8u)) >> 20;
-  const int code = (int)(cut - (low ? (127u - 6) << 3 : (127u - 7) << 3));   // 0 for x = 0; 126 is 448
-  if constexpr (ROOT) return x > 0.f ? (unsigned)min(max(code, 1), 126) : 0u;
+  const float y = __builtin_fabsf(x) * inv;
+  const int code = (int)((word_of(y * 0x1p-120f) + ((seq >> 16) << 4) + 8u) >> 20);   // 126 is 448
+  if constexpr (ROOT) return (unsigned)min(max(code, (int)min(word_of(x), 1u)), 126);
   return (unsigned)min(code, 126) | (word_of(x) >> 24 & 0x80u);
 }
 // The codes of four consecutive elements; inv = 448 / peak, 0 for a block that is held as zeros.
@@ -252,7 +248,7 @@ template <bool ROOT>
 __device__ __forceinline__ unsigned codes_of(f32x4 x, float inv, unsigned seq, unsigned step) {
   unsigned word = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) word |= dithered<ROOT>(x[e], inv, seq + e * step) << (8 * e);
+  for (int e = 3; e >= 0; --e) word = word << 8 | dithered<ROOT>(x[e], inv, seq + e * step);
   return inv > 0.f ? word : 0u;   // (uniform over the wave; a NaN peak leaves a NaN scale and codes of zero)
 }
 // 448 / peak for both moments of a wave's block, as the rounded reciprocal times 448: one
@@ -265,15 +261,14 @@ __device__ __forceinline__ void inverses(float m_peak, float r_peak, float &m_in
   r_inv = __builtin_bit_cast(float, __builtin_amdgcn_readlane((int)word_of(inv), 1));
 }
 
-// sqrt(v) rounded to nearest, for v = 0 or v >= 2^-96: the hardware's root s is within an ulp,
+// sqrt(v) rounded to nearest, for v = 0 or v in [2^-96, inf): the hardware's root s is within an ulp,
 // and v against s (s - ulp) and s (s + ulp), which lie on the midpoints' squares but for a
 // quarter of an ulp^2, says whether a neighbour is nearer.
 __device__ __forceinline__ float rounded_sqrt(float v) {
   const float s = __builtin_amdgcn_sqrtf(v);
   const float below = __builtin_bit_cast(float, word_of(s) - 1u), above = __builtin_bit_cast(float, word_of(s) + 1u);
   float r = __builtin_fmaf(-below, s, v) <= 0.f ? below : s;
-  r = __builtin_fmaf(-above, s, v) > 0.f ? above : r;
-  return v < __builtin_inff() ? r : s;   // (a NaN takes s too)
+  return __builtin_fmaf(-above, s, v) > 0.f ? above : r;
 }
 
 __device__ __forceinline__ unsigned load_codes(const unsigned char *p, int64_t i, int n) {
@@ -314,15 +309,16 @@ __device__ __forceinline__ void adamw8_block(const Entry<8> &t, int64_t b, float
   f32x4 mv = unpack_e4m3x4(m_word), rv = unpack_e4m3x4(r_word);
   {
 #pragma clang fp contract(off)
-    bool tiny = false;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float x = gv[e] * scale, r0 = rv[e] * r_unit;
       mv[e] = p.beta1 * (mv[e] * m_unit) + p.omb1 * x;
       rv[e] = p.beta2 * (r0 * r0) + p.omb2 * x * x;
-      tiny |= rv[e] < 0x1p-96f && rv[e] > 0.f;
     }
-    if (__builtin_expect(__ballot(tiny) == 0, 1)) {
+    // (a NaN may hide from the minimum and the maximum: it stays one through rounded_sqrt)
+    const float least = __builtin_fminf(__builtin_fminf(rv[0], rv[1]), __builtin_fminf(rv[2], rv[3]));
+    const float most = __builtin_fmaxf(__builtin_fmaxf(rv[0], rv[1]), __builtin_fmaxf(rv[2], rv[3]));
+    if (__builtin_expect(__ballot(!(least >= 0x1p-96f && most < __builtin_inff()) && most != 0.f) == 0, 1)) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) rv[e] = rounded_sqrt(rv[e]);
     } else {
@@ -334,7 +330,7 @@ __device__ __forceinline__ void adamw8_block(const Entry<8> &t, int64_t b, float
 #pragma unroll
   for (int e = 0; e < 4; ++e) wv[e] = new_weight(wv[e], mv[e], rv[e], decay, p);
   store_upto4<NT>(w, i, n, wv);
-  const float m_peak = wave_peak(mv), r_peak = wave_peak(rv);
+  const float m_peak = wave_peak<false>(mv), r_peak = wave_peak<true>(rv);
   float m_inv, r_inv;
   inverses(m_peak, r_peak, m_inv, r_inv);
   store_codes(m, i, n, codes_of<false>(mv, m_inv, (unsigned)i * kStepM + p.dither[0], kStepM));
