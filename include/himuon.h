@@ -402,8 +402,8 @@ HIMUON_API himuon_status himuon_adamw_step(const himuon_adamw_tensor *tensors, i
                                            const float *grad_scale, const uint32_t *dither, const void *table,
                                            void *hip_stream);
 
-/* Descriptors of many tensors for the device: *bytes is 0 where one launch holds them in
-   its arguments anyway, else the size of the table.  himuon_adamw_table writes it into host
+/* Descriptors of many tensors for the device: *bytes is 0 where a table gains nothing (8
+   tensors at most), else its size.  himuon_adamw_table writes it into host
    memory (8-byte aligned), from where the caller copies it to device memory (16-byte
    aligned); it holds for as long as no pointer, size or weight_decay of the tensors changes. */
 HIMUON_API himuon_status himuon_adamw_table_size(const himuon_adamw_tensor *tensors, int32_t n_tensors,

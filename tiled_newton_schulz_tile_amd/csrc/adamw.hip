@@ -100,19 +100,22 @@ struct Entry<8> {
   int64_t n;
   float weight_decay;
 };
+// Up to kMost tensors travel in the arguments, which have 4 KB; a call of kFew at most takes a
+// small table, for the launch of the large one costs the host a microsecond and a half more.
 template <int BITS>
-constexpr int kTensors = BITS == 8 ? 56 : 72;
+constexpr int kMost = BITS == 8 ? 56 : 72;
+constexpr int kFew = 8;
 
-template <int BITS>
+template <int BITS, int CAP>
 struct ArgTable {
   int32_t n;
-  int32_t first[kTensors<BITS> + 1];   // first chunk of each tensor; [n]: all chunks
-  Entry<BITS> t[kTensors<BITS>];
+  int32_t first[CAP + 1];   // first chunk of each tensor; [n]: all chunks
+  Entry<BITS> t[CAP];
   __device__ __forceinline__ const int32_t *firsts() const { return first; }
   __device__ __forceinline__ const Entry<BITS> *entries() const { return t; }
 };
-static_assert(sizeof(ArgTable<32>) + sizeof(AdamWParams) <= 4096, "kernel arguments");
-static_assert(sizeof(ArgTable<8>) + sizeof(AdamWParams) <= 4096, "kernel arguments");
+static_assert(sizeof(ArgTable<32, kMost<32>>) + sizeof(AdamWParams) <= 4096, "kernel arguments");
+static_assert(sizeof(ArgTable<8, kMost<8>>) + sizeof(AdamWParams) <= 4096, "kernel arguments");
 
 // The same in device memory: n + 1 first chunks, then the entries at entry_offset(n).
 size_t entry_offset(int64_t n) { return ((size_t)(n + 1) * sizeof(int32_t) + 15) / 16 * 16; }
@@ -417,6 +420,31 @@ void fill_table(const himuon_adamw_tensor *tensors, int32_t n_tensors, char *hos
   first[n] = (int32_t)at;
 }
 
+template <int BITS, int CAP>
+hipError_t launch_args(const himuon_adamw_tensor *tensors, int32_t n_tensors, Kind kind, const AdamWParams &p,
+                       hipStream_t stream) {
+  ArgTable<BITS, CAP> tab;
+  tab.n = 0;
+  tab.first[0] = 0;
+  auto flush = [&]() -> hipError_t {
+    if (tab.n == 0) return hipSuccess;
+    hipError_t e = launch_table<BITS>(tab, tab.first[tab.n], kind, p, stream);
+    tab.n = 0;
+    return e;
+  };
+  for (int32_t k = 0; k < n_tensors; ++k) {
+    if (tensors[k].n == 0) continue;
+    if (tab.n == CAP) {
+      hipError_t e = flush();
+      if (e != hipSuccess) return e;
+    }
+    fill_entry<BITS>(tab.t[tab.n], tensors[k]);
+    tab.first[tab.n + 1] = (int32_t)(tab.first[tab.n] + chunks_of(tensors[k].n, kChunkShift));
+    ++tab.n;
+  }
+  return flush();
+}
+
 template <int BITS>
 hipError_t launch_adamw_bits(const himuon_adamw_tensor *tensors, int32_t n_tensors, bool weight_bf16, bool grad_bf16,
                              const AdamWParams &p, const void *table, hipStream_t stream) {
@@ -436,26 +464,8 @@ hipError_t launch_adamw_bits(const himuon_adamw_tensor *tensors, int32_t n_tenso
     if (chunks == 0) return hipSuccess;
     return launch_table<BITS>(tab, chunks, kind, p, stream);
   }
-  ArgTable<BITS> tab;
-  tab.n = 0;
-  tab.first[0] = 0;
-  auto flush = [&]() -> hipError_t {
-    if (tab.n == 0) return hipSuccess;
-    hipError_t e = launch_table<BITS>(tab, tab.first[tab.n], kind, p, stream);
-    tab.n = 0;
-    return e;
-  };
-  for (int32_t k = 0; k < n_tensors; ++k) {
-    if (tensors[k].n == 0) continue;
-    if (tab.n == kTensors<BITS>) {
-      hipError_t e = flush();
-      if (e != hipSuccess) return e;
-    }
-    fill_entry<BITS>(tab.t[tab.n], tensors[k]);
-    tab.first[tab.n + 1] = (int32_t)(tab.first[tab.n] + chunks_of(tensors[k].n, kChunkShift));
-    ++tab.n;
-  }
-  return flush();
+  return n_tensors <= kFew ? launch_args<BITS, kFew>(tensors, n_tensors, kind, p, stream)
+                           : launch_args<BITS, kMost<BITS>>(tensors, n_tensors, kind, p, stream);
 }
 
 // ------------------------------------------------------------------ gradient norm
@@ -565,7 +575,7 @@ void adamw_table(const himuon_adamw_tensor *tensors, int32_t n_tensors, int stat
   else
     fill_table<32>(tensors, n_tensors, reinterpret_cast<char *>(host));
 }
-int adamw_arg_tensors(int state_bits) { return state_bits == 8 ? kTensors<8> : kTensors<32>; }
+int adamw_few_tensors() { return kFew; }
 
 // Chunks of the norm are long, for a block more costs its release (above): 4 M fp32 elements
 // in 4 tensors take 16.1 us in chunks of 2^12, 11.8 in 2^14 and 9.9 in 2^16, 16 M bf16 ones

@@ -179,13 +179,13 @@ struct AdamWParams {
   uint32_t dither[2];
   const float *grad_scale; // device, or nullptr
 };
-// table: nullptr (descriptors in the kernel arguments, adamw_arg_tensors() a launch), or
+// table: nullptr (descriptors in the kernel arguments, 56 or 72 a launch), or
 // device memory with what adamw_table wrote for these tensors (one launch).
 hipError_t launch_adamw(const himuon_adamw_tensor *tensors, int32_t n_tensors, bool weight_bf16, bool grad_bf16,
                         int state_bits, const AdamWParams &p, const void *table, hipStream_t stream);
 size_t adamw_table_size(int32_t n_tensors, int state_bits);
 void adamw_table(const himuon_adamw_tensor *tensors, int32_t n_tensors, int state_bits, void *host);
-int adamw_arg_tensors(int state_bits);
+int adamw_few_tensors();   // a call of that many needs no table
 
 size_t grad_norm_workspace(int32_t n_tensors);
 hipError_t launch_grad_norm(const himuon_grad *tensors, int32_t n_tensors, bool bf16, double max_norm, float *out,

@@ -129,8 +129,7 @@ HIMUON_API himuon_status himuon_adamw_table_size(const himuon_adamw_tensor *tens
   if (!bytes) return bad("NULL argument");
   himuon_status s = check_adamw(tensors, n_tensors, cfg);
   if (s != HIMUON_OK) return s;
-  *bytes = n_tensors > himuon::adamw_arg_tensors(cfg->state_bits) ? himuon::adamw_table_size(n_tensors, cfg->state_bits)
-                                                                  : 0;
+  *bytes = n_tensors > himuon::adamw_few_tensors() ? himuon::adamw_table_size(n_tensors, cfg->state_bits) : 0;
   return HIMUON_OK;
 } catch (...) {
   return HIMUON_ENOMEM;
