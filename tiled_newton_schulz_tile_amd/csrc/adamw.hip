@@ -11,6 +11,7 @@
 // with the alignment of one element and the hardware takes unaligned global accesses.
 #include "device_common.h"
 #include "himuon_internal.h"
+#include "wave_reduce.h"
 
 #include <cmath>
 
@@ -208,21 +209,6 @@ __device__ __forceinline__ f32x4 unpack_e4m3x4(unsigned x) {
 }
 
 __device__ __forceinline__ unsigned word_of(float x) { return __builtin_bit_cast(unsigned, x); }
-
-// Maximum over a wave with DPP moves (rows of 16, then the rows' last lanes).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ unsigned max_step(unsigned x) {
-  return max(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false));
-}
-__device__ __forceinline__ unsigned wave_max(unsigned x) {
-  x = max_step<0x111, 0xf>(x);
-  x = max_step<0x112, 0xf>(x);
-  x = max_step<0x114, 0xf>(x);
-  x = max_step<0x118, 0xf>(x);
-  x = max_step<0x142, 0xa>(x);
-  x = max_step<0x143, 0xc>(x);
-  return (unsigned)__builtin_amdgcn_readlane((int)x, 63);
-}
 
 // Largest magnitude of a wave's values, compared as bit patterns, so that a NaN is larger than
 // everything and stays.
@@ -475,11 +461,6 @@ hipError_t launch_adamw_bits(const himuon_adamw_tensor *tensors, int32_t n_tenso
 // in 8192; 1024 blocks 377 us, these 356 us (6.0 TB/s).
 constexpr int kNormThreads = 512, kNormBlocks = 512;   // each block leaves one partial sum
 
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
-  return x;
-}
 __device__ __forceinline__ double block_sum(double x, double *lds) {
   x = wave_sum(x);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;

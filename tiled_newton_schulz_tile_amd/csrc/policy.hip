@@ -5,6 +5,7 @@
 // rounding to fewer bits is that of the gradient to bf16 logits' own type.
 #include "device_common.h"
 #include "himuon_internal.h"
+#include "wave_reduce.h"
 
 namespace himuon {
 namespace {
@@ -75,35 +76,6 @@ struct Vec<__bf16> {
     *gmem(reinterpret_cast<unsigned short *>(p)) = to_bf16_bits(x);
   }
 };
-
-// Reductions over a wave with DPP moves (no LDS): rows of 16, then the rows' last lanes.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp(float old, float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, x),
-                                                               CTRL, ROWS, 0xf, false));
-}
-__device__ __forceinline__ float last_lane(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
-}
-__device__ __forceinline__ float wave_max(float x) {
-  const float none = -__builtin_inff();
-  x = __builtin_fmaxf(x, dpp<0x111, 0xf>(none, x));
-  x = __builtin_fmaxf(x, dpp<0x112, 0xf>(none, x));
-  x = __builtin_fmaxf(x, dpp<0x114, 0xf>(none, x));
-  x = __builtin_fmaxf(x, dpp<0x118, 0xf>(none, x));
-  x = __builtin_fmaxf(x, dpp<0x142, 0xa>(none, x));
-  x = __builtin_fmaxf(x, dpp<0x143, 0xc>(none, x));
-  return last_lane(x);
-}
-__device__ __forceinline__ float wave_sum(float x) {
-  x += dpp<0x111, 0xf>(0.f, x);
-  x += dpp<0x112, 0xf>(0.f, x);
-  x += dpp<0x114, 0xf>(0.f, x);
-  x += dpp<0x118, 0xf>(0.f, x);
-  x += dpp<0x142, 0xa>(0.f, x);
-  x += dpp<0x143, 0xc>(0.f, x);
-  return last_lane(x);
-}
 
 // Constants of a call in fp32.
 struct PolicyParams {
@@ -359,9 +331,7 @@ __device__ __forceinline__ void write_stats(const double (&mine)[3], float kl_co
   __shared__ double lds[W][3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    double s = mine[k];
-#pragma unroll
-    for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+    const double s = wave_sum(mine[k]);
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6][k] = s;
   }
   __syncthreads();
