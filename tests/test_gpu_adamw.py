@@ -470,3 +470,9 @@ def test_adamw_large_call_equals_small_calls(bits, wt, gt):
     for x, y in zip(a, b):
         for s, u in zip(x, y):
             assert torch.equal(s.view(torch.uint8), u.view(torch.uint8))
+
+
+def test_grad_norm_of_nothing():
+    _need_gpu()
+    got = GradNorm([torch.zeros(0, device=DEV), torch.zeros(0, device=DEV)]).compute(0.5)
+    assert got.tolist() == [0.0, 1.0]

@@ -350,3 +350,18 @@ def test_policy_large_gradient_equals_its_parts(V, dtype):
     reps = N // 400
     for k in range(1, reps):
         assert torch.equal(got.dlogits[400 * k:400 * (k + 1)], got.dlogits[:400])
+
+
+def test_policy_more_rows_than_a_launch_holds():
+    _need_gpu()
+    N, V = (1 << 21) + 3, 9
+    g = torch.Generator(device=DEV).manual_seed(1)
+    z = torch.randn(N, V, device=DEV, generator=g).bfloat16()
+    label = torch.randint(-1, V, (N,), device=DEV, generator=g)
+    weight, adv = torch.rand(N, device=DEV, generator=g), torch.randn(N, device=DEV, generator=g)
+    got = policy_loss(z, label, weight, adv)
+    for part in (slice(N - 300, N), slice(1000, 1300)):
+        one = policy_loss(z[part], label[part], weight[part], adv[part])
+        assert torch.equal(one.logp, got.logp[part]) and torch.equal(one.dlogits, got.dlogits[part])
+    live = label >= 0
+    assert abs(float(got.stats[1]) + float((weight * adv)[live].double().sum())) <= 1e-6 * float((weight * adv.abs())[live].sum())

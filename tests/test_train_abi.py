@@ -111,3 +111,35 @@ def test_adamw_table_refuses():
     refused(hm.himuon_adamw_table, tensors(dict(m=None)), config(), at, n)
     refused(hm.himuon_adamw_table_size, tensors(dict(n=-1)), config())
     refused(hm.himuon_adamw_step, many, config(), 1, 0.1, 0, None, FAKE + 8, 0)
+
+
+def test_wrappers_refuse_host_tensors():
+    import torch
+    from tiled_newton_schulz_tile_amd.adamw import AdamW, GradNorm, adamw_state
+    from tiled_newton_schulz_tile_amd.optim import AdamWOptimizer
+    from tiled_newton_schulz_tile_amd.policy import policy_loss
+    x = torch.zeros(8)
+    for call in (lambda: AdamW([(x, x, *adamw_state(x))]), lambda: GradNorm([x]), lambda: AdamW([]), lambda: GradNorm([]),
+                 lambda: AdamWOptimizer([torch.nn.Parameter(x)]),
+                 lambda: policy_loss(torch.zeros(2, 4), torch.zeros(2, dtype=torch.int64), x[:2], x[:2])):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_adamw_moments_decode_the_8_bit_states():
+    import torch
+    from oracle import training
+    from tiled_newton_schulz_tile_amd.adamw import adamw_moments, adamw_state
+    m, r, ms, rs = adamw_state(torch.zeros(300, 2), 8)
+    assert m.dtype == torch.float8_e4m3fn and m.shape == (300, 2) and ms.numel() == 3
+    g = torch.Generator().manual_seed(0)
+    code = torch.randint(0, 127, (600,), generator=g).to(torch.uint8)
+    m.view(torch.uint8).view(-1).copy_(code)
+    r.view(torch.uint8).view(-1).copy_(code.flip(0))
+    ms.copy_(torch.rand(3, generator=g))
+    rs.copy_(torch.rand(3, generator=g))
+    got = adamw_moments((m, r, ms, rs))
+    for x, c, s, square in ((got[0], code, ms, False), (got[1], code.flip(0), rs, True)):
+        want = training.unpack8(c.numpy(), s.double().numpy())
+        want = torch.from_numpy(want ** 2 if square else want).view(300, 2)
+        assert torch.allclose(x.double(), want, rtol=2.0 ** -22, atol=0)

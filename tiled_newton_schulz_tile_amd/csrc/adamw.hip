@@ -167,7 +167,7 @@ __device__ __forceinline__ float new_weight(float w, float m, float root, float 
 template <typename W, typename G, bool NT, class TABLE>
 __global__ __launch_bounds__(THREADS) void adamw32_kernel(TABLE tab, AdamWParams p) {
   const float scale = p.grad_scale ? *gmem(p.grad_scale) : 1.f;
-  const int c = blockIdx.x, ti = tensor_of(tab.firsts(), tab.n, c);
+  const int c = p.first_chunk + blockIdx.x, ti = tensor_of(tab.firsts(), tab.n, c);
   const Entry<32> &t = tab.entries()[ti];
   W *w = reinterpret_cast<W *>(t.w);
   const G *g = reinterpret_cast<const G *>(t.g);
@@ -197,8 +197,8 @@ __global__ __launch_bounds__(THREADS) void adamw32_kernel(TABLE tab, AdamWParams
 // a difference of a whole gap.  So the moments and codes are defined in fp32 with every
 // operation rounded on its own, in the order written here (no fused multiply-adds, the root
 // and the reciprocal correctly rounded): any other computation in that order gives the same
-// bits.  262 M elements, fp32 weights, bf16 gradients: 697 us (5.3 TB/s); with fused
-// multiply-adds and the hardware's root 674 us on the same card, in fp64 772 us.
+// bits.  262 M elements, fp32 weights, bf16 gradients: 587 us (6.3 TB/s), near both bounds (HBM,
+// and 350 VALU instructions a block of 256).
 constexpr int kBlock = HIMUON_ADAMW_BLOCK;
 static_assert(kBlock == 4 * 64, "a wave holds one block");
 constexpr unsigned kStepM = 0x9E3779B1u, kStepR = 0x85EBCA6Bu;   // of the dither sequences
@@ -221,8 +221,8 @@ __device__ __forceinline__ float wave_peak(f32x4 x) {
 }
 // The e4m3 code of x in units of the block's scale, rounded to a neighbouring value as the
 // dither says.  y 2^-120 is an fp32 number whose exponent field, three mantissa bits on, is the
-// e4m3 code of y: fp32's subnormals start at 2^-126 as e4m3's do at 2^-6, with 20 bits more.  A
-// dither of 16 bits and a half, added at the top of the 20 bits that are cut, carries up with
+// e4m3 code of y: fp32's subnormals (which the kernel's float mode keeps) start at 2^-126 as
+// e4m3's do at 2^-6, with 20 bits more.  A dither of 16 bits and a half, added at the top of the 20 bits that are cut, carries up with
 // the probability of the distance to the lower neighbour.
 // ROOT: x is a root, not negative; one that is not zero gets the smallest code at least.
 template <bool ROOT>
@@ -333,7 +333,7 @@ __device__ __forceinline__ void adamw8_block(const Entry<8> &t, int64_t b, float
 template <typename W, typename G, bool NT, class TABLE>
 __global__ __launch_bounds__(THREADS) void adamw8_kernel(TABLE tab, AdamWParams p) {
   const float scale = p.grad_scale ? *gmem(p.grad_scale) : 1.f;
-  const int c = blockIdx.x, ti = tensor_of(tab.firsts(), tab.n, c);
+  const int c = p.first_chunk + blockIdx.x, ti = tensor_of(tab.firsts(), tab.n, c);
   const Entry<8> &t = tab.entries()[ti];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t b = ((int64_t)(c - tab.firsts()[ti]) << kChunkShift) + wave * kBlock;
@@ -345,20 +345,30 @@ __global__ __launch_bounds__(THREADS) void adamw8_kernel(TABLE tab, AdamWParams 
 
 // A call that moves more than this goes past the caches: nothing of it is left there when the
 // next step comes, and its lines do not have to push others out.  Bytes of a call, cached
-// against non-temporal: 114 MB (8-bit states) 33.1 / 40.8 us, 250 MB (bf16, fp32 states)
-// 55.1 / 50.3 us, 3.7 GB 677 / 664 us, 6.8 GB 1231 / 1134 us.
+// against non-temporal (us): fp32 states 117 MB 18.7 / 21.6, 235 MB 46.1 / 41.3, 6.8 GB 1225 /
+// 1135; 8-bit 114 MB 29.0 / 35.2, 236 MB 45.7 / 41.3, 3.7 GB 617 / 591.
 constexpr double kCachedBytes = 128e6;
 
+// Chunks a launch: a grid holds fewer than 2^32 threads.
+constexpr int64_t kLaunchChunks = (int64_t)1 << 21;
+
 template <int BITS, typename W, typename G, class TABLE>
-void launch_typed(const TABLE &tab, unsigned chunks, bool nt, const AdamWParams &p, hipStream_t stream) {
-  const dim3 grid(chunks), block(THREADS);
-  if constexpr (BITS == 32) {
-    if (nt) hipLaunchKernelGGL((adamw32_kernel<W, G, true, TABLE>), grid, block, 0, stream, tab, p);
-    else hipLaunchKernelGGL((adamw32_kernel<W, G, false, TABLE>), grid, block, 0, stream, tab, p);
-  } else {
-    if (nt) hipLaunchKernelGGL((adamw8_kernel<W, G, true, TABLE>), grid, block, 0, stream, tab, p);
-    else hipLaunchKernelGGL((adamw8_kernel<W, G, false, TABLE>), grid, block, 0, stream, tab, p);
+hipError_t launch_typed(const TABLE &tab, int64_t chunks, bool nt, AdamWParams p, hipStream_t stream) {
+  const dim3 block(THREADS);
+  for (int64_t c = 0; c < chunks; c += kLaunchChunks) {
+    const dim3 grid((unsigned)(chunks - c < kLaunchChunks ? chunks - c : kLaunchChunks));
+    p.first_chunk = (int32_t)c;
+    if constexpr (BITS == 32) {
+      if (nt) hipLaunchKernelGGL((adamw32_kernel<W, G, true, TABLE>), grid, block, 0, stream, tab, p);
+      else hipLaunchKernelGGL((adamw32_kernel<W, G, false, TABLE>), grid, block, 0, stream, tab, p);
+    } else {
+      if (nt) hipLaunchKernelGGL((adamw8_kernel<W, G, true, TABLE>), grid, block, 0, stream, tab, p);
+      else hipLaunchKernelGGL((adamw8_kernel<W, G, false, TABLE>), grid, block, 0, stream, tab, p);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 // How a call is launched: its types, and whether it goes past the caches.
 struct Kind {
@@ -366,12 +376,11 @@ struct Kind {
 };
 template <int BITS, class TABLE>
 hipError_t launch_table(const TABLE &tab, int64_t chunks, Kind k, const AdamWParams &p, hipStream_t stream) {
-  const unsigned c = (unsigned)chunks;
-  if (k.weight_bf16 && k.grad_bf16) launch_typed<BITS, __bf16, __bf16>(tab, c, k.nt, p, stream);
-  else if (k.weight_bf16) launch_typed<BITS, __bf16, float>(tab, c, k.nt, p, stream);
-  else if (k.grad_bf16) launch_typed<BITS, float, __bf16>(tab, c, k.nt, p, stream);
-  else launch_typed<BITS, float, float>(tab, c, k.nt, p, stream);
-  return hipGetLastError();
+  if (k.weight_bf16)
+    return k.grad_bf16 ? launch_typed<BITS, __bf16, __bf16>(tab, chunks, k.nt, p, stream)
+                       : launch_typed<BITS, __bf16, float>(tab, chunks, k.nt, p, stream);
+  return k.grad_bf16 ? launch_typed<BITS, float, __bf16>(tab, chunks, k.nt, p, stream)
+                     : launch_typed<BITS, float, float>(tab, chunks, k.nt, p, stream);
 }
 
 int64_t chunks_of(int64_t n, int shift) { return (n + ((int64_t)1 << shift) - 1) >> shift; }

@@ -176,6 +176,7 @@ struct AdamWParams {
   float eps;
   float step;              // lr / (1 - beta1^t)
   float lr;
+  int32_t first_chunk;     // of a launch (set by it)
   uint32_t dither[2];
   const float *grad_scale; // device, or nullptr
 };

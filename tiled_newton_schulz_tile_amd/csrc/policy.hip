@@ -553,8 +553,7 @@ hipError_t launch_policy_t(const himuon_policy &c, const PolicyParams &p, hipStr
     return hipGetLastError();
   }
   const int out = !dz ? kForward : (double)c.rows * c.vocab * sizeof(T) > kL2Bytes ? kGradientNT : kGradient;
-  // (a grid's x extent holds 2^31 - 1 blocks; rows beyond go into further launches)
-  constexpr int64_t kRows = (int64_t)1 << 30;
+  constexpr int64_t kRows = (int64_t)1 << 21;   // a launch: a grid holds fewer than 2^32 threads
   for (int64_t r = 0; r < c.rows; r += kRows) {
     const unsigned rows = (unsigned)(c.rows - r < kRows ? c.rows - r : kRows);
     PolicyParams q = p;
