@@ -167,3 +167,50 @@ def test_example_learns_by_reward(bits):
     spec.loader.exec_module(mod)
     first, last = mod.train(steps=50, state_bits=bits, log=None)
     assert last > 2 * first
+
+
+def test_adamw_optimizer_follows_moved_parameters():
+    """A parameter whose storage is replaced between steps is updated where it is now."""
+    _need_gpu()
+    a, b = params(7), params(7)
+    x, y = AdamWOptimizer(a, lr=1e-2), AdamWOptimizer(b, lr=1e-2)
+    for step in range(4):
+        if step == 2:
+            old = a[1].data
+            a[1].data = old.clone()
+            old.fill_(5.0)
+        set_grads(a, step)
+        set_grads(b, step)
+        x.step()
+        y.step()
+    for p, q in zip(a, b):
+        assert torch.equal(p, q)
+    assert (old == 5).all()
+
+
+def test_adamw_set_grads_and_graphs():
+    """Gradients of a call with a device table are set before a graph is captured (inside, set_grads refuses and the
+    capture goes on); the replays take them."""
+    _need_gpu()
+    from tiled_newton_schulz_tile_amd.adamw import AdamW, adamw_state
+    sizes = [100 + k for k in range(20)]
+    g = torch.Generator().manual_seed(0)
+    W = [torch.randn(n, generator=g).to(DEV) for n in sizes]
+    V = [w.clone() for w in W]
+    G1, G2 = ([torch.randn(n, generator=g).to(DEV) for n in sizes] for _ in range(2))
+    sw, sv = [adamw_state(w) for w in W], [adamw_state(v) for v in V]
+    opt = AdamW([(w, x, *s) for w, x, s in zip(W, G1, sw)])
+    ref = AdamW([(v, x, *s) for v, x, s in zip(V, G2, sv)])
+    opt.set_grads(G2)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError):
+            opt.set_grads(G1)
+        opt.step(1e-2, 1)
+    for _ in range(3):
+        graph.replay()
+        ref.step(1e-2, 1)
+        torch.cuda.synchronize()
+        for w, v in zip(W, V):
+            assert torch.equal(w, v)

@@ -69,8 +69,9 @@ class AdamW:
     bfloat16), all G share one, and all states are of one kind.  weight_decay is one number
     or one per tensor.  The tensors are referenced, not copied; set_grads replaces the
     gradients (a training program whose gradients are new tensors each step).  For more
-    tensors than one launch takes in its arguments the descriptors are kept on the device;
-    set_grads and the steps after it then go on one stream."""
+    tensors than a small argument table takes (8) the descriptors are kept on the device;
+    set_grads and the steps after it then go on one stream.  A graph that captured its calls
+    needs the object, and its tensors, for as long as it is replayed."""
 
     def __init__(self, tensors, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0):
         import torch
@@ -125,6 +126,8 @@ class AdamW:
         """Replaces the gradients from the next step on (same dtype and sizes)."""
         torch = self._torch
         grads = tuple(grads)
+        if self._table is not None and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("set the gradients before the graph is captured: their table is copied from host memory")
         if len(grads) != len(self._n):
             raise ValueError("one gradient per tensor")
         size, at = _column(grads, "G", (self._grad_dtype,), self.device)
@@ -134,7 +137,7 @@ class AdamW:
         for c, p in zip(self._c, at):
             c.grad = p
         if self._table is not None:
-            host = torch.empty(self._table.numel() + 7, dtype=torch.uint8, pin_memory=True)
+            host = torch.empty(self._table.numel(), dtype=torch.uint8, pin_memory=True)
             himuon_adamw_table(self._c, self.cfg, host.data_ptr(), host.numel())
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
                 self._table.copy_(host[:self._table.numel()], non_blocking=True)

@@ -226,20 +226,23 @@ class AdamWOptimizer(torch.optim.Optimizer):
         if state_bits not in (32, 8):
             raise ValueError("state_bits must be 32 or 8")
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
-        for g in self.param_groups:
-            for p in g["params"]:
-                if p.dtype not in (torch.float32, torch.bfloat16) or not p.is_cuda or not p.is_contiguous():
-                    raise ValueError("parameters must be contiguous float32 or bfloat16 CUDA tensors")
         self.state_bits = state_bits
         self._random = random.Random(seed)
         self._engines = {}
 
+    def add_param_group(self, group):
+        super().add_param_group(group)
+        for p in self.param_groups[-1]["params"]:
+            if p.dtype not in (torch.float32, torch.bfloat16) or not p.is_cuda or not p.is_contiguous():
+                self.param_groups.pop()
+                raise ValueError("parameters must be contiguous float32 or bfloat16 CUDA tensors")
+
     def _engine(self, key, params, group):
-        """The AdamW over these parameters, kept while they and the group's constants stay the same."""
+        """The AdamW over these parameters, kept while they, their memory and the group's constants stay the same."""
         held = self._engines.get(key)
         constants = (group["betas"], group["eps"], group["weight_decay"])
         same = held is not None and held[1] == constants and len(held[2]) == len(params) and \
-            all(a is b for a, b in zip(held[2], params))
+            all(a is b and a.data_ptr() == c.weight for a, b, c in zip(params, held[2], held[0]._c))
         grads = [p.grad if p.grad.is_contiguous() else p.grad.contiguous() for p in params]
         if not same:
             held = (AdamW([(p.data, g, *self.state[p]["adamw"]) for p, g in zip(params, grads)], group["betas"],
