@@ -8,8 +8,12 @@ from __future__ import annotations
 
 from typing import NamedTuple, Optional
 
+import torch
+
 from . import BF16, F32, himuon_policy, himuon_policy_loss, himuon_policy_workspace
 from .adamw import _launch
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 class PolicyLoss(NamedTuple):
@@ -32,8 +36,7 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
     dlogits: True allocates the gradient, False or None computes the forward pass alone, a tensor of logits' shape
     and dtype receives it (`logits` itself: in place).  Everything runs on `stream` (the current stream by default);
     stats, logp and the workspace share one allocation of the call."""
-    import torch
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or not logits.is_cuda:
+    if logits.dim() != 2 or logits.dtype not in _DTYPES or not logits.is_cuda:
         raise ValueError("logits must be a 2-D float32 or bfloat16 CUDA tensor")
     N, V = logits.shape
     if V < 1:
@@ -54,9 +57,9 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
         raise ValueError("dlogits must have the shape, dtype and device of logits")
     p = himuon_policy(N, V, ld, _leading(dlogits, "dlogits", N, V) if dlogits is not None else 0, logits.data_ptr(),
                       dlogits.data_ptr() if dlogits is not None else None, *rows, None, None,
-                      F32 if logits.dtype is torch.float32 else BF16, clip[0], clip[1], kl_coef, temperature, grad_scale)
+                      _DTYPES[logits.dtype], clip[0], clip[1], kl_coef, temperature, grad_scale)
     need = himuon_policy_workspace(p)
-    buf = torch.empty(4 + need // 4 + N, dtype=torch.float32, device=dev)   # stats, workspace (whole words), logp
+    buf = torch.empty(4 + need // 4 + N, dtype=f32, device=dev)   # stats, workspace (whole words), logp
     base = buf.data_ptr()
     p.stats, p.logp = base, base + 16 + need
     if stream is not None:
@@ -64,11 +67,12 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
             if t is not None:
                 t.record_stream(stream)
     _launch(torch, dev, stream, himuon_policy_loss, p, base + 16, need)
-    return PolicyLoss(buf[:4], buf[4 + need // 4:], dlogits)
+    stats, _, logp = buf.split_with_sizes((4, need // 4, N))
+    return PolicyLoss(stats, logp, dlogits)
 
 
 def _row(t, dtype, N, dev, name):
-    if t is None or t.dtype is not dtype or t.device != dev or t.dim() != 1 or t.numel() != N or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.shape != (N,) or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {N} elements on {dev}")
     return t.data_ptr()
 
