@@ -294,7 +294,8 @@ HIMUON_API himuon_status himuon_sign_vote(const uint8_t *bits, int32_t workers, 
    A row whose weight is zero or whose label is outside [0, vocab) is left out: nothing of
    its logits, advantage or log probabilities is read, its logp is 0, its dlogits are 0 and
    it adds nothing to the sums.  Logits of -inf have probability 0; a row with NaN or +inf
-   among its logits, or with nothing but -inf, gives NaN.                               */
+   among its logits, or with nothing but -inf, gives NaN.  With kl_coef 0 the KL term is
+   only summed (stats[2]): it is no part of loss and gradient, infinite or not.          */
 typedef struct {
   int64_t rows, vocab;           /* >= 0, >= 1                                          */
   int64_t ld_logits, ld_dlogits; /* leading dimensions in elements, >= vocab            */

@@ -36,8 +36,9 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
             clipped = u > c
             surrogate = c if clipped else u
             logp[i] = lp
-            stats += w * np.array([kl_coef * kl - surrogate, -surrogate, kl, float(clipped)])
-            dlp = (0.0 if clipped else -u) - kl_coef * np.expm1(d)
+            count = (kl_coef * kl, kl_coef * np.expm1(d)) if kl_coef else (0.0, 0.0)
+            stats += w * np.array([count[0] - surrogate, -surrogate, kl, float(clipped)])
+            dlp = (0.0 if clipped else -u) - count[1]
             grad[i] = -dlp * (e / e.sum())
             grad[i, y] += dlp
             grad[i] *= grad_scale * w / temperature

@@ -476,3 +476,18 @@ def test_grad_norm_of_nothing():
     _need_gpu()
     got = GradNorm([torch.zeros(0, device=DEV), torch.zeros(0, device=DEV)]).compute(0.5)
     assert got.tolist() == [0.0, 1.0]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_subnormal_second_moments(bits):
+    """Gradients whose squares are subnormal in fp32, and an eps below their roots: the first step is lr times the
+    sign, as the formula says, within what a subnormal of 2^-149's multiples resolves: v = 1e-3 g^2 lies within 1 %
+    of a multiple of 2^-149 for these g, so its root is within 1 %."""
+    _need_gpu()
+    unit = 2.0 ** -149
+    v = torch.arange(100, 1124, dtype=torch.float64) * unit
+    G = torch.sqrt(v / (1 - 0.999)).float().to(DEV)
+    W = torch.zeros(1024, device=DEV)
+    state = adamw_state(W, bits)
+    AdamW([(W, G, *state)], eps=1e-30).step(1e-2, 1, dither=(1, 2))
+    assert ((W + 1e-2).abs() <= 1e-2 * 0.01).all()

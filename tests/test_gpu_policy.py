@@ -365,3 +365,19 @@ def test_policy_more_rows_than_a_launch_holds():
         assert torch.equal(one.logp, got.logp[part]) and torch.equal(one.dlogits, got.dlogits[part])
     live = label >= 0
     assert abs(float(got.stats[1]) + float((weight * adv)[live].double().sum())) <= 1e-6 * float((weight * adv.abs())[live].sum())
+
+
+@pytest.mark.parametrize("N,V", [(4, 500), (4, 40000), (140, 40000), (140, 140001)])
+def test_policy_infinite_kl_that_does_not_count(N, V):
+    """A sampled token that the policy now gives probability 0: with kl_coef 0 the KL sum is infinite, the loss and
+    the gradient are not."""
+    _need_gpu()
+    logits, rest = make(N, V, torch.float32, 31, masked=0.0)
+    label, weight, adv, old, ref = rest
+    logits[0, label[0]] = float("-inf")
+    ref[1] = 500.0                          # exp(ref - lp) past fp32
+    got = policy_loss(logits, label, weight, adv, old, ref)
+    assert torch.isfinite(got.stats[[0, 1, 3]]).all() and not torch.isfinite(got.stats[2])
+    assert torch.isfinite(got.dlogits).all() and got.logp[0] == float("-inf")
+    want = policy_loss(logits, label, weight, adv, old)
+    assert torch.equal(got.dlogits, want.dlogits) and torch.equal(got.stats[:2], want.stats[:2])

@@ -158,7 +158,9 @@ __device__ __forceinline__ int tensor_of(const int32_t *first, int n, int c) {
 
 // ------------------------------------------------------------------ AdamW
 // The weight after a step with the new first moment and the root of the new second one.  The
-// hardware's root and reciprocal are within an ulp each, far inside what the step needs.
+// hardware's reciprocal is within an ulp, far inside what the step needs, and its argument is
+// eps at least, a normal number.  (The hardware's root takes subnormals for zero, and so would
+// let a tiny eps divide: the rounded root is used.)
 __device__ __forceinline__ float new_weight(float w, float m, float root, float decay, const AdamWParams &p) {
   const float den = __builtin_fmaf(root, p.root_scale, p.eps);
   return __builtin_fmaf(w, decay, -p.step * (m * __builtin_amdgcn_rcpf(den)));
@@ -184,7 +186,7 @@ __global__ __launch_bounds__(THREADS) void adamw32_kernel(TABLE tab, AdamWParams
     const float x = gv[e] * scale;
     mv[e] = __builtin_fmaf(p.beta1, mv[e], p.omb1 * x);
     vv[e] = __builtin_fmaf(p.beta2, vv[e], p.omb2 * x * x);
-    wv[e] = new_weight(wv[e], mv[e], __builtin_amdgcn_sqrtf(vv[e]), decay, p);
+    wv[e] = new_weight(wv[e], mv[e], __builtin_sqrtf(vv[e]), decay, p);
   }
   store_upto4<NT>(m, i, n, mv);
   store_upto4<NT>(v, i, n, vv);

@@ -138,7 +138,8 @@ __device__ __forceinline__ RowTerms row_terms(Softmax s, const RowIn &r, const P
   const float d = p.ref_logp ? r.ref_logp - lp : 0.f;
   const float em1 = p.ref_logp ? expm1f(d) : 0.f;
   const bool clipped = u > c;
-  return {lp, ((clipped ? 0.f : -u) - p.kl_coef * em1) * r.w * p.grad_scale * p.inv_temp,
+  const float kl_part = p.kl_coef != 0.f ? p.kl_coef * em1 : 0.f;   // (an infinite KL that does not count)
+  return {lp, ((clipped ? 0.f : -u) - kl_part) * r.w * p.grad_scale * p.inv_temp,
           f32x4{r.w * -(clipped ? c : u), r.w * (em1 - d), clipped ? r.w : 0.f, 0.f}};
 }
 __device__ __forceinline__ void write_terms(float lp, f32x4 part, int64_t row, const PolicyParams &p) {
@@ -340,7 +341,7 @@ __device__ __forceinline__ void write_stats(const double (&mine)[3], float kl_co
   for (int i = 0; i < W; ++i)
 #pragma unroll
     for (int k = 0; k < 3; ++k) t[k] += lds[i][k];
-  gmem(stats)[0] = (float)(t[0] + (double)kl_coef * t[1]);
+  gmem(stats)[0] = (float)(kl_coef != 0.f ? t[0] + (double)kl_coef * t[1] : t[0]);
 #pragma unroll
   for (int k = 0; k < 3; ++k) gmem(stats)[1 + k] = (float)t[k];
 }
