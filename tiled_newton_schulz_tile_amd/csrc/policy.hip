@@ -174,14 +174,19 @@ __device__ __forceinline__ float max_of(u32x4 v, float m) {
   for (int e = 0; e < Vec<T>::N; ++e) m = __builtin_fmaxf(m, x[e]);
   return m;
 }
+// (by pairs: as many additions, fewer roundings of a sum that one power has already made large)
 template <class T>
 __device__ __forceinline__ float sum_of(u32x4 v, float k, float ref) {
-  float x[Vec<T>::N];
+  constexpr int N = Vec<T>::N;
+  float x[N];
   Vec<T>::unpack(v, x);
-  float s = 0.f;
 #pragma unroll
-  for (int e = 0; e < Vec<T>::N; ++e) s += pow2(x[e], k, ref);
-  return s;
+  for (int e = 0; e < N; ++e) x[e] = pow2(x[e], k, ref);
+#pragma unroll
+  for (int d = 1; d < N; d *= 2)
+#pragma unroll
+    for (int e = 0; e < N; e += 2 * d) x[e] += x[e + d];
+  return x[0];
 }
 // A vector of the gradient: coef ((j == label) - p_j), f = -coef / sum.
 template <class T, bool NT>
