@@ -27,8 +27,12 @@ def _column(tensors, name, dtypes, device):
 
 def _launch(torch, device, stream, call, *args):
     """call(*args, stream) with `device` the current one, as the library needs it.  The current stream is asked for
-    by its raw handle: a call of a few microseconds should not spend two on a Stream object."""
-    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    by its raw handle where torch gives it: a call of a few microseconds should not spend two on a Stream object."""
+    if stream is not None:
+        s = stream.cuda_stream
+    else:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        s = raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
     if torch.cuda.current_device() == device.index:
         call(*args, s)
     else:
