@@ -271,8 +271,8 @@ __global__ __launch_bounds__(THR) void policy_row_kernel(const T *logits, T *dlo
 // are read again for the gradient, in the reverse order, mostly from the last-level cache
 // (one block of 1024 threads a CU keeps the rows in flight below its 256 MB).  The forward
 // pass alone holds nothing and runs two blocks a CU.  1000 fp32 rows of 128256, 1 in 5 left
-// out: gradient 212 us held (4.35 TB/s of what has to move), 263 us with every vector read
-// twice; forward 90 us held, 78 us streamed.
+// out: gradient 212 us held, 263 us with every vector read twice (193 us with the stores past
+// the L2s, 4.8 TB/s of what has to move); forward 90 us held, 78 us streamed.
 constexpr int kLongThreads = 1024;
 template <int OUT>
 constexpr int kLongK = OUT != kForward ? 16 : 0;
