@@ -83,7 +83,8 @@ struct PolicyParams {
   const float *weight, *advantage, *old_logp, *ref_logp;
   float *logp;
   f32x4 *part;        // workspace: per row, weight times (-min(u, c), kl, clipped, 0)
-  f32x2 *spans;       // workspace: per row and span, the span's largest logit and its sum
+  f32x2 *spans;       // workspace, of rows that are cut into spans instead: per row and span, the span's
+                      // largest logit and its sum; then the row's label's logit
   int64_t ld_logits, ld_dlogits;
   int32_t vocab;
   float k;            // log2(e) / temperature
@@ -107,8 +108,7 @@ struct RowIn {
   float w, adv, old, ref_logp, zy;
   int32_t label;   // -1: the row is left out
 };
-template <class T>
-__device__ __forceinline__ RowIn row_in(const T *z, int64_t row, const PolicyParams &p) {
+__device__ __forceinline__ RowIn row_scalars(int64_t row, const PolicyParams &p) {   // all but zy
   RowIn r;
   r.w = gmem(p.weight)[row];
   const int64_t y = gmem(p.label)[row];
@@ -117,7 +117,12 @@ __device__ __forceinline__ RowIn row_in(const T *z, int64_t row, const PolicyPar
   r.adv = gmem(p.advantage)[row];
   r.old = p.old_logp ? gmem(p.old_logp)[row] : 0.f;
   r.ref_logp = p.ref_logp ? gmem(p.ref_logp)[row] : 0.f;
-  r.zy = Vec<T>::load1(z + r.label);
+  return r;
+}
+template <class T>
+__device__ __forceinline__ RowIn row_in(const T *z, int64_t row, const PolicyParams &p) {
+  RowIn r = row_scalars(row, p);
+  if (r.label >= 0) r.zy = Vec<T>::load1(z + r.label);
   return r;
 }
 
@@ -372,9 +377,12 @@ __global__ __launch_bounds__(1024) void policy_join_kernel(const f32x4 *part, in
 
 // Few long rows: a row's vectors are cut into spans of kSpanVecs, one block each, so that a
 // handful of rows still occupies the whole chip.  The first kernel leaves each span's largest
-// logit and sum; in the second one every block joins its row's spans (one per lane and turn)
-// and writes its span of the gradient, and one block more computes the rows' terms and stats.
-// The span of a row's last V % N elements is its last one.
+// logit and sum, and the row's label's logit; in the second one every block joins its row's
+// spans (one per lane and turn) and writes its span of the gradient, and one block more computes
+// the rows' terms and stats.  The span of a row's last V % N elements is its last one.
+// A gradient may be written over its logits, and the second kernel's blocks run in any order: no
+// block of it reads a logit outside its own span, so the label's logit comes from the first.  It
+// stands behind the spans, where a join's loads reach it in the same turn.
 constexpr int kSpanThreads = 256, kSpanK = 4, kSpanVecs = kSpanThreads * kSpanK;
 constexpr int64_t span_count(int64_t vecs) { return vecs < 1 ? 1 : (vecs + kSpanVecs - 1) / kSpanVecs; }
 
@@ -386,7 +394,9 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_kernel(const T *logi
   const int tid = threadIdx.x, V = p.vocab, vecs = V / N, v0 = blockIdx.x * kSpanVecs, rest = vecs * N + tid;
   const T *z = logits + row * p.ld_logits;
   const float w = gmem(p.weight)[row];
-  if (w == 0.f) return;   // (a label out of range leaves a span that nobody reads)
+  const int64_t y = gmem(p.label)[row];
+  if (!(w != 0.f && y >= 0 && y < V)) return;
+  const float zy = Vec<T>::load1(z + y);   // (by every block: a branch would wait for it before the vectors)
   u32x4 v[kSpanK];
 #pragma unroll
   for (int i = 0; i < kSpanK; ++i) {
@@ -405,31 +415,43 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_kernel(const T *logi
   for (int i = 0; i < kSpanK; ++i) sum += sum_of<T>(v[i], p.k, ref);
   const Softmax s = block_softmax<THR / 64>(m, sum, p.k, lds);
   // (a span of nothing but -inf has ref 0 and sum 0: its largest logit is -inf)
-  if (tid == 0) gmem(p.spans)[row * gridDim.x + blockIdx.x] = f32x2{s.sum == 0.f ? -__builtin_inff() : s.ref, s.sum};
+  if (tid == 0) {
+    f32x2 *out = p.spans + row * (gridDim.x + 1);
+    gmem(out)[blockIdx.x] = f32x2{s.sum == 0.f ? -__builtin_inff() : s.ref, s.sum};
+    if (blockIdx.x == 0) gmem(out)[gridDim.x] = f32x2{zy, 0.f};
+  }
 }
 
-// A row's softmax from its spans; every lane of a wave calls it.
-__device__ __forceinline__ Softmax join_spans(const f32x2 *spans, int n, float k) {
+// A row's softmax from its n spans (1 at least), and its label's logit; every lane of a wave
+// calls it.
+__device__ __forceinline__ Softmax join_spans(const f32x2 *spans, int n, float k, float &label_logit) {
   const int lane = threadIdx.x & 63;
   Softmax s = {0.f, 0.f};
   float top = -__builtin_inff();
-  for (int i = 0; i < n; i += 64) {
+  int i = 0;
+  do {   // (with a loop of no turn the compiler waits for the caller's vectors again between their stores: 0.5 us)
     f32x2 x = {-__builtin_inff(), 0.f};
-    if (i + lane < n) x = gmem(spans)[i + lane];
+    if (i + lane <= n) x = gmem(spans)[i + lane];
+    if (n - i < 64) {
+      label_logit = __shfl(x[0], n - i);
+      if (i + lane == n) x = f32x2{-__builtin_inff(), 0.f};
+    }
     const float m = __builtin_fmaxf(top, wave_max(x[0])), to = ref_of(m);
     const float part = wave_sum(x[1] * pow2(x[0], k, to));
     s.sum = (s.sum > 0.f ? s.sum * pow2(s.ref, k, to) : s.sum) + part;
     s.ref = to;
     top = m;
-  }
+    i += 64;
+  } while (i <= n);
   return s;
 }
 
 // The same for a row on four neighbouring lanes, so that one block takes 64 rows at a time:
 // each lane joins every fourth span, eight loads in flight, and the four are joined.
 constexpr int kRowLanes = 4;
-__device__ __forceinline__ Softmax join_spans_quad(const f32x2 *spans, int n, float k) {
+__device__ __forceinline__ Softmax join_spans_quad(const f32x2 *spans, int n, float k, float &label_logit) {
   constexpr int U = 8;
+  label_logit = gmem(spans)[n][0];
   float top = -__builtin_inff();
   Softmax s = {0.f, 0.f};
   for (int i = threadIdx.x % kRowLanes; i < n; i += kRowLanes * U) {
@@ -469,9 +491,12 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_finish_kernel(const 
     if (blockIdx.x != 0) return;
     double sum[3] = {0, 0, 0};
     for (int row = tid / kRowLanes; row < rows; row += THR / kRowLanes) {
-      const RowIn r = row_in(logits + row * p.ld_logits, row, p);
+      RowIn r = row_scalars(row, p);
       RowTerms t = {0.f, 0.f, f32x4{0.f, 0.f, 0.f, 0.f}};
-      if (r.label >= 0) t = row_terms(join_spans_quad(p.spans + (int64_t)row * spans, spans, p.k), r, p);
+      if (r.label >= 0) {
+        const Softmax s = join_spans_quad(p.spans + (int64_t)row * (spans + 1), spans, p.k, r.zy);
+        t = row_terms(s, r, p);
+      }
       if (tid % kRowLanes == 0) {
         gmem(p.logp)[row] = t.lp;
 #pragma unroll
@@ -486,7 +511,7 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_finish_kernel(const 
   const bool has_rest = (int)blockIdx.x == spans - 1 && rest < V;
   const T *z = logits + row * p.ld_logits;
   T *dz = dlogits + row * p.ld_dlogits;
-  const RowIn r = row_in(z, row, p);
+  RowIn r = row_scalars(row, p);
   if (r.label < 0) {
     const float zero[N] = {};
 #pragma unroll
@@ -505,7 +530,7 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_finish_kernel(const 
     if (at < vecs) v[i] = Vec<T>::load(z + (int64_t)at * N);
   }
   const float tail = has_rest ? Vec<T>::load1(z + rest) : 0.f;
-  const Softmax s = join_spans(p.spans + row * spans, spans, p.k);
+  const Softmax s = join_spans(p.spans + row * (spans + 1), spans, p.k, r.zy);
   const float coef = row_terms(s, r, p).coef, f = -coef / s.sum;
 #pragma unroll
   for (int i = 0; i < kSpanK; ++i) {
@@ -588,10 +613,10 @@ hipError_t launch_policy_t(const himuon_policy &c, const PolicyParams &p, hipStr
 
 }  // namespace
 
-// The rows' terms, then the spans of few long rows.
+// The spans of few long rows and their labels' logits, or the rows' terms.
 size_t policy_workspace(const himuon_policy &p) {
   const int64_t vecs = p.vocab / (p.dtype == HIMUON_BF16 ? 8 : 4);
-  return (size_t)p.rows * (sizeof(f32x4) + (few_rows(p.rows, vecs) ? span_count(vecs) * sizeof(f32x2) : 0));
+  return (size_t)p.rows * (few_rows(p.rows, vecs) ? (span_count(vecs) + 1) * sizeof(f32x2) : sizeof(f32x4));
 }
 
 hipError_t launch_policy(const himuon_policy &c, void *workspace, hipStream_t stream) {
@@ -603,7 +628,7 @@ hipError_t launch_policy(const himuon_policy &c, void *workspace, hipStream_t st
   p.ref_logp = c.ref_logp;
   p.logp = c.logp;
   p.part = reinterpret_cast<f32x4 *>(workspace);
-  p.spans = reinterpret_cast<f32x2 *>(p.part + c.rows);
+  p.spans = reinterpret_cast<f32x2 *>(workspace);
   p.ld_logits = c.ld_logits;
   p.ld_dlogits = c.ld_dlogits;
   p.vocab = (int32_t)c.vocab;
