@@ -1,10 +1,12 @@
 """Calls of the training step's operators at the edges of what their documentation allows
-(MI355X only): gradients in the place of the logits for many blocks a row."""
+(MI355X only): gradients in the place of the logits for many blocks a row, and calls on
+another stream than the current one."""
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
 hm = pytest.importorskip("tiled_newton_schulz_tile_amd")
+from tiled_newton_schulz_tile_amd.adamw import GradNorm  # noqa: E402
 from tiled_newton_schulz_tile_amd.policy import policy_loss  # noqa: E402
 
 DEV = "cuda"
@@ -42,3 +44,56 @@ def test_policy_few_rows_in_place_equal_their_own_buffer(N, V, dtype):
     got = policy_loss(z, *rest, dlogits=z, **kw)
     assert torch.equal(got.logp, want.logp) and torch.equal(got.stats, want.stats)
     assert torch.equal(z, want.dlogits)
+
+
+def pool_stream(t):
+    """The stream whose pool of torch's allocator a tensor's memory belongs to."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not torch's memory")
+
+
+def reused(nbytes, ptr):
+    """Whether one of the next allocations of that many bytes on the current stream gets the address `ptr`."""
+    held = [torch.empty(nbytes, dtype=torch.uint8, device=DEV) for _ in range(8)]
+    return any(t.data_ptr() == ptr for t in held)
+
+
+def test_results_belong_to_the_stream_that_writes_them():
+    """Memory of the current stream's pool may still be used by kernels pending there: what a call on another stream
+    writes is allocated on that one."""
+    _need_gpu()
+    logits, rest = policy_inputs(12, 1001, F32, 1)
+    G = torch.randn(1000, device=DEV)
+    norm = GradNorm([G])
+    want, n = policy_loss(logits, *rest), norm.compute(1.0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got, m = policy_loss(logits, *rest, stream=s), norm.compute(1.0, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    for t in (got.stats, got.logp, got.dlogits, m):
+        assert pool_stream(t) == s.cuda_stream
+    for t in (want.stats, want.dlogits, n):
+        assert pool_stream(t) == torch.cuda.current_stream().cuda_stream
+    for x, y in zip((*got, m), (*want, n)):
+        assert torch.equal(x, y)
+
+
+def test_policy_arguments_outlive_a_call_on_another_stream():
+    """Logits that the caller lets go of while a call on another stream has yet to read them are not handed out."""
+    _need_gpu()
+    logits, rest = policy_inputs(32, 40000, F32, 2)
+    want = policy_loss(logits, *rest)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    z = logits.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    got = policy_loss(z, *rest, stream=s)
+    ptr, nbytes = z.data_ptr(), z.numel() * 4
+    del z
+    assert not reused(nbytes, ptr)
+    torch.cuda.synchronize()
+    assert torch.equal(got.dlogits, want.dlogits) and torch.equal(got.stats, want.stats)

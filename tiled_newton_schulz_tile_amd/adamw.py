@@ -40,6 +40,18 @@ def _launch(torch, device, stream, call, *args):
             call(*args, s)
 
 
+def _empty(torch, stream, size, dtype, device):
+    """A new tensor that work on `stream` (None: the current one) may write at once.  One of the current stream's
+    pool may be memory that kernels still pending there use; a tensor of another stream's pool is recorded on the
+    current one, whose work will read it."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(size, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def adamw_state(W, bits: int = 32):
     """Zero states of parameter W as AdamW takes them: (m, v) in float32, or with bits=8
     (m, r, m_scale, r_scale) with e4m3 values and one float32 scale per 256 elements."""
@@ -199,13 +211,11 @@ class GradNorm:
     def compute(self, max_norm: float, out=None, stream=None):
         """A float32 CUDA tensor (norm, factor): the 2-norm over all tensors and min(1, max_norm / (norm + 1e-6)),
         NaN where the gradient is not finite.  out: a tensor of two elements to write to instead of a new one
-        (allocated on the current stream).  Calls of one GradNorm share its workspace: they go on one stream, or
+        (allocated on the stream of the call).  Calls of one GradNorm share its workspace: they go on one stream, or
         the caller orders them."""
         torch = self._torch
         if out is None:
-            out = torch.empty(2, dtype=torch.float32, device=self.device)
-            if stream is not None:
-                out.record_stream(stream)
+            out = _empty(torch, stream, (2,), torch.float32, self.device)
         elif out.dtype != torch.float32 or out.shape != (2,) or out.device != self.device or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous float32 tensor of two elements on {self.device}")
         _launch(torch, self.device, stream, himuon_grad_norm, self._c, self._dt, max_norm, out.data_ptr(),

@@ -11,7 +11,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import BF16, F32, himuon_policy, himuon_policy_loss, himuon_policy_workspace
-from .adamw import _launch
+from .adamw import _empty, _launch
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -34,8 +34,9 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
     label: int64 (N); weight, advantage, old_logp, ref_logp: float32 (N).  A row with weight 0 or a label outside
     [0, V) is left out.  old_logp None: the ratio is 1; ref_logp None: no KL term.  clip: the pair (low, high).
     dlogits: True allocates the gradient, False or None computes the forward pass alone, a tensor of logits' shape
-    and dtype receives it (`logits` itself: in place).  Everything runs on `stream` (the current stream by default);
-    stats, logp and the workspace share one allocation of the call."""
+    and dtype receives it (`logits` itself: in place).  Everything runs on `stream` (the current stream by default),
+    whose work has to come after what made the arguments; stats, logp and the workspace share one allocation of the
+    call.  With a `stream`, results are allocated on it and arguments are recorded on it (torch's record_stream)."""
     if logits.dim() != 2 or logits.dtype not in _DTYPES or not logits.is_cuda:
         raise ValueError("logits must be a 2-D float32 or bfloat16 CUDA tensor")
     N, V = logits.shape
@@ -49,7 +50,7 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
             0 if old_logp is None else _row(old_logp, f32, N, dev, "old_logp"),
             0 if ref_logp is None else _row(ref_logp, f32, N, dev, "ref_logp"))
     if dlogits is True:
-        dlogits = torch.empty(N, V, dtype=logits.dtype, device=dev)
+        dlogits = _empty(torch, stream, (N, V), logits.dtype, dev)
     elif dlogits is False:
         dlogits = None
     elif dlogits is not None and (dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype or
@@ -59,11 +60,11 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
                       dlogits.data_ptr() if dlogits is not None else None, *rows, None, None,
                       _DTYPES[logits.dtype], clip[0], clip[1], kl_coef, temperature, grad_scale)
     need = himuon_policy_workspace(p)
-    buf = torch.empty(4 + need // 4 + N, dtype=f32, device=dev)   # stats, workspace (whole words), logp
+    buf = _empty(torch, stream, (4 + need // 4 + N,), f32, dev)   # stats, workspace (whole words), logp
     base = buf.data_ptr()
     p.stats, p.logp = base, base + 16 + need
     if stream is not None:
-        for t in (buf, dlogits):
+        for t in (logits, label, weight, advantage, old_logp, ref_logp, dlogits):
             if t is not None:
                 t.record_stream(stream)
     _launch(torch, dev, stream, himuon_policy_loss, p, base + 16, need)
