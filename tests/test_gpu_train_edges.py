@@ -6,7 +6,7 @@ import torch
 
 pytestmark = pytest.mark.gpu
 hm = pytest.importorskip("tiled_newton_schulz_tile_amd")
-from tiled_newton_schulz_tile_amd.adamw import GradNorm  # noqa: E402
+from tiled_newton_schulz_tile_amd.adamw import AdamW, GradNorm, adamw_state  # noqa: E402
 from tiled_newton_schulz_tile_amd.policy import policy_loss  # noqa: E402
 
 DEV = "cuda"
@@ -97,3 +97,43 @@ def test_policy_arguments_outlive_a_call_on_another_stream():
     assert not reused(nbytes, ptr)
     torch.cuda.synchronize()
     assert torch.equal(got.dlogits, want.dlogits) and torch.equal(got.stats, want.stats)
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_descriptors_and_workspaces_outlive_steps_on_another_stream(given):
+    """The device table of an AdamW, the workspace of a GradNorm and gradients that were replaced, all made on one
+    stream and let go of while work on another has yet to read them, are not handed out; given: the stream is an
+    argument, or the current one at the call."""
+    _need_gpu()
+    sizes = [1000 + k for k in range(20)]
+    W = [torch.randn(n, device=DEV) for n in sizes]
+    G = [torch.randn(n, device=DEV) for n in sizes]
+    V, sw, sv = [w.clone() for w in W], [adamw_state(w) for w in W], [adamw_state(w) for w in W]
+    AdamW([(v, g, *t) for v, g, t in zip(V, G, sv)]).step(1e-2, 1)
+    want = GradNorm(G).compute(1.0)
+    old = [g.clone() for g in G]
+    opt, norm = AdamW([(w, g, *t) for w, g, t in zip(W, old, sw)]), GradNorm(old)
+    table, ws = opt._table.data_ptr(), norm._ws.data_ptr()
+    sizes_of = opt._table.numel(), norm._ws.numel()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        if not given:
+            opt.step(1e-2, 1)
+            got = norm.compute(1.0)
+    if given:
+        opt.step(1e-2, 1, stream=s)
+        got = norm.compute(1.0, stream=s)
+    last = [g.data_ptr() for g in old[-2:]]
+    opt.set_grads([*old[:-1], G[-1]], stream=s)   # (for the next step there)
+    norm.set_grads([*old[:-1], G[-1]])
+    del old
+    assert not reused(sizes[-1] * 4, last[1])
+    del opt, norm
+    assert not reused(sizes[-2] * 4, last[0])
+    assert not reused(sizes_of[0], table) and not reused(sizes_of[1], ws)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    for w, v in zip(W, V):
+        assert torch.equal(w, v)

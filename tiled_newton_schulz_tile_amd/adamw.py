@@ -26,8 +26,9 @@ def _column(tensors, name, dtypes, device):
 
 
 def _launch(torch, device, stream, call, *args):
-    """call(*args, stream) with `device` the current one, as the library needs it.  The current stream is asked for
-    by its raw handle where torch gives it: a call of a few microseconds should not spend two on a Stream object."""
+    """call(*args, stream) with `device` the current one, as the library needs it; returns the stream's handle.  The
+    current stream is asked for by its raw handle where torch gives it: a call of a few microseconds should not spend
+    two on a Stream object."""
     if stream is not None:
         s = stream.cuda_stream
     else:
@@ -38,17 +39,47 @@ def _launch(torch, device, stream, call, *args):
     else:
         with torch.cuda.device(device):
             call(*args, s)
+    return s
 
 
-def _empty(torch, stream, size, dtype, device):
-    """A new tensor that work on `stream` (None: the current one) may write at once.  One of the current stream's
-    pool may be memory that kernels still pending there use; a tensor of another stream's pool is recorded on the
-    current one, whose work will read it."""
-    if stream is None:
-        return torch.empty(size, dtype=dtype, device=device)
+class _Streams:
+    """The streams, besides the one that an object was made on, that its calls went to: memory that the object lets
+    go of has to wait for them."""
+
+    def _made(self, memory):
+        """memory: the object's own tensor on the device, or None."""
+        self._own, self._abroad = memory, []
+        self._home = self._torch.cuda.current_stream(self.device).cuda_stream
+
+    def _went_abroad(self, stream):
+        """A call went to `stream` (None: the current one), whose handle is not self._home."""
+        if stream is None:
+            stream = self._torch.cuda.current_stream(self.device)
+        if self._own is not None:
+            self._own.record_stream(stream)
+        if stream not in self._abroad:
+            self._abroad.append(stream)
+
+    def _let_go(self, tensors):
+        for stream in self._abroad:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def __del__(self):
+        try:
+            self._let_go(self._held())
+        except Exception:   # not made, or the interpreter ends
+            pass
+
+
+def _empty(torch, stream, size, dtype):
+    """A new tensor that work on `stream` may write at once.  One of the current stream's pool may be memory that
+    kernels still pending there use; this one is of `stream`'s own, recorded on the current one, whose work will
+    read it."""
     with torch.cuda.stream(stream):
-        t = torch.empty(size, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
+        t = torch.empty(size, dtype=dtype, device=stream.device)
+    t.record_stream(torch.cuda.current_stream(stream.device))
     return t
 
 
@@ -77,7 +108,7 @@ def adamw_moments(state):
     return out[0], out[1].square()
 
 
-class AdamW:
+class AdamW(_Streams):
     """AdamW over a list of contiguous CUDA tensors.
 
     tensors: list of (W, G, m, v) with float32 states, or of (W, G, m, r, m_scale, r_scale)
@@ -129,6 +160,7 @@ class AdamW:
         self.cfg = himuon_adamw_config(dt(cols[0][0]), dt(cols[1][0]), self.bits, betas[0], betas[1], eps)
         size = himuon_adamw_table_size(self._c, self.cfg)
         self._table = torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
+        self._made(self._table)
         if size:
             host = array("Q", bytes(-(-size // 8) * 8))
             himuon_adamw_table(self._c, self.cfg, host.buffer_info()[0], size)
@@ -137,6 +169,9 @@ class AdamW:
     @property
     def tensors(self):
         return list(zip(*self._tensors))
+
+    def _held(self):
+        return [t for col in self._tensors for t in col]
 
     def set_grads(self, grads, stream=None) -> None:
         """Replaces the gradients from the next step on (same dtype and sizes)."""
@@ -149,6 +184,7 @@ class AdamW:
         size, at = _column(grads, "G", (self._grad_dtype,), self.device)
         if size != self._n:
             raise ValueError("a gradient must have its weight's number of elements")
+        self._let_go(self._tensors[1])
         self._tensors[1] = grads
         for c, p in zip(self._c, at):
             c.grad = p
@@ -157,10 +193,13 @@ class AdamW:
             himuon_adamw_table(self._c, self.cfg, host.data_ptr(), host.numel())
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
                 self._table.copy_(host[:self._table.numel()], non_blocking=True)
+            if (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream != self._home:
+                self._went_abroad(stream)
 
     def drop_grads(self) -> None:
         """Forgets the gradients, so that their memory may go; set_grads gives the next step's, unless those are at
         the same addresses."""
+        self._let_go(self._tensors[1])
         self._tensors[1] = (None,) * len(self._n)
 
     def step(self, lr: float, t: int, scale=None, dither=None, stream=None) -> None:
@@ -173,11 +212,12 @@ class AdamW:
             if scale.dtype != torch.float32 or scale.device != self.device or scale.numel() < 1:
                 raise ValueError(f"scale must be a float32 tensor on {self.device}")
             at = scale.data_ptr()
-        _launch(torch, self.device, stream, himuon_adamw_step, self._c, self.cfg, t, lr, at, dither,
-                self._table.data_ptr() if self._table is not None else 0)
+        if _launch(torch, self.device, stream, himuon_adamw_step, self._c, self.cfg, t, lr, at, dither,
+                   self._table.data_ptr() if self._table is not None else 0) != self._home:
+            self._went_abroad(stream)
 
 
-class GradNorm:
+class GradNorm(_Streams):
     """Norm and clip factor of a list of contiguous CUDA tensors of one dtype (float32 or bfloat16)."""
 
     def __init__(self, grads):
@@ -194,7 +234,11 @@ class GradNorm:
         self._dtypes = (grads[0].dtype,)
         self._dt = F32 if grads[0].dtype == torch.float32 else BF16
         self._ws = torch.zeros(himuon_grad_norm_workspace(len(grads)), dtype=torch.uint8, device=self.device)
+        self._made(self._ws)
         torch.cuda.current_stream(self.device).synchronize()   # the zeros are there for a call on any stream
+
+    def _held(self):
+        return self.grads
 
     def set_grads(self, grads) -> None:
         """Replaces the tensors (as many as before, of the same dtype)."""
@@ -205,6 +249,8 @@ class GradNorm:
         words = array("Q")
         for row in zip(n, at):
             words.extend(row)
+        if self._c is not None:
+            self._let_go(self.grads)
         self._words, self.grads = words, grads
         self._c = (himuon_grad * len(n)).from_buffer(words)
 
@@ -215,9 +261,13 @@ class GradNorm:
         the caller orders them."""
         torch = self._torch
         if out is None:
-            out = _empty(torch, stream, (2,), torch.float32, self.device)
+            if stream is None:
+                out = torch.empty(2, dtype=torch.float32, device=self.device)
+            else:
+                out = _empty(torch, stream, (2,), torch.float32)
         elif out.dtype != torch.float32 or out.shape != (2,) or out.device != self.device or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous float32 tensor of two elements on {self.device}")
-        _launch(torch, self.device, stream, himuon_grad_norm, self._c, self._dt, max_norm, out.data_ptr(),
-                self._ws.data_ptr(), self._ws.numel())
+        if _launch(torch, self.device, stream, himuon_grad_norm, self._c, self._dt, max_norm, out.data_ptr(),
+                   self._ws.data_ptr(), self._ws.numel()) != self._home:
+            self._went_abroad(stream)
         return out

@@ -50,7 +50,8 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
             0 if old_logp is None else _row(old_logp, f32, N, dev, "old_logp"),
             0 if ref_logp is None else _row(ref_logp, f32, N, dev, "ref_logp"))
     if dlogits is True:
-        dlogits = _empty(torch, stream, (N, V), logits.dtype, dev)
+        dlogits = (torch.empty(N, V, dtype=logits.dtype, device=dev) if stream is None else
+                   _empty(torch, stream, (N, V), logits.dtype))
     elif dlogits is False:
         dlogits = None
     elif dlogits is not None and (dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype or
@@ -60,7 +61,8 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
                       dlogits.data_ptr() if dlogits is not None else None, *rows, None, None,
                       _DTYPES[logits.dtype], clip[0], clip[1], kl_coef, temperature, grad_scale)
     need = himuon_policy_workspace(p)
-    buf = _empty(torch, stream, (4 + need // 4 + N,), f32, dev)   # stats, workspace (whole words), logp
+    words = 4 + need // 4 + N   # stats, workspace (whole words), logp
+    buf = torch.empty(words, dtype=f32, device=dev) if stream is None else _empty(torch, stream, (words,), f32)
     base = buf.data_ptr()
     p.stats, p.logp = base, base + 16 + need
     if stream is not None:
