@@ -137,3 +137,20 @@ def test_descriptors_and_workspaces_outlive_steps_on_another_stream(given):
     assert torch.equal(got, want)
     for w, v in zip(W, V):
         assert torch.equal(w, v)
+
+
+@pytest.mark.parametrize("count", [2, 20])
+def test_adamw_needs_gradients_after_they_were_dropped(count):
+    """(with descriptors in the arguments and in a table)"""
+    _need_gpu()
+    W = [torch.zeros(100, device=DEV) for _ in range(count)]
+    G = [torch.ones(100, device=DEV) for _ in range(count)]
+    opt = AdamW([(w, g, *adamw_state(w)) for w, g in zip(W, G)])
+    opt.step(0.5, 1)
+    opt.drop_grads()
+    with pytest.raises(RuntimeError):
+        opt.step(0.5, 2)
+    assert all((w == -0.5).all() for w in W)
+    opt.set_grads(G)
+    opt.step(0.5, 2)
+    assert all(((w + 1).abs() < 1e-6).all() for w in W)

@@ -197,16 +197,24 @@ class AdamW(_Streams):
                 self._went_abroad(stream)
 
     def drop_grads(self) -> None:
-        """Forgets the gradients, so that their memory may go; set_grads gives the next step's, unless those are at
-        the same addresses."""
+        """Forgets the gradients, so that their memory may go; a step needs new ones first (set_grads)."""
         self._let_go(self._tensors[1])
         self._tensors[1] = (None,) * len(self._n)
+
+    def _same_grads(self, grads) -> bool:
+        """Holds `grads` again, after drop_grads, if they are where the descriptors say."""
+        if any(g.data_ptr() != c.grad or g.numel() != c.n for g, c in zip(grads, self._c)):
+            return False
+        self._tensors[1] = tuple(grads)
+        return True
 
     def step(self, lr: float, t: int, scale=None, dither=None, stream=None) -> None:
         """Step number t >= 1.  scale: None or a float32 CUDA tensor whose first element multiplies
         the gradients (GradNorm's factor; NaN leaves everything unchanged).  dither: two random
         numbers in [0, 2^32), new ones each step, for 8-bit states."""
         torch = self._torch
+        if self._tensors[1][0] is None:
+            raise RuntimeError("the gradients were dropped: set_grads gives the step's")
         at = 0
         if scale is not None:
             if scale.dtype != torch.float32 or scale.device != self.device or scale.numel() < 1:

@@ -248,7 +248,7 @@ class AdamWOptimizer(torch.optim.Optimizer):
             held = (AdamW([(p.data, g, *self.state[p]["adamw"]) for p, g in zip(params, grads)], group["betas"],
                           group["eps"], group["weight_decay"]), constants, list(params))
             self._engines[key] = held
-        elif any(g.data_ptr() != c.grad for g, c in zip(grads, held[0]._c)):
+        elif not held[0]._same_grads(grads):
             held[0].set_grads(grads)
         return held[0]
 
