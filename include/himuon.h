@@ -382,7 +382,9 @@ typedef struct {
    8-bit states: moments and codes are computed in fp32 with every operation rounded on its
    own, in the order of these formulas ((1 - beta2) g first, then times g; r^2 before its
    product with beta2; 448 / peak as the rounded reciprocal times 448), so that any other
-   computation in that order gives the same states bit for bit.  The weight takes the fp32
+   computation in that order gives the same states bit for bit.  Where v overflows fp32 though r
+   and g are finite, r is 2^66 times the root of those products of r 2^-66 and g 2^-66 (fp32's
+   largest number at most): r is what the states hold.  The weight takes the fp32
    moments; then the step stores m and r = sqrt(v)
    by blocks of 256 elements: peak = the block's largest magnitude, scale = peak / 448, and
    y = |x| 448 / peak rounded to one of its two e4m3 neighbours, up with the probability of

@@ -8,6 +8,7 @@ pytestmark = pytest.mark.gpu
 hm = pytest.importorskip("tiled_newton_schulz_tile_amd")
 from tiled_newton_schulz_tile_amd.adamw import AdamW, GradNorm, adamw_state  # noqa: E402
 from tiled_newton_schulz_tile_amd.policy import policy_loss  # noqa: E402
+from test_gpu_adamw import check8  # noqa: E402
 
 DEV = "cuda"
 F32, BF16 = torch.float32, torch.bfloat16
@@ -154,3 +155,26 @@ def test_adamw_needs_gradients_after_they_were_dropped(count):
     opt.set_grads(G)
     opt.step(0.5, 2)
     assert all(((w + 1).abs() < 1e-6).all() for w in W)
+
+
+@pytest.mark.parametrize("wt,gt", [(F32, F32), (BF16, BF16)])
+@pytest.mark.parametrize("big", [1e25, -3e30, 6e37, 3e38])
+def test_adamw8_gradient_whose_square_overflows(wt, gt, big):
+    """A finite gradient whose weighted square is past fp32: its root is not, so the states hold it, its own weight
+    takes the step of the formulas, and its block's other weights stay finite, in this step and in later ones."""
+    _need_gpu()
+    n = 1000
+    g = torch.Generator().manual_seed(5)
+    W, G = torch.randn(n, generator=g).to(wt).to(DEV), torch.randn(n, generator=g).to(gt).to(DEV)
+    G[300] = big
+    state = adamw_state(W, 8)
+    opt = AdamW([(W, G, *state)], betas=(0.9, 0.999), eps=1e-8, weight_decay=0.1)
+    for t, dither in ((1, (7, 8)), (2, (0xFFFF1234, 3)), (3, (1 << 31, 1 << 30))):
+        before = [x.clone() for x in opt.tensors[0]]
+        opt.step(1e-2, t, dither=dither)
+        assert torch.isfinite(W.float()).all() and all(torch.isfinite(s.float()).all() for s in state)
+        if abs(big) < 2.0 ** 126:   # (the reciprocal of a root past that is subnormal: its weight may keep still)
+            check8(before, opt.tensors[0], t, 1e-2, 0.9, 0.999, 1e-8, 0.1, 1.0, dither)
+        if t == 1:
+            assert abs(float(state[3][1]) * 448 / (0.001 ** 0.5 * abs(float(G[300]))) - 1) < 1e-5   # the block's scale
+            G[300] = 0.5

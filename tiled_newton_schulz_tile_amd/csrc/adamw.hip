@@ -262,6 +262,16 @@ __device__ __forceinline__ float rounded_sqrt(float v) {
   return __builtin_fmaf(-above, s, v) > 0.f ? above : r;
 }
 
+// The root of a second moment that overflows though what it is made of does not (|g| above some
+// 5e20 at beta2 0.999): from the terms times 2^-66, whose squares stay below 2^124.  The state
+// holds the root, so nothing is lost; it is fp32's largest number where it rounds past that.
+__device__ __forceinline__ float root_of_large(float r0, float x, const AdamWParams &p) {
+#pragma clang fp contract(off)
+  const float r = r0 * 0x1p-66f, g = x * 0x1p-66f;
+  const float v = p.beta2 * (r * r) + p.omb2 * g * g;
+  return v < __builtin_inff() ? __builtin_fminf(__builtin_sqrtf(v) * 0x1p66f, 0x1.fffffep127f) : v;
+}
+
 __device__ __forceinline__ unsigned load_codes(const unsigned char *p, int64_t i, int n) {
   if (n >= 4) return *reinterpret_cast<const GLOBAL_AS u32u *>(gmem(p + i));
   unsigned word = 0;
@@ -313,8 +323,10 @@ __device__ __forceinline__ void adamw8_block(const Entry<8> &t, int64_t b, float
 #pragma unroll
       for (int e = 0; e < 4; ++e) rv[e] = rounded_sqrt(rv[e]);
     } else {
+      const f32x4 r0 = unpack_e4m3x4(r_word);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) rv[e] = __builtin_sqrtf(rv[e]);
+      for (int e = 0; e < 4; ++e)
+        rv[e] = rv[e] == __builtin_inff() ? root_of_large(r0[e] * r_unit, gv[e] * scale, p) : __builtin_sqrtf(rv[e]);
     }
   }
   const float decay = 1.f - p.lr * t.weight_decay;
