@@ -394,7 +394,9 @@ typedef struct {
    Rounding to nearest would hold a moment still that moves by less than half a gap a step.
    dither: two random numbers of the caller, new ones for each step (host memory; NULL is
    {0, 0}).  A nonzero r is stored as 2^-9 at least, so that no weight is divided by eps
-   alone while its m is not zero; a block with peak < 2^-100 is stored as zeros.
+   alone while its m is not zero; a block with peak < 2^-100 is stored as zeros.  Where r is
+   not finite, r and an m that is not are stored as the NaN code, and peak is that of the
+   block's others: as with 32-bit states only that element is lost.
    table: NULL, or device memory that holds what himuon_adamw_table wrote for these tensors
    and this config: the step is then one launch however many tensors there are; without it
    the descriptors go in the kernel arguments, some 56 (8-bit states) or 72 tensors a launch.

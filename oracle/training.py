@@ -85,8 +85,11 @@ def pack8(x, kind, dither):
     """x (fp64, flat) in the 8-bit state format: (values, scale, margin).  kind 0: first moment, 1: root of the
     second.  values are in units of the scale; margin is the distance, in units of the neighbours' gap, of the
     dithered magnitude to the nearest point where the rounding turns over (rounding errors of another computation
-    smaller than that leave the value unchanged)."""
+    smaller than that leave the value unchanged).  Elements that are not finite have the value NaN and no part in
+    their block's scale."""
     x = np.asarray(x, np.float64)
+    lost = ~np.isfinite(x)
+    x = np.where(lost, 0.0, x)
     n = x.size
     i = np.arange(n, dtype=np.uint64)
     u = (((i * MULT[kind] + dither) % 2 ** 32) >> np.uint64(16)).astype(np.float64)
@@ -106,4 +109,5 @@ def pack8(x, kind, dither):
         q = np.clip(q, 2.0 ** -9 if kind else 0.0, E4M3_MAX)
         values[s] = np.where(x[s] == 0, 0.0, np.sign(x[s]) * q)
         scale[b] = peak / E4M3_MAX
+    values[lost] = np.nan
     return values, scale, margin

@@ -6,7 +6,7 @@ import torch
 
 pytestmark = pytest.mark.gpu
 hm = pytest.importorskip("tiled_newton_schulz_tile_amd")
-from tiled_newton_schulz_tile_amd.adamw import AdamW, GradNorm, adamw_state  # noqa: E402
+from tiled_newton_schulz_tile_amd.adamw import AdamW, GradNorm, adamw_moments, adamw_state  # noqa: E402
 from tiled_newton_schulz_tile_amd.policy import policy_loss  # noqa: E402
 from test_gpu_adamw import check8  # noqa: E402
 
@@ -178,3 +178,35 @@ def test_adamw8_gradient_whose_square_overflows(wt, gt, big):
         if t == 1:
             assert abs(float(state[3][1]) * 448 / (0.001 ** 0.5 * abs(float(G[300]))) - 1) < 1e-5   # the block's scale
             G[300] = 0.5
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("n", [1000, 300, 1])
+def test_adamw8_element_that_is_not_finite_stays_alone(bad, n):
+    """As with states in 32 bits, a gradient that is not finite and is not skipped takes its own weight and states,
+    and nothing else: the others are those of a step without it, in this step and in later ones."""
+    _need_gpu()
+    g = torch.Generator().manual_seed(6)
+    at = n // 3
+    W = torch.randn(n, generator=g).to(DEV)
+    V = W.clone()
+    sw, sv = adamw_state(W, 8), adamw_state(V, 8)
+    G = [torch.randn(n, generator=g).to(DEV) for _ in range(3)]
+    H = [x.clone() for x in G]
+    G[1][at] = bad
+    for x in H:
+        x[at] = 0   # (an element that is not finite does not set its block's scale)
+    a, b = AdamW([(W, G[0], *sw)]), AdamW([(V, H[0], *sv)])
+    G[0][at] = 0
+    rest = torch.arange(n, device=DEV) != at
+    for t in (1, 2, 3):
+        a.set_grads([G[t - 1]])
+        b.set_grads([H[t - 1]])
+        a.step(1e-2, t, dither=(t, 9))
+        b.step(1e-2, t, dither=(t, 9))
+        assert torch.equal(W[rest], V[rest])
+        for x, y in zip(sw[:2], sv[:2]):
+            assert torch.equal(x.view(torch.uint8)[rest], y.view(torch.uint8)[rest])
+        assert torch.equal(sw[2], sv[2]) and torch.equal(sw[3], sv[3])
+        if t > 1:
+            assert torch.isnan(W[at]) and all(torch.isnan(m[at]) for m in adamw_moments(sw))

@@ -114,3 +114,12 @@ def test_grad_norm_limits():
     assert T.grad_norm([np.array([3.0]), np.array([4.0])], 1.0)[0] == 5.0
     assert T.grad_norm([np.array([3e-9])], 1.0)[1] == 1.0
     assert np.isnan(T.grad_norm([np.array([np.inf])], 1.0)[1])
+
+
+def test_pack8_leaves_elements_that_are_not_finite_alone():
+    x = np.array([1.0, np.nan, -0.25, np.inf, 3e-3])
+    for kind in (0, 1):
+        y = np.abs(x) if kind else x
+        q, s, _ = T.pack8(y, kind, 12345)
+        want, unit, _ = T.pack8(np.where(np.isfinite(y), y, 0), kind, 12345)
+        assert np.isnan(q[[1, 3]]).all() and np.array_equal(q[[0, 2, 4]], want[[0, 2, 4]]) and np.array_equal(s, unit)
