@@ -238,15 +238,18 @@ class AdamWOptimizer(torch.optim.Optimizer):
                 raise ValueError("parameters must be contiguous float32 or bfloat16 CUDA tensors")
 
     def _engine(self, key, params, group):
-        """The AdamW over these parameters, kept while they, their memory and the group's constants stay the same."""
+        """The AdamW over these parameters, kept while they, their memory, their states and the group's constants
+        stay the same."""
         held = self._engines.get(key)
         constants = (group["betas"], group["eps"], group["weight_decay"])
+        states = [self.state[p]["adamw"] for p in params]
         same = held is not None and held[1] == constants and len(held[2]) == len(params) and \
-            all(a is b and a.data_ptr() == c.weight for a, b, c in zip(params, held[2], held[0]._c))
+            all(a is b and s is t and a.data_ptr() == c.weight and a.numel() == c.n
+                for a, b, s, t, c in zip(params, held[2], states, held[3], held[0]._c))
         grads = [p.grad if p.grad.is_contiguous() else p.grad.contiguous() for p in params]
         if not same:
-            held = (AdamW([(p.data, g, *self.state[p]["adamw"]) for p, g in zip(params, grads)], group["betas"],
-                          group["eps"], group["weight_decay"]), constants, list(params))
+            held = (AdamW([(p.data, g, *s) for p, g, s in zip(params, grads, states)], group["betas"], group["eps"],
+                          group["weight_decay"]), constants, list(params), states)
             self._engines[key] = held
         elif not held[0]._same_grads(grads):
             held[0].set_grads(grads)
