@@ -1,11 +1,11 @@
 """AdamWOptimizer and HiMuonOptimizer where a training program does the unusual (MI355X only):
-states that are replaced."""
+states that are replaced, refused factors."""
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
 hm = pytest.importorskip("tiled_newton_schulz_tile_amd")
-from tiled_newton_schulz_tile_amd.optim import AdamWOptimizer  # noqa: E402
+from tiled_newton_schulz_tile_amd.optim import AdamWOptimizer, HiMuonOptimizer  # noqa: E402
 
 DEV = "cuda"
 SHAPES = [(7,), (300, 170), (1,), (64, 3, 3), (5000,)]
@@ -53,3 +53,29 @@ def test_adamw_optimizer_takes_states_that_were_replaced(bits):
         x.step()
         y.step()
         same_states(x, a, y, b)
+
+
+def bad_factors():
+    one = torch.ones(1, device=DEV)
+    return [0.5, one.double(), one.cpu(), one[:0], one.bfloat16()]
+
+
+@pytest.mark.parametrize("which", range(5))
+def test_refused_factor_changes_nothing(which):
+    _need_gpu()
+    bad = bad_factors()[which]
+    ps = params(2, [(300, 170), (128, 64), (77,)])
+    opt = HiMuonOptimizer(ps, lr=0.02, tile=64, fallback=lambda q: AdamWOptimizer(q, lr=1e-2))
+    set_grads(ps, 0)
+    opt.step()
+    set_grads(ps, 1)
+    before = [p.detach().clone() for p in ps] + [opt.momentum(p).clone() for p in ps[:2]]
+    with pytest.raises(ValueError):
+        opt.step(grad_scale=bad)
+    with pytest.raises(ValueError):
+        opt.fallback.step(grad_scale=bad)
+    torch.cuda.synchronize()
+    for x, y in zip(before, [*ps, *(opt.momentum(p) for p in ps[:2])]):
+        assert torch.equal(x, y)
+    assert opt.step_count == 1 and opt.fallback.state[ps[2]]["step"] == 1
+    opt.close()

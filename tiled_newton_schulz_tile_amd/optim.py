@@ -77,6 +77,13 @@ def split_params(params, lr: float):
     return list(by_lr.items()), other
 
 
+def _check_factor(grad_scale, params):
+    """Refuses a factor for the gradients of `params` before anything changes, so that no step is half done."""
+    if not isinstance(grad_scale, torch.Tensor) or grad_scale.dtype != torch.float32 or grad_scale.numel() < 1 or \
+            any(p.device != grad_scale.device for p in params):
+        raise ValueError("grad_scale must be a float32 tensor on the parameters' device")
+
+
 class HiMuonOptimizer(torch.optim.Optimizer):
     """HiMuon on the 2-D parameters, a plain optimizer on the others.
 
@@ -142,6 +149,9 @@ class HiMuonOptimizer(torch.optim.Optimizer):
         gradients, so a grad_scale with them is refused."""
         if grad_scale is not None and self.fallback is not None and not isinstance(self.fallback, AdamWOptimizer):
             raise ValueError("grad_scale needs an AdamWOptimizer fallback")
+        if grad_scale is not None:
+            groups = self.param_groups + (self.fallback.param_groups if self.fallback is not None else [])
+            _check_factor(grad_scale, [p for grp in groups for p in grp["params"]])
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -263,23 +273,28 @@ class AdamWOptimizer(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        calls = {}   # one launch each
         for k, group in enumerate(self.param_groups):
-            calls = {}
             for p in group["params"]:
                 if p.grad is None:
                     continue
                 st = self.state[p]
                 if "adamw" not in st:
                     st["step"], st["adamw"] = 0, adamw_state(p, self.state_bits)
-                st["step"] += 1
-                calls.setdefault((k, p.device.index, p.dtype, p.grad.dtype, st["step"]), []).append(p)
-            for (*key, t), params in calls.items():
-                # parameters that joined late have a step count, and an engine, of their own
-                key = (*key, tuple(map(id, params)) if len(calls) > 1 else None)
-                dither = [self._random.getrandbits(32) for _ in range(2)] if self.state_bits == 8 else None
-                engine = self._engine(key, params, group)
-                engine.step(float(group["lr"]), t, scale=grad_scale, dither=dither)
-                engine.drop_grads()
+                calls.setdefault((k, p.device, p.dtype, p.grad.dtype, st["step"] + 1), []).append(p)
+        if grad_scale is not None:
+            _check_factor(grad_scale, [params[0] for params in calls.values()])
+        of_group = [key[0] for key in calls]
+        for (*key, t), params in calls.items():
+            group = self.param_groups[key[0]]
+            # parameters that joined late have a step count, and an engine, of their own
+            key = (*key, tuple(map(id, params)) if of_group.count(key[0]) > 1 else None)
+            dither = [self._random.getrandbits(32) for _ in range(2)] if self.state_bits == 8 else None
+            engine = self._engine(key, params, group)
+            engine.step(float(group["lr"]), t, scale=grad_scale, dither=dither)
+            engine.drop_grads()
+            for p in params:
+                self.state[p]["step"] = t
         return loss
 
     def state_dict(self):
