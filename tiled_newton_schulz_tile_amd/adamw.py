@@ -143,6 +143,7 @@ class AdamW(_Streams):
             if size != n:
                 raise ValueError("W, G and the states must have the same number of elements")
             ptrs.append(at)
+        self._at = ptrs[:2]   # addresses of W and G
         for col in cols[4:]:
             size, at = _column(col, "scale", (torch.float32,), self.device)
             if size != [-(-k // ADAMW_BLOCK) for k in n]:
@@ -185,9 +186,8 @@ class AdamW(_Streams):
         if size != self._n:
             raise ValueError("a gradient must have its weight's number of elements")
         self._let_go(self._tensors[1])
-        self._tensors[1] = grads
-        for c, p in zip(self._c, at):
-            c.grad = p
+        self._tensors[1], self._at[1] = grads, at
+        self._words[2::8] = array("Q", at)
         if self._table is not None:
             host = torch.empty(self._table.numel(), dtype=torch.uint8, pin_memory=True)
             himuon_adamw_table(self._c, self.cfg, host.data_ptr(), host.numel())
@@ -203,7 +203,7 @@ class AdamW(_Streams):
 
     def _same_grads(self, grads) -> bool:
         """Holds `grads` again, after drop_grads, if they are where the descriptors say."""
-        if any(g.data_ptr() != c.grad or g.numel() != c.n for g, c in zip(grads, self._c)):
+        if [g.data_ptr() for g in grads] != self._at[1] or [g.numel() for g in grads] != self._n:
             return False
         self._tensors[1] = tuple(grads)
         return True

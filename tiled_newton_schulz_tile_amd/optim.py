@@ -247,20 +247,17 @@ class AdamWOptimizer(torch.optim.Optimizer):
                 self.param_groups.pop()
                 raise ValueError("parameters must be contiguous float32 or bfloat16 CUDA tensors")
 
-    def _engine(self, key, params, group):
+    def _engine(self, key, params, grads, states, group):
         """The AdamW over these parameters, kept while they, their memory, their states and the group's constants
         stay the same."""
+        grads = [g if g.is_contiguous() else g.contiguous() for g in grads]
+        # (ids: what they stand for is held with them)
+        kind = (group["betas"], group["eps"], group["weight_decay"], list(map(id, params)), list(map(id, states)))
         held = self._engines.get(key)
-        constants = (group["betas"], group["eps"], group["weight_decay"])
-        states = [self.state[p]["adamw"] for p in params]
-        same = held is not None and held[1] == constants and len(held[2]) == len(params) and \
-            all(a is b and s is t and a.data_ptr() == c.weight and a.numel() == c.n
-                for a, b, s, t, c in zip(params, held[2], states, held[3], held[0]._c))
-        grads = [p.grad if p.grad.is_contiguous() else p.grad.contiguous() for p in params]
-        if not same:
-            held = (AdamW([(p.data, g, *s) for p, g, s in zip(params, grads, states)], group["betas"], group["eps"],
-                          group["weight_decay"]), constants, list(params), states)
-            self._engines[key] = held
+        if held is None or held[1] != kind or held[0]._at[0] != [p.data_ptr() for p in params] or \
+                held[0]._n != [p.numel() for p in params]:
+            engine = AdamW([(p.data, g, *s) for p, g, s in zip(params, grads, states)], *kind[:3])
+            self._engines[key] = held = (engine, kind, params, states)
         elif not held[0]._same_grads(grads):
             held[0].set_grads(grads)
         return held[0]
@@ -276,25 +273,27 @@ class AdamWOptimizer(torch.optim.Optimizer):
         calls = {}   # one launch each
         for k, group in enumerate(self.param_groups):
             for p in group["params"]:
-                if p.grad is None:
+                g = p.grad
+                if g is None:
                     continue
                 st = self.state[p]
                 if "adamw" not in st:
                     st["step"], st["adamw"] = 0, adamw_state(p, self.state_bits)
-                calls.setdefault((k, p.device, p.dtype, p.grad.dtype, st["step"] + 1), []).append(p)
+                calls.setdefault((k, p.device, p.dtype, g.dtype, st["step"] + 1), []).append((p, g, st))
         if grad_scale is not None:
-            _check_factor(grad_scale, [params[0] for params in calls.values()])
+            _check_factor(grad_scale, [call[0][0] for call in calls.values()])
         of_group = [key[0] for key in calls]
-        for (*key, t), params in calls.items():
+        for (*key, t), call in calls.items():
+            params, grads, states = zip(*call)
             group = self.param_groups[key[0]]
             # parameters that joined late have a step count, and an engine, of their own
             key = (*key, tuple(map(id, params)) if of_group.count(key[0]) > 1 else None)
             dither = [self._random.getrandbits(32) for _ in range(2)] if self.state_bits == 8 else None
-            engine = self._engine(key, params, group)
+            engine = self._engine(key, params, grads, [st["adamw"] for st in states], group)
             engine.step(float(group["lr"]), t, scale=grad_scale, dither=dither)
             engine.drop_grads()
-            for p in params:
-                self.state[p]["step"] = t
+            for st in states:
+                st["step"] = t
         return loss
 
     def state_dict(self):
