@@ -1,5 +1,5 @@
 """AdamWOptimizer and HiMuonOptimizer where a training program does the unusual (MI355X only):
-states that are replaced, refused factors."""
+states that are replaced, refused factors, parameters whose gradients come and go."""
 import pytest
 import torch
 
@@ -79,3 +79,38 @@ def test_refused_factor_changes_nothing(which):
         assert torch.equal(x, y)
     assert opt.step_count == 1 and opt.fallback.state[ps[2]]["step"] == 1
     opt.close()
+
+
+def test_parameters_whose_gradients_come_and_go():
+    """Another set of parameters at nearly every step (routed experts): what the optimizer keeps for its calls stays
+    bounded, and the parameters are torch's (within the two fp32 computations' rounding, as in a usual run)."""
+    _need_gpu()
+    shapes = [(40 + k,) for k in range(12)]
+    a, b = params(3, shapes), params(3, shapes)
+    x, y = AdamWOptimizer(a, lr=1e-2, weight_decay=0.1), torch.optim.AdamW(b, lr=1e-2, weight_decay=0.1)
+    g = torch.Generator().manual_seed(0)
+    sets = set()
+    for step in range(60):
+        take = torch.rand(12, generator=g) < 0.5
+        sets.add(tuple(take.tolist()))
+        for opt, ps in ((x, a), (y, b)):
+            set_grads(ps, step)
+            for p, t in zip(ps, take.tolist()):
+                if not t:
+                    p.grad = None
+            opt.step()
+    assert len(sets) > 50 and len(x._engines) <= 32
+    for p, q in zip(a, b):
+        assert ((p - q).abs() <= 2.0 ** -20 * (0.6 + q.abs())).all()
+
+
+def test_many_groups_keep_their_descriptors():
+    _need_gpu()
+    ps = params(8, [(5,)] * 50)
+    opt = AdamWOptimizer([{"params": [p]} for p in ps], lr=1e-2)
+    kept = []
+    for step in range(3):
+        set_grads(ps, step)
+        opt.step()
+        kept.append({key: held[0] for key, held in opt._engines.items()})
+    assert len(kept[0]) == 50 and all(k == kept[0] for k in kept)

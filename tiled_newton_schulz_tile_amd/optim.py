@@ -231,6 +231,8 @@ class AdamWOptimizer(torch.optim.Optimizer):
     rounding).  A parameter's state is ``state[p]["adamw"]``, the tensors that
     adamw.adamw_state makes; its step count starts with its first gradient."""
 
+    ENGINES = 32   # sets of parameters whose descriptors are kept, a step's own always: they pile up where sets vary
+
     def __init__(self, params, lr: float = 3e-4, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
                  state_bits: int = 32, seed: int = 0):
         if state_bits not in (32, 8):
@@ -253,13 +255,14 @@ class AdamWOptimizer(torch.optim.Optimizer):
         grads = [g if g.is_contiguous() else g.contiguous() for g in grads]
         # (ids: what they stand for is held with them)
         kind = (group["betas"], group["eps"], group["weight_decay"], list(map(id, params)), list(map(id, states)))
-        held = self._engines.get(key)
+        held = self._engines.pop(key, None)
         if held is None or held[1] != kind or held[0]._at[0] != [p.data_ptr() for p in params] or \
                 held[0]._n != [p.numel() for p in params]:
             engine = AdamW([(p.data, g, *s) for p, g, s in zip(params, grads, states)], *kind[:3])
-            self._engines[key] = held = (engine, kind, params, states)
+            held = (engine, kind, params, states)
         elif not held[0]._same_grads(grads):
             held[0].set_grads(grads)
+        self._engines[key] = held   # the last one used stands last
         return held[0]
 
     @torch.no_grad()
@@ -294,6 +297,8 @@ class AdamWOptimizer(torch.optim.Optimizer):
             engine.drop_grads()
             for st in states:
                 st["step"] = t
+        while len(self._engines) > max(self.ENGINES, len(calls)):
+            del self._engines[next(iter(self._engines))]
         return loss
 
     def state_dict(self):
