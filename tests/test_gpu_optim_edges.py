@@ -1,5 +1,7 @@
 """AdamWOptimizer and HiMuonOptimizer where a training program does the unusual (MI355X only):
-states that are replaced, refused factors, parameters whose gradients come and go."""
+states that are replaced, refused factors, parameters whose gradients come and go, copies."""
+import copy
+
 import pytest
 import torch
 
@@ -114,3 +116,24 @@ def test_many_groups_keep_their_descriptors():
         opt.step()
         kept.append({key: held[0] for key, held in opt._engines.items()})
     assert len(kept[0]) == 50 and all(k == kept[0] for k in kept)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_copied_optimizer_goes_on_alone(bits):
+    _need_gpu()
+    a = params(4)
+    x = AdamWOptimizer(a, lr=1e-2, state_bits=bits, seed=3)
+    for step in range(2):
+        set_grads(a, step)
+        x.step()
+    y = copy.deepcopy(x)
+    b = y.param_groups[0]["params"]
+    assert all(p is not q for p, q in zip(a, b))
+    for step in range(2, 4):
+        set_grads(a, step)
+        set_grads(b, step)
+        x.step()
+        y.step()
+        same_states(x, a, y, b)
+    assert all(s.data_ptr() != t.data_ptr() for p, q in zip(a, b)
+               for s, t in zip(x.state[p]["adamw"], y.state[q]["adamw"]))

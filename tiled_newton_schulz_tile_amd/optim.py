@@ -301,6 +301,10 @@ class AdamWOptimizer(torch.optim.Optimizer):
             del self._engines[next(iter(self._engines))]
         return loss
 
+    def __getstate__(self):
+        """For copies and pickles, which make descriptors of their own."""
+        return {**super().__getstate__(), "state_bits": self.state_bits, "_random": self._random, "_engines": {}}
+
     def state_dict(self):
         sd = super().state_dict()
         sd["random"] = self._random.getstate()
