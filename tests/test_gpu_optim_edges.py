@@ -1,5 +1,6 @@
 """AdamWOptimizer and HiMuonOptimizer where a training program does the unusual (MI355X only):
-states that are replaced, refused factors, parameters whose gradients come and go, copies."""
+states that are replaced, refused factors, parameters whose gradients come and go, copies, and
+what autograd has to know of writes that it does not make."""
 import copy
 
 import pytest
@@ -8,6 +9,7 @@ import torch
 pytestmark = pytest.mark.gpu
 hm = pytest.importorskip("tiled_newton_schulz_tile_amd")
 from tiled_newton_schulz_tile_amd.optim import AdamWOptimizer, HiMuonOptimizer  # noqa: E402
+from tiled_newton_schulz_tile_amd.policy import policy_loss  # noqa: E402
 
 DEV = "cuda"
 SHAPES = [(7,), (300, 170), (1,), (64, 3, 3), (5000,)]
@@ -137,3 +139,24 @@ def test_copied_optimizer_goes_on_alone(bits):
         same_states(x, a, y, b)
     assert all(s.data_ptr() != t.data_ptr() for p, q in zip(a, b)
                for s, t in zip(x.state[p]["adamw"], y.state[q]["adamw"]))
+
+
+def test_autograd_sees_the_gradient_written_over_logits():
+    """A backward pass that saved the logits (a tanh cap keeps its output) raises torch's error and does not take the
+    gradient for them; logits that nothing saved may be written over."""
+    _need_gpu()
+    g = torch.Generator().manual_seed(0)
+    z = torch.randn(6, 50, generator=g).to(DEV).requires_grad_()
+    label, w, adv = torch.arange(6, device=DEV), torch.ones(6, device=DEV), torch.ones(6, device=DEV)
+    logits = torch.tanh(z)
+    got = policy_loss(logits.detach(), label, w, adv, dlogits=logits.detach())
+    with pytest.raises(RuntimeError):
+        logits.backward(got.dlogits)
+    logits = z * 2
+    want = policy_loss(logits.detach(), label, w, adv).dlogits
+    got = policy_loss(logits.detach(), label, w, adv, dlogits=logits.detach())
+    logits.backward(got.dlogits)
+    assert torch.equal(z.grad, want * 2)
+    with torch.inference_mode():   # (tensors without a version)
+        t = z.detach().clone()
+        assert torch.equal(policy_loss(t, label, w, adv, dlogits=t).dlogits, policy_loss(z.detach(), label, w, adv).dlogits)

@@ -2,7 +2,7 @@
 
 One call gives the loss, its parts, the log probability of every sampled token and, where
 it is asked for, the gradient with respect to the logits, which a training program hands
-to torch (``logits.backward(got.dlogits)``).  Formulas and conventions: include/himuon.h.
+to torch (``logits.backward(got.dlogits)``; the loss itself has no graph).  Formulas and conventions: include/himuon.h.
 """
 from __future__ import annotations
 
@@ -49,7 +49,8 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
             _row(advantage, f32, N, dev, "advantage"),
             0 if old_logp is None else _row(old_logp, f32, N, dev, "old_logp"),
             0 if ref_logp is None else _row(ref_logp, f32, N, dev, "ref_logp"))
-    if dlogits is True:
+    given = dlogits is not True
+    if not given:
         dlogits = (torch.empty(N, V, dtype=logits.dtype, device=dev) if stream is None else
                    _empty(torch, stream, (N, V), logits.dtype))
     elif dlogits is False:
@@ -70,6 +71,8 @@ def policy_loss(logits, label, weight, advantage, old_logp=None, ref_logp=None, 
             if t is not None:
                 t.record_stream(stream)
     _launch(torch, dev, stream, himuon_policy_loss, p, base + 16, need)
+    if given and dlogits is not None:
+        torch.autograd.graph.increment_version(dlogits)   # a backward pass that saved what stood here has to say so
     stats, _, logp = buf.split_with_sizes((4, need // 4, N))
     return PolicyLoss(stats, logp, dlogits)
 
