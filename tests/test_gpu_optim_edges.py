@@ -160,3 +160,14 @@ def test_autograd_sees_the_gradient_written_over_logits():
     with torch.inference_mode():   # (tensors without a version)
         t = z.detach().clone()
         assert torch.equal(policy_loss(t, label, w, adv, dlogits=t).dlogits, policy_loss(z.detach(), label, w, adv).dlogits)
+
+
+def test_autograd_sees_a_step():
+    _need_gpu()
+    p = torch.nn.Parameter(torch.ones(100, device=DEV))
+    opt = AdamWOptimizer([p], lr=1e-2)
+    loss = (p * p).sum()
+    p.grad = torch.ones(100, device=DEV)
+    opt.step()
+    with pytest.raises(RuntimeError):
+        loss.backward()

@@ -295,6 +295,7 @@ class AdamWOptimizer(torch.optim.Optimizer):
             engine = self._engine(key, params, grads, [st["adamw"] for st in states], group)
             engine.step(float(group["lr"]), t, scale=grad_scale, dither=dither)
             engine.drop_grads()
+            torch.autograd.graph.increment_version(params)   # a graph that saved them must not go on with the new ones
             for st in states:
                 st["step"] = t
         while len(self._engines) > max(self.ENGINES, len(calls)):
