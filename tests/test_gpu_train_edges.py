@@ -210,3 +210,20 @@ def test_adamw8_element_that_is_not_finite_stays_alone(bad, n):
         assert torch.equal(sw[2], sv[2]) and torch.equal(sw[3], sv[3])
         if t > 1:
             assert torch.isnan(W[at]) and all(torch.isnan(m[at]) for m in adamw_moments(sw))
+
+
+@pytest.mark.parametrize("dtype,V", [(BF16, 1001), (BF16, 8000), (BF16, 20000), (BF16, 50257), (BF16, 100001),
+                                     (F32, 1001), (F32, 9000), (F32, 30001), (F32, 57000)])
+def test_policy_gradient_past_the_caches_equals_a_cached_one(dtype, V):
+    """Every kernel for rows that a block holds, with stores past the L2s (a gradient above 32 MB) and with cached
+    ones (a part of its rows below that), gives the same bits."""
+    _need_gpu()
+    row = V * (2 if dtype == BF16 else 4)
+    n = 130   # (more rows than are cut into spans)
+    N = max(2 * n, int(32e6 / row) + 10)
+    assert N * row > 32e6 >= n * row
+    logits, rest = policy_inputs(N, V, dtype, V)
+    got = policy_loss(logits, *rest, kl_coef=0.1)
+    for part in (slice(0, n), slice(N - n, N)):
+        one = policy_loss(logits[part], *(t[part] for t in rest), kl_coef=0.1)
+        assert torch.equal(one.logp, got.logp[part]) and torch.equal(one.dlogits, got.dlogits[part])

@@ -278,7 +278,7 @@ __global__ __launch_bounds__(THR) void policy_row_kernel(const T *logits, T *dlo
 // pass alone holds nothing and runs two blocks a CU.  1000 fp32 rows of 128256, 1 in 5 left
 // out: gradient 212 us held, 263 us with every vector read twice (193 us with the stores past
 // the L2s, 4.8 TB/s of what has to move); forward 90 us held, 78 us streamed.
-constexpr int kLongThreads = 1024;
+constexpr int kLongThreads = 1024, kHeldVecs = 1024 * 16;   // vectors that a block's registers hold
 template <int OUT>
 constexpr int kLongK = OUT != kForward ? 16 : 0;
 template <typename T, int OUT>
@@ -544,8 +544,9 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_finish_kernel(const 
 // rows x vocabulary (bf16) 1 x 50257 5.7 / 11.2, 8 x 131072 6.4 / 18.3, 64 x 4096 6.4 / 6.5,
 // 64 x 50257 8.6 / 13.4, 96 x 4096 7.3 / 6.7, 96 x 128256 14.9 / 21.5, 128 x 16384 7.7 / 8.0,
 // 128 x 128256 18.1 / 22.2, 192 x 50257 15.9 / 15.9, 192 x 128256 26.5 / 24.7.
+constexpr int kFewRows = 128;
 bool few_rows(int64_t rows, int64_t vecs) {
-  return rows > 0 && ((rows <= 64 && vecs >= 256) || (rows <= 128 && vecs >= 2048));
+  return rows > 0 && ((rows <= 64 && vecs >= 256) || (rows <= kFewRows && vecs >= 2048));
 }
 
 // A gradient that the L2s together (32 MB) cannot hold goes past them: 4096 x 128256 bf16 356 /
@@ -563,8 +564,9 @@ void launch_rows(const T *z, T *dz, unsigned rows, int out, const PolicyParams &
 template <typename T>
 void launch_long_rows(const T *z, T *dz, unsigned rows, int out, const PolicyParams &p, hipStream_t stream) {
   const dim3 grid(rows), block(kLongThreads);
+  // (fewer rows are cut into spans: the gradient is one that the L2s cannot hold)
+  static_assert((kFewRows + 1.0) * kHeldVecs * 16 > kL2Bytes, "long rows past the L2s");
   if (out == kForward) hipLaunchKernelGGL((policy_long_kernel<T, kForward>), grid, block, 0, stream, z, dz, p);
-  else if (out == kGradient) hipLaunchKernelGGL((policy_long_kernel<T, kGradient>), grid, block, 0, stream, z, dz, p);
   else hipLaunchKernelGGL((policy_long_kernel<T, kGradientNT>), grid, block, 0, stream, z, dz, p);
 }
 
@@ -602,7 +604,7 @@ hipError_t launch_policy_t(const himuon_policy &c, const PolicyParams &p, hipStr
     else if (vecs <= 512 * 4) launch_rows<T, 512, 4>(zr, dr, rows, out, q, stream);
     else if (vecs <= 512 * 8) launch_rows<T, 512, 8>(zr, dr, rows, out, q, stream);
     else if (vecs <= 1024 * 8) launch_rows<T, 1024, 8>(zr, dr, rows, out, q, stream);
-    else if (vecs <= 1024 * 16) launch_rows<T, 1024, 16>(zr, dr, rows, out, q, stream);
+    else if (vecs <= kHeldVecs) launch_rows<T, 1024, 16>(zr, dr, rows, out, q, stream);
     else launch_long_rows<T>(zr, dr, rows, out, q, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
