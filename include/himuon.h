@@ -378,7 +378,8 @@ typedef struct {
      m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2
      w <- w (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
    with w rounded to nearest even where weight_dtype is bf16.  Where *grad_scale is NaN
-   (himuon_grad_norm's factor for a gradient that is not finite) the step changes nothing.
+   (himuon_grad_norm's factor for a gradient that is not finite) the step changes nothing; t
+   is the caller's, who decides whether such a step counts.
    8-bit states: moments and codes are computed in fp32 with every operation rounded on its
    own, in the order of these formulas ((1 - beta2) g first, then times g; r^2 before its
    product with beta2; 448 / peak as the rounded reciprocal times 448), so that any other

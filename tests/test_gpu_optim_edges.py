@@ -1,10 +1,12 @@
 """AdamWOptimizer and HiMuonOptimizer where a training program does the unusual (MI355X only):
-states that are replaced, refused factors, parameters whose gradients come and go, copies, and
-what autograd has to know of writes that it does not make."""
+states that are replaced, refused factors, parameters whose gradients come and go, copies,
+skipped steps, and what autograd has to know of writes that it does not make."""
 import copy
 
 import pytest
 import torch
+
+from oracle import training as T
 
 pytestmark = pytest.mark.gpu
 hm = pytest.importorskip("tiled_newton_schulz_tile_amd")
@@ -171,3 +173,25 @@ def test_autograd_sees_a_step():
     opt.step()
     with pytest.raises(RuntimeError):
         loss.backward()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_skipped_step_counts_and_changes_nothing_else(bits):
+    """The step after a skipped first one is the formula's with t = 2 on zero moments, within the kernel's 2^-18 of
+    the step and 2^-22 of the weight."""
+    _need_gpu()
+    p = torch.nn.Parameter(torch.randn(1000, generator=torch.Generator().manual_seed(1)).to(DEV))
+    w = p.detach().double().cpu().numpy()
+    opt = AdamWOptimizer([p], lr=1e-2, weight_decay=0.1, state_bits=bits)
+    set_grads([p], 0)
+    opt.step(grad_scale=torch.full((1,), float("nan"), device=DEV))
+    assert (p.detach().double().cpu().numpy() == w).all() and opt.state[p]["step"] == 1
+    assert not any(s.view(torch.uint8).any() for s in opt.state[p]["adamw"])
+    set_grads([p], 1)
+    opt.step()
+    want, _, _ = T.adamw(w, p.grad.double().cpu().numpy(), 0 * w, 0 * w, 2, 1e-2, weight_decay=0.1)
+    got = p.detach().double().cpu().numpy()
+    assert (abs(got - want) <= 2.0 ** -18 * 1e-2 + 2.0 ** -22 * abs(w)).all()
+    full, _, _ = T.adamw(w, p.grad.double().cpu().numpy(), 0 * w, 0 * w, 1, 1e-2, weight_decay=0.1)
+    decayed = w * (1 - 1e-3)
+    assert abs((want - decayed) / (full - decayed) - 0.744).max() < 1e-3   # the documented size

@@ -145,7 +145,8 @@ class HiMuonOptimizer(torch.optim.Optimizer):
     def step(self, closure=None, grad_scale=None):
         """grad_scale: None, or a float32 CUDA tensor whose first element multiplies every gradient (the clip
         factor of adamw.GradNorm), read on the device.  Where it is NaN (a gradient that is not finite) the HiMuon
-        gradients count as zero and an AdamWOptimizer fallback skips its step.  Other fallbacks take unscaled
+        gradients count as zero (the momentum decays and still moves the matrices) and an AdamWOptimizer fallback
+        skips its step, which it counts.  Other fallbacks take unscaled
         gradients, so a grad_scale with them is refused."""
         if grad_scale is not None and self.fallback is not None and not isinstance(self.fallback, AdamWOptimizer):
             raise ValueError("grad_scale needs an AdamWOptimizer fallback")
@@ -268,7 +269,9 @@ class AdamWOptimizer(torch.optim.Optimizer):
     @torch.no_grad()
     def step(self, closure=None, grad_scale=None):
         """grad_scale: None, or a float32 CUDA tensor whose first element multiplies the gradients; NaN leaves
-        parameters and states as they are."""
+        parameters and moments as they are.  Such a step still counts for the bias corrections, for only the device
+        knows of it: after k skipped ones a step divides its moments by 1 - beta^t with t too large by k (which
+        matters while beta^t does: skipping the very first step makes the second one 0.74 of its size)."""
         loss = None
         if closure is not None:
             with torch.enable_grad():
