@@ -108,7 +108,8 @@ struct RowIn {
   float w, adv, old, ref_logp, zy;
   int32_t label;   // -1: the row is left out
 };
-__device__ __forceinline__ RowIn row_scalars(int64_t row, const PolicyParams &p) {   // all but zy
+template <class T, bool ZY = true>   // (ZY false: all but zy, and z is not used)
+__device__ __forceinline__ RowIn row_in(const T *z, int64_t row, const PolicyParams &p) {
   RowIn r;
   r.w = gmem(p.weight)[row];
   const int64_t y = gmem(p.label)[row];
@@ -117,12 +118,7 @@ __device__ __forceinline__ RowIn row_scalars(int64_t row, const PolicyParams &p)
   r.adv = gmem(p.advantage)[row];
   r.old = p.old_logp ? gmem(p.old_logp)[row] : 0.f;
   r.ref_logp = p.ref_logp ? gmem(p.ref_logp)[row] : 0.f;
-  return r;
-}
-template <class T>
-__device__ __forceinline__ RowIn row_in(const T *z, int64_t row, const PolicyParams &p) {
-  RowIn r = row_scalars(row, p);
-  if (r.label >= 0) r.zy = Vec<T>::load1(z + r.label);
+  if constexpr (ZY) r.zy = Vec<T>::load1(z + r.label);
   return r;
 }
 
@@ -491,7 +487,7 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_finish_kernel(const 
     if (blockIdx.x != 0) return;
     double sum[3] = {0, 0, 0};
     for (int row = tid / kRowLanes; row < rows; row += THR / kRowLanes) {
-      RowIn r = row_scalars(row, p);
+      RowIn r = row_in<T, false>(nullptr, row, p);
       RowTerms t = {0.f, 0.f, f32x4{0.f, 0.f, 0.f, 0.f}};
       if (r.label >= 0) {
         const Softmax s = join_spans_quad(p.spans + (int64_t)row * (spans + 1), spans, p.k, r.zy);
@@ -511,7 +507,7 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_finish_kernel(const 
   const bool has_rest = (int)blockIdx.x == spans - 1 && rest < V;
   const T *z = logits + row * p.ld_logits;
   T *dz = dlogits + row * p.ld_dlogits;
-  RowIn r = row_scalars(row, p);
+  RowIn r = row_in<T, false>(nullptr, row, p);
   if (r.label < 0) {
     const float zero[N] = {};
 #pragma unroll
@@ -540,10 +536,15 @@ __global__ __launch_bounds__(kSpanThreads) void policy_span_finish_kernel(const 
   if (has_rest) Vec<T>::store1(dz + rest, f * pow2(tail, p.k, s.ref) + (rest == r.label ? coef : 0.f));
 }
 
-// Measured on graphs of 21 calls, split against one block a row, gradient included (us):
-// rows x vocabulary (bf16) 1 x 50257 5.7 / 11.2, 8 x 131072 6.4 / 18.3, 64 x 4096 6.4 / 6.5,
-// 64 x 50257 8.6 / 13.4, 96 x 4096 7.3 / 6.7, 96 x 128256 14.9 / 21.5, 128 x 16384 7.7 / 8.0,
-// 128 x 128256 18.1 / 22.2, 192 x 50257 15.9 / 15.9, 192 x 128256 26.5 / 24.7.
+// Measured on graphs of 21 calls, split against one block a row, gradient included (us), rows x
+// vocabulary.  bf16: 1 x 50257 5.6 / 10.6, 8 x 131072 6.2 / 17.9, 64 x 4096 5.7 / 5.8, 64 x 50257
+// 9.5 / 12.6, 96 x 4096 6.9 / 5.9, 96 x 128256 15.0 / 21.2, 128 x 16384 7.5 / 7.4, 128 x 128256
+// 18.0 / 20.1, 192 x 50257 15.4 / 15.5, 192 x 128256 26.4 / 23.1.  fp32: 1 x 50257 5.9 / 9.8, 8 x
+// 131072 6.7 / 19.5, 64 x 4096 6.1 / 5.6, 64 x 16384 6.7 / 7.0, 64 x 131072 16.9 / 23.2, 65 x 128256
+// 17.9 / 22.3, 80 x 128256 21.6 / 23.1, 96 x 16384 9.3 / 7.9, 96 x 128256 26.0 / 24.8, 128 x 16384
+// 10.0 / 8.5, 128 x 128256 38.2 / 28.6.  One rule for both types, which suits bf16 throughout and
+// fp32 up to 64 rows; of 65 to 128 fp32 rows it suits the forward pass (80 x 128256 13.2 / 18.2, 128
+// x 60000 11.3 / 10.5) and the longest ones.
 constexpr int kFewRows = 128;
 bool few_rows(int64_t rows, int64_t vecs) {
   return rows > 0 && ((rows <= 64 && vecs >= 256) || (rows <= kFewRows && vecs >= 2048));
