@@ -275,7 +275,7 @@ HIMUON_API himuon_status himuon_sign_vote(const uint8_t *bits, int32_t workers, 
 
 /* ---- The rest of a training step ----------------------------------------------------
    HiMuon updates a model's matrices.  The entry points below are what stands next to it
-   in a training step: the loss with its gradient, the norm of the whole gradient with its
+   in a training step: the loss with its gradient, the norm of a gradient with its
    clip factor, and AdamW for every parameter that is not a matrix.  They are stateless
    (no plan): the arrays of descriptors are read on the host during the call and may be
    reused at once.  They enqueue only: no allocation, no wait for the GPU, so they may be

@@ -1,6 +1,6 @@
 """AdamW and the gradient norm over many torch tensors at once (himuon_adamw_step and
 himuon_grad_norm of libhimuon): the update of the parameters that HiMuon leaves alone, and
-the clip factor of the whole gradient, which stays on the device.
+the clip factor of a gradient, which stays on the device.
 
 AdamW and GradNorm hold the descriptors of a list of tensors; formulas, the 8-bit state
 format and conventions are in include/himuon.h.

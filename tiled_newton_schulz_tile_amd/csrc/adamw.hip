@@ -199,8 +199,8 @@ __global__ __launch_bounds__(THREADS) void adamw32_kernel(TABLE tab, AdamWParams
 // a difference of a whole gap.  So the moments and codes are defined in fp32 with every
 // operation rounded on its own, in the order written here (no fused multiply-adds, the root
 // and the reciprocal correctly rounded): any other computation in that order gives the same
-// bits.  262 M elements, fp32 weights, bf16 gradients: 587 us (6.3 TB/s), near both bounds (HBM,
-// and 350 VALU instructions a block of 256).
+// bits.  262 M elements, fp32 weights, bf16 gradients: 590 us (6.2 TB/s), near both bounds (HBM,
+// and 283 VALU instructions a block of 256, 310 with bf16 weights).
 constexpr int kBlock = HIMUON_ADAMW_BLOCK;
 static_assert(kBlock == 4 * 64, "a wave holds one block");
 constexpr unsigned kStepM = 0x9E3779B1u, kStepR = 0x85EBCA6Bu;   // of the dither sequences
