@@ -1,8 +1,11 @@
 """Calls of the training step's operators at the edges of what their documentation allows
-(MI355X only): gradients in the place of the logits for many blocks a row, and calls on
-another stream than the current one."""
+(MI355X only): gradients in the place of the logits for many blocks a row, calls on another
+stream than the current one, and gradients from subnormal ones to those whose squares overflow."""
+import numpy as np
 import pytest
 import torch
+
+from oracle import training as T
 
 pytestmark = pytest.mark.gpu
 hm = pytest.importorskip("tiled_newton_schulz_tile_amd")
@@ -227,3 +230,65 @@ def test_policy_gradient_past_the_caches_equals_a_cached_one(dtype, V):
     for part in (slice(0, n), slice(N - n, N)):
         one = policy_loss(logits[part], *(t[part] for t in rest), kl_coef=0.1)
         assert torch.equal(one.logp, got.logp[part]) and torch.equal(one.dlogits, got.dlogits[part])
+
+
+def states8_in_fp32(g, code, unit, dither, beta1=0.9, beta2=0.999):
+    """The documented 8-bit states after a step: numpy float32, every operation rounded on its own.  Returns the codes
+    and scales of m and r."""
+    f = np.float32
+    table = T.e4m3_values().astype(f)
+    n = g.size
+    with np.errstate(all="ignore"):
+        old = [table[c] * np.repeat(u, T.BLOCK)[:n] for c, u in zip(code, unit)]
+        m = f(beta1) * old[0] + f(1 - beta1) * g
+        v = f(beta2) * (old[1] * old[1]) + f(1 - beta2) * g * g
+        gs, rs = g * f(2.0 ** -66), old[1] * f(2.0 ** -66)
+        large = f(beta2) * (rs * rs) + f(1 - beta2) * gs * gs
+        past = np.isinf(v) & np.isfinite(large)
+        r = np.where(past, np.minimum(np.sqrt(large) * f(2.0 ** 66), np.finfo(f).max), np.sqrt(v))
+        out = []
+        for k, x in enumerate((m, r)):
+            lost = ~np.isfinite(x)
+            x = np.where(lost, f(0), x)
+            peak = np.abs(np.concatenate([x, np.zeros(-n % T.BLOCK, f)])).reshape(-1, T.BLOCK).max(1)
+            held = peak >= f(2.0 ** -100)
+            inv = np.repeat(np.where(held, f(1) / peak * f(448), f(0)), T.BLOCK)[:n]
+            seq = ((np.arange(n, dtype=np.uint64) * T.MULT[k] + dither[k]) % 2 ** 32 >> np.uint64(16)).astype(np.uint32)
+            bits = (np.abs(x) * inv * f(2.0 ** -120)).view(np.uint32)
+            c = np.minimum((bits + (seq << np.uint32(4)) + np.uint32(8)) >> np.uint32(20), 126)
+            c = np.maximum(c, x != 0) if k else c | (np.signbit(x) * np.uint32(128))
+            c = np.where(lost, 0x7f, np.where(inv > 0, c, 0)).astype(np.uint8)
+            out.append((c, np.where(held, peak * f(1 / 448), f(0))))
+    return out
+
+
+@pytest.mark.parametrize("spread", [2, 30, 150])
+@pytest.mark.parametrize("gt", [F32, BF16])
+@pytest.mark.parametrize("n", [256, 20001])
+def test_adamw8_states_over_the_range_of_fp32(spread, gt, n):
+    """Bit for bit, with gradients and scales from subnormal ones to the largest, zeros, and some that are not finite,
+    in blocks of one size (spread 2) or of many."""
+    _need_gpu()
+    for seed in range(4):
+        rng = np.random.default_rng(100 * spread + seed)
+        middle = np.repeat(rng.uniform(-145, 127, -(-n // T.BLOCK)), T.BLOCK)[:n]
+        size = np.clip(middle + rng.uniform(-spread, spread, n), -149, 127.9)
+        g = torch.from_numpy((np.sign(rng.standard_normal(n)) * 2.0 ** size * (rng.random(n) > 0.05)).astype(np.float32))
+        if seed == 3:
+            g[::997] = float("nan")
+            g[1::1499] = float("inf")
+        G = g.to(gt).to(DEV)
+        blocks = -(-n // T.BLOCK)
+        code = [rng.integers(0, 127, n).astype(np.uint8) for _ in range(2)]
+        code[0] |= (rng.integers(0, 2, n) * 128).astype(np.uint8)
+        unit = [(2.0 ** rng.uniform(-145, 119, blocks) * (rng.random(blocks) > 0.1)).astype(np.float32) for _ in range(2)]
+        dither = [int(x) for x in rng.integers(0, 2 ** 32, 2)]
+        state = [torch.from_numpy(c.copy()).to(DEV).view(torch.float8_e4m3fn) for c in code]
+        scale = [torch.from_numpy(u.copy()).to(DEV) for u in unit]
+        W = torch.zeros(n, device=DEV)
+        AdamW([(W, G, *state, *scale)]).step(1e-3, 7, dither=dither)
+        want = states8_in_fp32(G.float().cpu().numpy(), code, unit, dither)
+        for got, s, (c, u) in zip(state, scale, want):
+            assert np.array_equal(s.cpu().numpy(), u), (seed, np.nonzero(s.cpu().numpy() != u)[0][:5])
+            got = got.view(torch.uint8).cpu().numpy()
+            assert np.array_equal(got, c), (seed, np.nonzero(got != c)[0][:5], got[got != c][:5], c[got != c][:5])
