@@ -1,6 +1,6 @@
 """AdamWOptimizer and HiMuonOptimizer where a training program does the unusual (MI355X only):
 states that are replaced, refused factors, parameters whose gradients come and go, copies,
-skipped steps, and what autograd has to know of writes that it does not make."""
+skipped steps, refused states, and what autograd has to know of writes that it does not make."""
 import copy
 
 import pytest
@@ -195,3 +195,28 @@ def test_a_skipped_step_counts_and_changes_nothing_else(bits):
     full, _, _ = T.adamw(w, p.grad.double().cpu().numpy(), 0 * w, 0 * w, 1, 1e-2, weight_decay=0.1)
     decayed = w * (1 - 1e-3)
     assert abs((want - decayed) / (full - decayed) - 0.744).max() < 1e-3   # the documented size
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_refused_states_leave_the_optimizer_as_it_was(bits):
+    """States of the other kind, of another shape or type, and of another optimizer."""
+    _need_gpu()
+    a, b = params(5), params(5)
+    x, y = AdamWOptimizer(a, lr=1e-2, state_bits=bits), AdamWOptimizer(b, lr=1e-2, state_bits=bits)
+    other = AdamWOptimizer(params(5), lr=0.5, state_bits=40 - bits)
+    torchs = torch.optim.AdamW(params(5), lr=0.5)
+    short = AdamWOptimizer(params(5, [(7,), (300, 171), (1,), (64, 3, 3), (5000,)]), lr=0.5, state_bits=bits)
+    for opt in (x, y, other, torchs, short):
+        set_grads(opt.param_groups[0]["params"], 0)
+        opt.step()
+    cast = copy.deepcopy(x.state_dict())
+    cast["state"][4]["adamw"] = tuple(s.double() for s in cast["state"][4]["adamw"])
+    for sd in (other.state_dict(), torchs.state_dict(), short.state_dict(), cast):
+        with pytest.raises(ValueError):
+            x.load_state_dict(sd)
+        same_states(x, a, y, b)
+    assert x.param_groups[0]["lr"] == 1e-2
+    for opt, ps in ((x, a), (y, b)):
+        set_grads(ps, 1)
+        opt.step()
+    same_states(x, a, y, b)

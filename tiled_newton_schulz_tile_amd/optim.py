@@ -25,7 +25,7 @@ import random
 
 import torch
 
-from . import HiMuon, PREC_BF16X3, QUINTIC
+from . import ADAMW_BLOCK, HiMuon, PREC_BF16X3, QUINTIC
 from .adamw import AdamW, adamw_state
 
 
@@ -315,20 +315,28 @@ class AdamWOptimizer(torch.optim.Optimizer):
         return sd
 
     def load_state_dict(self, state_dict):
-        """Restores states bit for bit (torch would cast them to the parameters' dtype) and the random numbers."""
+        """Restores states bit for bit (torch would cast them to the parameters' dtype) and the random numbers; a
+        state_dict that does not fit leaves the optimizer as it was."""
         state_dict = dict(state_dict)
-        rng = state_dict.pop("random", None)
-        held = state_dict["state"]
-        super().load_state_dict({**state_dict, "state": {}})
+        rng, numbers = state_dict.pop("random", None), self._random
+        if rng is not None:
+            numbers = random.Random()
+            numbers.setstate((rng[0], tuple(rng[1]), rng[2]))
+        held, states = state_dict["state"], {}
         for saved, group in zip(state_dict["param_groups"], self.param_groups):
             for i, p in zip(saved["params"], group["params"]):
-                st = held.get(i)
-                if not st:
-                    continue
-                kept = tuple(x.to(p.device, copy=True) for x in st["adamw"])
-                if len(kept) != (2 if self.state_bits == 32 else 4) or kept[0].shape != p.shape:
-                    raise ValueError("the saved states are of another kind or shape")
-                self.state[p] = {"step": int(st["step"]), "adamw": kept}
-        if rng is not None:
-            self._random.setstate((rng[0], tuple(rng[1]), rng[2]))
-        self._engines = {}
+                if held.get(i):
+                    states[p] = self._loaded(held[i], p)
+        super().load_state_dict({**state_dict, "state": {}})
+        self.state.update(states)
+        self._random, self._engines = numbers, {}
+
+    def _loaded(self, saved, p):
+        """A copy of a saved state of parameter p on its device."""
+        blocks = (-(-p.numel() // ADAMW_BLOCK),)
+        kinds = ([(torch.float32, p.shape)] * 2 if self.state_bits == 32 else
+                 [(torch.float8_e4m3fn, p.shape)] * 2 + [(torch.float32, blocks)] * 2)
+        tensors = saved.get("adamw", ())
+        if "step" not in saved or [(x.dtype, x.shape) for x in tensors] != kinds:
+            raise ValueError("the saved states are of another kind or shape")
+        return {"step": int(saved["step"]), "adamw": tuple(x.to(p.device, copy=True) for x in tensors)}
