@@ -143,6 +143,31 @@ def test_descriptors_and_workspaces_outlive_steps_on_another_stream(given):
         assert torch.equal(w, v)
 
 
+@pytest.mark.parametrize("given", [True, False])
+def test_factors_outlive_calls_on_another_stream(given):
+    """A factor that a step has yet to read, and a result's place that a norm has yet to write, are not handed out."""
+    _need_gpu()
+    W, G = torch.zeros(100, device=DEV), torch.ones(100, device=DEV)
+    opt, norm = AdamW([(W, G, *adamw_state(W))]), GradNorm([G])
+    s = torch.cuda.Stream()
+    factor, out = torch.full((1,), float("nan"), device=DEV), torch.zeros(2, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        if not given:
+            opt.step(0.5, 1, scale=factor)
+            norm.compute(1.0, out=out)
+    if given:
+        opt.step(0.5, 1, scale=factor, stream=s)
+        norm.compute(1.0, out=out, stream=s)
+    ptrs = factor.data_ptr(), out.data_ptr()
+    del factor, out
+    held = [torch.ones(1, device=DEV) for _ in range(16)]
+    assert not {t.data_ptr() for t in held} & set(ptrs)
+    torch.cuda.synchronize()
+    assert not W.any() and all(t == 1 for t in held)
+
+
 @pytest.mark.parametrize("count", [2, 20])
 def test_adamw_needs_gradients_after_they_were_dropped(count):
     """(with descriptors in the arguments and in a table)"""

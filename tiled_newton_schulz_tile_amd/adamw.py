@@ -51,12 +51,14 @@ class _Streams:
         self._own, self._abroad = memory, []
         self._home = self._torch.cuda.current_stream(self.device).cuda_stream
 
-    def _went_abroad(self, stream):
-        """A call went to `stream` (None: the current one), whose handle is not self._home."""
+    def _went_abroad(self, stream, of_call=None):
+        """A call went to `stream` (None: the current one), whose handle is not self._home; of_call: a tensor that it
+        was given and that is not held."""
         if stream is None:
             stream = self._torch.cuda.current_stream(self.device)
-        if self._own is not None:
-            self._own.record_stream(stream)
+        for t in (self._own, of_call):
+            if t is not None:
+                t.record_stream(stream)
         if stream not in self._abroad:
             self._abroad.append(stream)
 
@@ -222,7 +224,7 @@ class AdamW(_Streams):
             at = scale.data_ptr()
         if _launch(torch, self.device, stream, himuon_adamw_step, self._c, self.cfg, t, lr, at, dither,
                    self._table.data_ptr() if self._table is not None else 0) != self._home:
-            self._went_abroad(stream)
+            self._went_abroad(stream, scale)
 
 
 class GradNorm(_Streams):
@@ -277,5 +279,5 @@ class GradNorm(_Streams):
             raise ValueError(f"out must be a contiguous float32 tensor of two elements on {self.device}")
         if _launch(torch, self.device, stream, himuon_grad_norm, self._c, self._dt, max_norm, out.data_ptr(),
                    self._ws.data_ptr(), self._ws.numel()) != self._home:
-            self._went_abroad(stream)
+            self._went_abroad(stream, out)
         return out
