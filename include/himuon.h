@@ -329,6 +329,59 @@ HIMUON_API himuon_status himuon_policy_workspace(const himuon_policy *p, size_t 
 HIMUON_API himuon_status himuon_policy_loss(const himuon_policy *p, void *workspace, size_t ws_bytes,
                                             void *hip_stream);
 
+/* Entries of a teacher's row at most, and tokens of a vocabulary in the calls that take them. */
+#define HIMUON_TOP_MOST 1024
+#define HIMUON_TOP_VOCAB (1 << 20)
+
+/* Distillation from a teacher's top logits, over `rows` tokens with `vocab` student logits each.
+   Entry j of a row (j < k) names token v_j = index[j] with the teacher's logit value[j]; an entry
+   whose index is outside [0, vocab) does not count.  rest, where given, is the log-sum-exp of the
+   teacher's other logits over the temperature (himuon_top_logits leaves it), one class more.  With
+     q = softmax over the row's entries of value / temperature (and of rest),
+     p = softmax(logits / temperature), p_rest = the sum of p over the tokens that no entry names,
+     kl = sum_j q_j (log q_j - log p[v_j])  (+ q_rest (log q_rest - log p_rest)),
+     loss = sum over rows of weight kl
+   and, where dlogits is not NULL,
+     dlogits[u] = grad_scale weight / temperature (p[u] - sum of q_j over the entries that name u),
+   for a token u that no entry names grad_scale weight / temperature p[u] (1 - q_rest / p_rest)
+   (q_rest = 0 without rest).  Terms with q = 0 are 0.  A token that more than one entry names is
+   one of the tokens that are named, and each of its entries counts.  A row whose weight is zero, or
+   whose teacher has no probability anywhere (no entry that counts and is not -inf, no rest that is
+   not -inf), is left out: its kl and dlogits are 0; with weight zero nothing else of it is read.
+   Logits of -inf have probability 0 (and an infinite kl where the teacher gives them some); a row
+   with NaN or +inf among its student's or its teacher's logits that count, or with nothing but
+   -inf, gives NaN. */
+typedef struct {
+  int64_t rows, vocab;           /* >= 0, in [1, HIMUON_TOP_VOCAB]                      */
+  int64_t ld_logits, ld_dlogits; /* leading dimensions in elements, >= vocab            */
+  int64_t ld_top;                /* of value and index, >= k                            */
+  const void *logits;            /* device, dtype                                       */
+  void *dlogits;                 /* device, dtype, or NULL: no gradient.  May be logits
+                                    itself (ld_dlogits == ld_logits); must not overlap it
+                                    otherwise                                           */
+  const void *value;             /* device, value_dtype, rows x k                       */
+  const int64_t *index;          /* device, rows x k                                    */
+  const float *rest;             /* device, rows, or NULL: q is over the entries alone  */
+  const float *weight;           /* device, rows                                        */
+  float *kl;                     /* device, rows                                        */
+  float *loss;                   /* device, 1                                           */
+  int32_t k;                     /* in [1, HIMUON_TOP_MOST]                             */
+  himuon_dtype dtype;            /* of logits and dlogits                               */
+  himuon_dtype value_dtype;
+  double temperature;            /* in [2^-20, 2^20]                                    */
+  double grad_scale;             /* finite; multiplies dlogits only                     */
+} himuon_distill;
+
+/* Workspace bytes himuon_distill_loss needs for this call (device memory, 16-byte aligned,
+   contents immaterial; may be 0). */
+HIMUON_API himuon_status himuon_distill_workspace(const himuon_distill *p, size_t *bytes);
+
+/* Enqueues the loss (and its gradient) on hip_stream.  All sums have a fixed order: the same call
+   gives the same bits.  EINVAL: NULL pointers with rows > 0 (loss always), bad sizes, leading
+   dimensions, scalars or dtypes, a short or misaligned workspace.  EDEVICE: launch failure. */
+HIMUON_API himuon_status himuon_distill_loss(const himuon_distill *p, void *workspace, size_t ws_bytes,
+                                             void *hip_stream);
+
 /* One tensor of a gradient: n contiguous elements on the device. */
 typedef struct {
   int64_t n;

@@ -111,3 +111,47 @@ def pack8(x, kind, dither):
         scale[b] = peak / E4M3_MAX
     values[lost] = np.nan
     return values, scale, margin
+
+
+def distill_loss(logits, value, index, weight, rest=None, temperature=1.0, grad_scale=1.0):
+    """(loss, kl (N), dlogits (N, V)) of the distillation loss on a teacher's entries, row by row."""
+    z = np.asarray(logits, np.float64)
+    N, V = z.shape
+    kl, grad = np.zeros(N), np.zeros((N, V))
+    for i in range(N):
+        w = float(weight[i])
+        if w == 0:
+            continue
+        with np.errstate(all="ignore"):
+            counts = [j for j in range(len(index[i])) if 0 <= index[i][j] < V]
+            token = np.array([int(index[i][j]) for j in counts], np.int64)
+            t = np.array([float(value[i][j]) for j in counts]) / temperature
+            if rest is not None:
+                t = np.append(t, float(rest[i]))
+            if not (t != -np.inf).any():
+                continue
+            q = np.exp(t - t.max())
+            q /= q.sum()
+            logq = t - t.max() - np.log(np.exp(t - t.max()).sum())
+            row = z[i] / temperature
+            lse = row.max() + np.log(np.exp(row - row.max()).sum())
+            others = np.ones(V, bool)
+            others[token] = False
+            lp = row[token] - lse
+            share = np.zeros(V)
+            if rest is not None:
+                top = row[others].max() if others.any() else -np.inf
+                e = np.exp(row[others] - top) if np.isfinite(top) else np.zeros(others.sum())
+                if np.isnan(row).any():
+                    e = e * np.nan
+                lp = np.append(lp, top + np.log(e.sum()) - lse)
+                if q[-1] != 0 and e.sum() != 0:
+                    share[others] = q[-1] * (e / e.sum())
+            kl[i] = sum(a * (b - c) for a, b, c in zip(q, logq, lp) if a != 0)
+            grad[i] = np.exp(row - lse) - share
+            for v, a in zip(token, q):
+                grad[i, v] -= a
+            if np.isnan(q).any():
+                grad[i] = np.nan
+            grad[i] *= grad_scale * w / temperature
+    return float(sum(w * d for w, d in zip(np.asarray(weight, np.float64), kl) if d != 0)), kl, grad

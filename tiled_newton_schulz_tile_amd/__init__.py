@@ -19,7 +19,8 @@ __all__ = [
     "himuon_plan_stats", "himuon_plan_tiles", "himuon_plan_destroy", "himuon_last_error",
     "himuon_plan_runtime_counts", "himuon_runtime_counts", "himuon_step_static", "STATIC_WORKSPACE_BYTES",
     "himuon_stream_step",
-    "himuon_policy", "himuon_policy_workspace", "himuon_policy_loss", "himuon_grad", "himuon_grad_norm_workspace",
+    "himuon_policy", "himuon_policy_workspace", "himuon_policy_loss", "himuon_distill", "himuon_distill_workspace",
+    "himuon_distill_loss", "TOP_MOST", "TOP_VOCAB", "himuon_grad", "himuon_grad_norm_workspace",
     "himuon_grad_norm", "himuon_adamw_tensor", "himuon_adamw_config", "himuon_adamw_step",
     "himuon_adamw_table_size", "himuon_adamw_table", "ADAMW_BLOCK",
     "HiMuon", "CUBIC", "QUINTIC", "TILE_FULL", "F32", "BF16", "PREC_F32", "PREC_BF16",
@@ -35,6 +36,8 @@ FLAG_WRITE_UPDATE = 1
 FLAG_IDENTITY_MAP = 2
 STATIC_WORKSPACE_BYTES = 64 << 20   # HIMUON_STATIC_WORKSPACE_BYTES
 ADAMW_BLOCK = 256                   # HIMUON_ADAMW_BLOCK
+TOP_MOST = 1024                     # HIMUON_TOP_MOST
+TOP_VOCAB = 1 << 20                 # HIMUON_TOP_VOCAB
 
 STATUS = {0: "HIMUON_OK", -1: "HIMUON_EINVAL", -2: "HIMUON_EBUDGET", -3: "HIMUON_ENOMEM",
           -4: "HIMUON_EDEVICE", -5: "HIMUON_EUNSUPPORTED"}
@@ -43,8 +46,8 @@ STATUS = {0: "HIMUON_OK", -1: "HIMUON_EINVAL", -2: "HIMUON_EBUDGET", -3: "HIMUON
 EXPORTED = ("himuon_plan", "himuon_workspace_size", "himuon_step", "himuon_set_tile_schedule",
             "himuon_plan_stats", "himuon_plan_tiles", "himuon_plan_destroy", "himuon_last_error",
             "himuon_plan_runtime_counts", "himuon_step_static", "himuon_stream_step", "himuon_sign_pack",
-            "himuon_sign_vote", "himuon_policy_workspace", "himuon_policy_loss", "himuon_grad_norm_workspace",
-            "himuon_grad_norm", "himuon_adamw_step", "himuon_adamw_table_size", "himuon_adamw_table")
+            "himuon_sign_vote", "himuon_policy_workspace", "himuon_policy_loss", "himuon_distill_workspace",
+            "himuon_distill_loss", "himuon_grad_norm_workspace", "himuon_grad_norm", "himuon_adamw_step", "himuon_adamw_table_size", "himuon_adamw_table")
 
 
 class HiMuonError(RuntimeError):
@@ -102,6 +105,15 @@ class himuon_policy(ctypes.Structure):
                 ("kl_coef", ctypes.c_double), ("temperature", ctypes.c_double), ("grad_scale", ctypes.c_double)]
 
 
+class himuon_distill(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("ld_logits", ctypes.c_int64), ("ld_dlogits", ctypes.c_int64), ("ld_top", ctypes.c_int64),
+                ("logits", ctypes.c_void_p), ("dlogits", ctypes.c_void_p), ("value", ctypes.c_void_p),
+                ("index", ctypes.c_void_p), ("rest", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("kl", ctypes.c_void_p), ("loss", ctypes.c_void_p), ("k", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("value_dtype", ctypes.c_int), ("temperature", ctypes.c_double), ("grad_scale", ctypes.c_double)]
+
+
 class himuon_grad(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("grad", ctypes.c_void_p)]
 
@@ -150,6 +162,8 @@ def _load() -> ctypes.CDLL:
                                      P, ctypes.c_float, P]
     lib.himuon_policy_workspace.argtypes = [ctypes.POINTER(himuon_policy), ctypes.POINTER(ctypes.c_size_t)]
     lib.himuon_policy_loss.argtypes = [ctypes.POINTER(himuon_policy), P, ctypes.c_size_t, P]
+    lib.himuon_distill_workspace.argtypes = [ctypes.POINTER(himuon_distill), ctypes.POINTER(ctypes.c_size_t)]
+    lib.himuon_distill_loss.argtypes = [ctypes.POINTER(himuon_distill), P, ctypes.c_size_t, P]
     lib.himuon_grad_norm_workspace.argtypes = [ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]
     lib.himuon_grad_norm.argtypes = [ctypes.POINTER(himuon_grad), ctypes.c_int32, ctypes.c_int, ctypes.c_double,
                                      P, P, ctypes.c_size_t, P]
@@ -255,6 +269,16 @@ def himuon_policy_workspace(p: himuon_policy) -> int:
 
 def himuon_policy_loss(p: himuon_policy, workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> None:
     _check(_lib.himuon_policy_loss(ctypes.byref(p), workspace_ptr or None, ws_bytes, stream_ptr or None))
+
+
+def himuon_distill_workspace(p: himuon_distill) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.himuon_distill_workspace(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+def himuon_distill_loss(p: himuon_distill, workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> None:
+    _check(_lib.himuon_distill_loss(ctypes.byref(p), workspace_ptr or None, ws_bytes, stream_ptr or None))
 
 
 def himuon_grad_norm_workspace(n_tensors: int) -> int:

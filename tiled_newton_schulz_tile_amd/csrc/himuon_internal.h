@@ -196,4 +196,8 @@ hipError_t launch_grad_norm(const himuon_grad *tensors, int32_t n_tensors, bool 
 size_t policy_workspace(const himuon_policy &p);
 hipError_t launch_policy(const himuon_policy &p, void *workspace, hipStream_t stream);
 
+// ---- distillation from a teacher's top logits (distill.hip) ----------------------
+size_t distill_workspace(const himuon_distill &p);
+hipError_t launch_distill(const himuon_distill &p, void *workspace, hipStream_t stream);
+
 }  // namespace himuon

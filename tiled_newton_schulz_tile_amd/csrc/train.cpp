@@ -47,6 +47,25 @@ himuon_status check_policy(const himuon_policy *p) {
   return HIMUON_OK;
 }
 
+bool is_temperature(double t) { return t >= 0x1p-20 && t <= 0x1p20; }
+
+himuon_status check_distill(const himuon_distill *p) {
+  if (!p) return bad("NULL argument");
+  if (p->rows < 0 || p->rows > kMostElements) return bad("rows must be in [0, 2^40]");
+  if (p->vocab < 1 || p->vocab > HIMUON_TOP_VOCAB) return bad("vocab must be in [1, 2^20]");
+  if (!is_dtype(p->dtype) || !is_dtype(p->value_dtype)) return bad("dtype");
+  if (p->k < 1 || p->k > HIMUON_TOP_MOST) return bad("k must be in [1, 1024]");
+  if (p->ld_logits < p->vocab || p->ld_top < p->k) return bad("ld_logits must be >= vocab and ld_top >= k");
+  if (p->dlogits && p->ld_dlogits < p->vocab) return bad("ld_dlogits must be >= vocab");
+  if (p->ld_logits > kMostElements || p->ld_top > kMostElements || (p->dlogits && p->ld_dlogits > kMostElements))
+    return bad("leading dimension too large");
+  if (p->dlogits && p->dlogits == p->logits && p->ld_dlogits != p->ld_logits)
+    return bad("dlogits in the place of logits needs the same leading dimension");
+  if (!is_temperature(p->temperature)) return bad("temperature must be in [2^-20, 2^20]");
+  if (!std::isfinite(p->grad_scale)) return bad("grad_scale must be finite");
+  return HIMUON_OK;
+}
+
 himuon_status check_adamw(const himuon_adamw_tensor *tensors, int32_t n_tensors, const himuon_adamw_config *cfg) {
   if (n_tensors < 0 || (n_tensors > 0 && !tensors) || !cfg) return bad("bad argument");
   if (n_tensors > kMostTensors) return bad("more than 2^24 tensors");
@@ -90,6 +109,29 @@ HIMUON_API himuon_status himuon_policy_loss(const himuon_policy *p, void *worksp
   if ((s = check_workspace(workspace, ws_bytes, himuon::policy_workspace(*p))) != HIMUON_OK) return s;
   return launched(himuon::launch_policy(*p, workspace, reinterpret_cast<hipStream_t>(hip_stream)),
                   "policy loss launch");
+} catch (...) {
+  return HIMUON_ENOMEM;
+}
+
+HIMUON_API himuon_status himuon_distill_workspace(const himuon_distill *p, size_t *bytes) try {
+  if (!bytes) return bad("NULL argument");
+  himuon_status s = check_distill(p);
+  if (s != HIMUON_OK) return s;
+  *bytes = himuon::distill_workspace(*p);
+  return HIMUON_OK;
+} catch (...) {
+  return HIMUON_ENOMEM;
+}
+
+HIMUON_API himuon_status himuon_distill_loss(const himuon_distill *p, void *workspace, size_t ws_bytes,
+                                             void *hip_stream) try {
+  himuon_status s = check_distill(p);
+  if (s != HIMUON_OK) return s;
+  if (!p->loss) return bad("NULL pointer");
+  if (p->rows > 0 && (!p->logits || !p->value || !p->index || !p->weight || !p->kl)) return bad("NULL pointer");
+  if ((s = check_workspace(workspace, ws_bytes, himuon::distill_workspace(*p))) != HIMUON_OK) return s;
+  return launched(himuon::launch_distill(*p, workspace, reinterpret_cast<hipStream_t>(hip_stream)),
+                  "distillation loss launch");
 } catch (...) {
   return HIMUON_ENOMEM;
 }
