@@ -329,9 +329,76 @@ HIMUON_API himuon_status himuon_policy_workspace(const himuon_policy *p, size_t 
 HIMUON_API himuon_status himuon_policy_loss(const himuon_policy *p, void *workspace, size_t ws_bytes,
                                             void *hip_stream);
 
-/* Entries of a teacher's row at most, and tokens of a vocabulary in the calls that take them. */
+/* Entries of a teacher's row at most, and tokens of a vocabulary in the three calls below. */
 #define HIMUON_TOP_MOST 1024
 #define HIMUON_TOP_VOCAB (1 << 20)
+
+/* Sampling a token from each of `rows` rows of `vocab` logits, from given random numbers.
+   With T the row's temperature, e_i = exp((logits[i] - max) / T) and the row's tokens in the order
+   of their logits from the largest, equal ones by index (-0 equals 0), the filters keep the first
+     n = min(top_k, the smallest n whose e sum to top_p of what the first top_k sum to,
+             the number of tokens with e_i >= min_p)
+   of them, one at least: top_k outside [1, vocab] and top_p not below 1 keep all, a top_p of 0 or
+   less keeps one, min_p not above 0 keeps all and counts as 1 above 1.  The token is the first one,
+   by index among those kept, up to which their e sum to more than uniform times the sum over all
+   that are kept: with uniform drawn from [0, 1), each with its share of probability (a uniform
+   outside of that counts as its nearest end, NaN as 0).  Then
+     logp = log of the token's probability under softmax(logits / T), filters aside: old_logp of
+            himuon_policy_loss with that temperature,
+     kept = the probability that all kept tokens have there.
+   T = 0 takes the first of the largest logits (logp 0, kept 1).  Tokens of -inf are never taken; a
+   row with NaN or +inf among its logits or with nothing but -inf, and a row_temperature that is
+   neither 0 nor in [2^-20, 2^20], give token -1 and NaN.  Borders are decided as 64-bit sums of the
+   formulas above decide them. */
+typedef struct {
+  int64_t rows, vocab;           /* >= 0, in [1, HIMUON_TOP_VOCAB]                      */
+  int64_t ld_logits;             /* leading dimension in elements, >= vocab             */
+  const void *logits;            /* device, dtype                                       */
+  const float *uniform;          /* device, rows                                        */
+  const float *row_temperature;  /* device, rows, each: in the place of the number      */
+  const int32_t *row_top_k;      /*   below for all rows, or NULL                       */
+  const float *row_top_p;
+  const float *row_min_p;
+  int64_t *token;                /* device, rows                                        */
+  float *logp, *kept;            /* device, rows                                        */
+  himuon_dtype dtype;
+  int32_t top_k;
+  double temperature;            /* 0 or in [2^-20, 2^20]                               */
+  double top_p, min_p;           /* not NaN                                             */
+} himuon_sampling;
+
+/* Workspace bytes himuon_sample needs for this call (device memory, 16-byte aligned, contents
+   immaterial; may be 0). */
+HIMUON_API himuon_status himuon_sample_workspace(const himuon_sampling *p, size_t *bytes);
+
+/* Enqueues the draws on hip_stream; the same call gives the same bits.  EINVAL: NULL pointers with
+   rows > 0, bad sizes, leading dimension, scalars or dtype, a short or misaligned workspace.
+   EDEVICE: launch failure. */
+HIMUON_API himuon_status himuon_sample(const himuon_sampling *p, void *workspace, size_t ws_bytes, void *hip_stream);
+
+/* The k largest logits of each of `rows` rows, from the largest, equal ones by index (-0 equals 0,
+   NaN is larger than every number), with their indices, and what is left:
+     rest = log of the sum over all other tokens of exp(logits / temperature),
+   -inf where there is none or all are -inf, NaN where NaN or +inf is among them. */
+typedef struct {
+  int64_t rows, vocab;           /* >= 0, in [1, HIMUON_TOP_VOCAB]                      */
+  int64_t ld_logits, ld_top;     /* leading dimensions: of logits, >= vocab; of value and
+                                    index, >= k                                         */
+  const void *logits;            /* device, dtype                                       */
+  void *value;                   /* device, dtype, rows x k                             */
+  int64_t *index;                /* device, rows x k                                    */
+  float *rest;                   /* device, rows                                        */
+  int32_t k;                     /* in [1, min(vocab, HIMUON_TOP_MOST)]                 */
+  himuon_dtype dtype;
+  double temperature;            /* in [2^-20, 2^20]                                    */
+} himuon_top;
+
+/* Workspace bytes himuon_top_logits needs for this call (as above). */
+HIMUON_API himuon_status himuon_top_workspace(const himuon_top *p, size_t *bytes);
+
+/* Enqueues the selection on hip_stream; the same call gives the same bits.  Errors as for
+   himuon_sample. */
+HIMUON_API himuon_status himuon_top_logits(const himuon_top *p, void *workspace, size_t ws_bytes, void *hip_stream);
 
 /* Distillation from a teacher's top logits, over `rows` tokens with `vocab` student logits each.
    Entry j of a row (j < k) names token v_j = index[j] with the teacher's logit value[j]; an entry

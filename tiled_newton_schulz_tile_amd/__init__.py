@@ -19,8 +19,9 @@ __all__ = [
     "himuon_plan_stats", "himuon_plan_tiles", "himuon_plan_destroy", "himuon_last_error",
     "himuon_plan_runtime_counts", "himuon_runtime_counts", "himuon_step_static", "STATIC_WORKSPACE_BYTES",
     "himuon_stream_step",
-    "himuon_policy", "himuon_policy_workspace", "himuon_policy_loss", "himuon_distill", "himuon_distill_workspace",
-    "himuon_distill_loss", "TOP_MOST", "TOP_VOCAB", "himuon_grad", "himuon_grad_norm_workspace",
+    "himuon_policy", "himuon_policy_workspace", "himuon_policy_loss", "himuon_sampling", "himuon_sample_workspace",
+    "himuon_sample", "himuon_top", "himuon_top_workspace", "himuon_top_logits", "himuon_distill",
+    "himuon_distill_workspace", "himuon_distill_loss", "TOP_MOST", "TOP_VOCAB", "himuon_grad", "himuon_grad_norm_workspace",
     "himuon_grad_norm", "himuon_adamw_tensor", "himuon_adamw_config", "himuon_adamw_step",
     "himuon_adamw_table_size", "himuon_adamw_table", "ADAMW_BLOCK",
     "HiMuon", "CUBIC", "QUINTIC", "TILE_FULL", "F32", "BF16", "PREC_F32", "PREC_BF16",
@@ -46,8 +47,10 @@ STATUS = {0: "HIMUON_OK", -1: "HIMUON_EINVAL", -2: "HIMUON_EBUDGET", -3: "HIMUON
 EXPORTED = ("himuon_plan", "himuon_workspace_size", "himuon_step", "himuon_set_tile_schedule",
             "himuon_plan_stats", "himuon_plan_tiles", "himuon_plan_destroy", "himuon_last_error",
             "himuon_plan_runtime_counts", "himuon_step_static", "himuon_stream_step", "himuon_sign_pack",
-            "himuon_sign_vote", "himuon_policy_workspace", "himuon_policy_loss", "himuon_distill_workspace",
-            "himuon_distill_loss", "himuon_grad_norm_workspace", "himuon_grad_norm", "himuon_adamw_step", "himuon_adamw_table_size", "himuon_adamw_table")
+            "himuon_sign_vote", "himuon_policy_workspace", "himuon_policy_loss", "himuon_sample_workspace",
+            "himuon_sample", "himuon_top_workspace", "himuon_top_logits", "himuon_distill_workspace", "himuon_distill_loss",
+            "himuon_grad_norm_workspace", "himuon_grad_norm", "himuon_adamw_step", "himuon_adamw_table_size",
+            "himuon_adamw_table")
 
 
 class HiMuonError(RuntimeError):
@@ -103,6 +106,23 @@ class himuon_policy(ctypes.Structure):
                 ("ref_logp", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("stats", ctypes.c_void_p),
                 ("dtype", ctypes.c_int), ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
                 ("kl_coef", ctypes.c_double), ("temperature", ctypes.c_double), ("grad_scale", ctypes.c_double)]
+
+
+class himuon_sampling(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("ld_logits", ctypes.c_int64),
+                ("logits", ctypes.c_void_p), ("uniform", ctypes.c_void_p), ("row_temperature", ctypes.c_void_p),
+                ("row_top_k", ctypes.c_void_p), ("row_top_p", ctypes.c_void_p), ("row_min_p", ctypes.c_void_p),
+                ("token", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("kept", ctypes.c_void_p),
+                ("dtype", ctypes.c_int), ("top_k", ctypes.c_int32), ("temperature", ctypes.c_double),
+                ("top_p", ctypes.c_double), ("min_p", ctypes.c_double)]
+
+
+class himuon_top(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("ld_logits", ctypes.c_int64), ("ld_top", ctypes.c_int64),
+                ("logits", ctypes.c_void_p), ("value", ctypes.c_void_p), ("index", ctypes.c_void_p),
+                ("rest", ctypes.c_void_p), ("k", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("temperature", ctypes.c_double)]
 
 
 class himuon_distill(ctypes.Structure):
@@ -162,6 +182,10 @@ def _load() -> ctypes.CDLL:
                                      P, ctypes.c_float, P]
     lib.himuon_policy_workspace.argtypes = [ctypes.POINTER(himuon_policy), ctypes.POINTER(ctypes.c_size_t)]
     lib.himuon_policy_loss.argtypes = [ctypes.POINTER(himuon_policy), P, ctypes.c_size_t, P]
+    lib.himuon_sample_workspace.argtypes = [ctypes.POINTER(himuon_sampling), ctypes.POINTER(ctypes.c_size_t)]
+    lib.himuon_sample.argtypes = [ctypes.POINTER(himuon_sampling), P, ctypes.c_size_t, P]
+    lib.himuon_top_workspace.argtypes = [ctypes.POINTER(himuon_top), ctypes.POINTER(ctypes.c_size_t)]
+    lib.himuon_top_logits.argtypes = [ctypes.POINTER(himuon_top), P, ctypes.c_size_t, P]
     lib.himuon_distill_workspace.argtypes = [ctypes.POINTER(himuon_distill), ctypes.POINTER(ctypes.c_size_t)]
     lib.himuon_distill_loss.argtypes = [ctypes.POINTER(himuon_distill), P, ctypes.c_size_t, P]
     lib.himuon_grad_norm_workspace.argtypes = [ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]
@@ -269,6 +293,26 @@ def himuon_policy_workspace(p: himuon_policy) -> int:
 
 def himuon_policy_loss(p: himuon_policy, workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> None:
     _check(_lib.himuon_policy_loss(ctypes.byref(p), workspace_ptr or None, ws_bytes, stream_ptr or None))
+
+
+def himuon_sample_workspace(p: himuon_sampling) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.himuon_sample_workspace(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+def himuon_sample(p: himuon_sampling, workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> None:
+    _check(_lib.himuon_sample(ctypes.byref(p), workspace_ptr or None, ws_bytes, stream_ptr or None))
+
+
+def himuon_top_workspace(p: himuon_top) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.himuon_top_workspace(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+def himuon_top_logits(p: himuon_top, workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> None:
+    _check(_lib.himuon_top_logits(ctypes.byref(p), workspace_ptr or None, ws_bytes, stream_ptr or None))
 
 
 def himuon_distill_workspace(p: himuon_distill) -> int:

@@ -196,6 +196,12 @@ hipError_t launch_grad_norm(const himuon_grad *tensors, int32_t n_tensors, bool 
 size_t policy_workspace(const himuon_policy &p);
 hipError_t launch_policy(const himuon_policy &p, void *workspace, hipStream_t stream);
 
+// ---- sampling and a row's top logits (select.hip) --------------------------------
+size_t sample_workspace(const himuon_sampling &p);
+hipError_t launch_sample(const himuon_sampling &p, void *workspace, hipStream_t stream);
+size_t top_workspace(const himuon_top &p);
+hipError_t launch_top(const himuon_top &p, void *workspace, hipStream_t stream);
+
 // ---- distillation from a teacher's top logits (distill.hip) ----------------------
 size_t distill_workspace(const himuon_distill &p);
 hipError_t launch_distill(const himuon_distill &p, void *workspace, hipStream_t stream);

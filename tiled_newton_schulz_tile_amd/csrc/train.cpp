@@ -49,16 +49,42 @@ himuon_status check_policy(const himuon_policy *p) {
 
 bool is_temperature(double t) { return t >= 0x1p-20 && t <= 0x1p20; }
 
+himuon_status check_rows(int64_t rows, int64_t vocab, int64_t ld_logits, himuon_dtype dtype) {
+  if (rows < 0 || rows > kMostElements) return bad("rows must be in [0, 2^40]");
+  if (vocab < 1 || vocab > HIMUON_TOP_VOCAB) return bad("vocab must be in [1, 2^20]");
+  if (!is_dtype(dtype)) return bad("dtype");
+  if (ld_logits < vocab || ld_logits > kMostElements) return bad("ld_logits must be in [vocab, 2^40]");
+  return HIMUON_OK;
+}
+
+himuon_status check_sample(const himuon_sampling *p) {
+  if (!p) return bad("NULL argument");
+  const himuon_status s = check_rows(p->rows, p->vocab, p->ld_logits, p->dtype);
+  if (s != HIMUON_OK) return s;
+  if (!(p->temperature == 0 || is_temperature(p->temperature))) return bad("temperature must be 0 or in [2^-20, 2^20]");
+  if (std::isnan(p->top_p) || std::isnan(p->min_p)) return bad("top_p and min_p must be numbers");
+  return HIMUON_OK;
+}
+
+himuon_status check_top(const himuon_top *p) {
+  if (!p) return bad("NULL argument");
+  const himuon_status s = check_rows(p->rows, p->vocab, p->ld_logits, p->dtype);
+  if (s != HIMUON_OK) return s;
+  if (p->k < 1 || p->k > HIMUON_TOP_MOST || p->k > p->vocab) return bad("k must be in [1, min(vocab, 1024)]");
+  if (p->ld_top < p->k || p->ld_top > kMostElements) return bad("ld_top must be in [k, 2^40]");
+  if (!is_temperature(p->temperature)) return bad("temperature must be in [2^-20, 2^20]");
+  return HIMUON_OK;
+}
+
 himuon_status check_distill(const himuon_distill *p) {
   if (!p) return bad("NULL argument");
-  if (p->rows < 0 || p->rows > kMostElements) return bad("rows must be in [0, 2^40]");
-  if (p->vocab < 1 || p->vocab > HIMUON_TOP_VOCAB) return bad("vocab must be in [1, 2^20]");
-  if (!is_dtype(p->dtype) || !is_dtype(p->value_dtype)) return bad("dtype");
+  const himuon_status s = check_rows(p->rows, p->vocab, p->ld_logits, p->dtype);
+  if (s != HIMUON_OK) return s;
+  if (!is_dtype(p->value_dtype)) return bad("dtype");
   if (p->k < 1 || p->k > HIMUON_TOP_MOST) return bad("k must be in [1, 1024]");
-  if (p->ld_logits < p->vocab || p->ld_top < p->k) return bad("ld_logits must be >= vocab and ld_top >= k");
-  if (p->dlogits && p->ld_dlogits < p->vocab) return bad("ld_dlogits must be >= vocab");
-  if (p->ld_logits > kMostElements || p->ld_top > kMostElements || (p->dlogits && p->ld_dlogits > kMostElements))
-    return bad("leading dimension too large");
+  if (p->ld_top < p->k || p->ld_top > kMostElements) return bad("ld_top must be in [k, 2^40]");
+  if (p->dlogits && (p->ld_dlogits < p->vocab || p->ld_dlogits > kMostElements))
+    return bad("ld_dlogits must be in [vocab, 2^40]");
   if (p->dlogits && p->dlogits == p->logits && p->ld_dlogits != p->ld_logits)
     return bad("dlogits in the place of logits needs the same leading dimension");
   if (!is_temperature(p->temperature)) return bad("temperature must be in [2^-20, 2^20]");
@@ -109,6 +135,46 @@ HIMUON_API himuon_status himuon_policy_loss(const himuon_policy *p, void *worksp
   if ((s = check_workspace(workspace, ws_bytes, himuon::policy_workspace(*p))) != HIMUON_OK) return s;
   return launched(himuon::launch_policy(*p, workspace, reinterpret_cast<hipStream_t>(hip_stream)),
                   "policy loss launch");
+} catch (...) {
+  return HIMUON_ENOMEM;
+}
+
+HIMUON_API himuon_status himuon_sample_workspace(const himuon_sampling *p, size_t *bytes) try {
+  if (!bytes) return bad("NULL argument");
+  himuon_status s = check_sample(p);
+  if (s != HIMUON_OK) return s;
+  *bytes = himuon::sample_workspace(*p);
+  return HIMUON_OK;
+} catch (...) {
+  return HIMUON_ENOMEM;
+}
+
+HIMUON_API himuon_status himuon_sample(const himuon_sampling *p, void *workspace, size_t ws_bytes, void *hip_stream) try {
+  himuon_status s = check_sample(p);
+  if (s != HIMUON_OK) return s;
+  if (p->rows > 0 && (!p->logits || !p->uniform || !p->token || !p->logp || !p->kept)) return bad("NULL pointer");
+  if ((s = check_workspace(workspace, ws_bytes, himuon::sample_workspace(*p))) != HIMUON_OK) return s;
+  return launched(himuon::launch_sample(*p, workspace, reinterpret_cast<hipStream_t>(hip_stream)), "sampling launch");
+} catch (...) {
+  return HIMUON_ENOMEM;
+}
+
+HIMUON_API himuon_status himuon_top_workspace(const himuon_top *p, size_t *bytes) try {
+  if (!bytes) return bad("NULL argument");
+  himuon_status s = check_top(p);
+  if (s != HIMUON_OK) return s;
+  *bytes = himuon::top_workspace(*p);
+  return HIMUON_OK;
+} catch (...) {
+  return HIMUON_ENOMEM;
+}
+
+HIMUON_API himuon_status himuon_top_logits(const himuon_top *p, void *workspace, size_t ws_bytes, void *hip_stream) try {
+  himuon_status s = check_top(p);
+  if (s != HIMUON_OK) return s;
+  if (p->rows > 0 && (!p->logits || !p->value || !p->index || !p->rest)) return bad("NULL pointer");
+  if ((s = check_workspace(workspace, ws_bytes, himuon::top_workspace(*p))) != HIMUON_OK) return s;
+  return launched(himuon::launch_top(*p, workspace, reinterpret_cast<hipStream_t>(hip_stream)), "top logits launch");
 } catch (...) {
   return HIMUON_ENOMEM;
 }

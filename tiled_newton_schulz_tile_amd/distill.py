@@ -1,6 +1,7 @@
-"""Distillation over torch tensors: himuon_distill_loss of libhimuon.
+"""Distillation over torch tensors: himuon_top_logits and himuon_distill_loss of libhimuon.
 
-distill_loss takes the entries that a teacher kept of each token's distribution and gives the
+top_logits gives what a teacher keeps of each token's distribution: its k largest logits, their
+tokens and the log-sum-exp of the others.  distill_loss takes them and gives the
 divergence to the student's softmax and, where it is asked for, its gradient with respect to the
 student's logits, which a training program hands to torch (``logits.backward(got.dlogits)``; the
 loss itself has no graph).  Formulas and conventions: include/himuon.h.
@@ -11,9 +12,37 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import himuon_distill, himuon_distill_loss, himuon_distill_workspace
+from . import (himuon_distill, himuon_distill_loss, himuon_distill_workspace, himuon_top, himuon_top_logits,
+               himuon_top_workspace)
 from .adamw import _empty, _launch
 from .policy import _DTYPES, _leading, _row
+
+
+class TopLogits(NamedTuple):
+    value: object      # logits' dtype (N, k): the largest logits, from the largest
+    index: object      # int64 (N, k): their tokens
+    rest: object       # float32 (N): log-sum-exp of the others / temperature
+
+
+def top_logits(logits, k: int, temperature: float = 1.0, stream=None) -> TopLogits:
+    """The k largest logits (k up to 1024) of each row of the (N, V) float32 or bfloat16 CUDA tensor `logits` (unit column
+    stride, any row stride; V up to 2^20), equal ones by index, and the log-sum-exp of the others over the temperature.
+    stream: as for policy_loss."""
+    N, V, ld = _logits(logits)
+    dev = logits.device
+    p = himuon_top(N, V, ld, k, logits.data_ptr(), None, None, None, k, _DTYPES[logits.dtype], temperature)
+    need = himuon_top_workspace(p)
+
+    def empty(size, dtype):
+        return torch.empty(size, dtype=dtype, device=dev) if stream is None else _empty(torch, stream, size, dtype)
+
+    value, index = empty((N, k), logits.dtype), empty((N, k), torch.int64)
+    buf = empty((need // 4 + N,), torch.float32)   # workspace (whole words), rest
+    p.value, p.index, p.rest = value.data_ptr(), index.data_ptr(), buf.data_ptr() + need
+    if stream is not None:
+        logits.record_stream(stream)
+    _launch(torch, dev, stream, himuon_top_logits, p, buf.data_ptr(), need)
+    return TopLogits(value, index, buf[need // 4:])
 
 
 class DistillLoss(NamedTuple):
@@ -32,13 +61,8 @@ def distill_loss(logits, value, index, weight, rest=None, temperature: float = 1
     row with weight 0 is left out.  rest: float32 (N), the log-sum-exp of the teacher's other logits / temperature, or
     None: the teacher's probabilities are those of its entries alone.  dlogits, stream: as for policy_loss; loss, kl and
     the workspace share one allocation of the call."""
-    if logits.dim() != 2 or logits.dtype not in _DTYPES or not logits.is_cuda:
-        raise ValueError("logits must be a 2-D float32 or bfloat16 CUDA tensor")
-    N, V = logits.shape
-    if V < 1:
-        raise ValueError("logits must have at least one column")
+    N, V, ld = _logits(logits)
     dev = logits.device
-    ld = _leading(logits, "logits", N, V)
     if value.dim() != 2 or value.dtype not in _DTYPES or value.shape[0] != N or value.device != dev:
         raise ValueError(f"value must be a float32 or bfloat16 tensor of {N} rows on {dev}")
     k = value.shape[1]
@@ -77,3 +101,13 @@ def distill_loss(logits, value, index, weight, rest=None, temperature: float = 1
         torch.autograd.graph.increment_version(dlogits)   # a backward pass that saved what stood here has to say so
     loss, _, kl = buf.split_with_sizes((1, 3 + need // 4, N))
     return DistillLoss(loss[0], kl, dlogits)
+
+
+def _logits(logits):
+    """(rows, columns, row stride) of a tensor of logits."""
+    if logits.dim() != 2 or logits.dtype not in _DTYPES or not logits.is_cuda:
+        raise ValueError("logits must be a 2-D float32 or bfloat16 CUDA tensor")
+    N, V = logits.shape
+    if V < 1:
+        raise ValueError("logits must have at least one column")
+    return N, V, _leading(logits, "logits", N, V)
