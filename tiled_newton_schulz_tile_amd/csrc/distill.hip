@@ -9,8 +9,10 @@
 // A bitmap of the row in LDS says which logits are named; those are taken out of the row's
 // vectors (-inf in their place) and come from the entries instead, a few a row.
 //
-// All sums, maxima and exponents are fp32 (the sum over rows fp64); the only rounding to fewer
-// bits is that of the gradient to bf16 logits' own type.
+// The rest's sums, maxima and exponents are fp32.  The gradient of a named token is a difference of
+// two probabilities that may both be near 1: the few powers and sums that it takes are fp64, as is
+// the sum over rows.  The only rounding to fewer bits is that of the gradient to bf16 logits' own
+// type.
 #include "device_common.h"
 #include "himuon_internal.h"
 #include "row_softmax.h"
@@ -18,57 +20,68 @@
 namespace himuon {
 namespace {
 
-// Constants of a call in fp32.
 struct DistillParams {
   const void *value;
   const int64_t *index;
   const float *rest, *weight;
   float *kl;
   unsigned *ticket;   // workspace, of rows that are cut into spans: counts the rows that are done,
-  f32x4 *spans;       // per row and span the rest's and the named tokens' largest logit and sum,
-  float *entry_z;     // and the student's logit of every entry
+  f32x2 *spans;       // per row and span the rest's largest logit and sum,
+  f32x2 *entry;       // and of every entry the student's logit, and 1 if it is the first of its token
   int64_t ld_logits, ld_dlogits, ld_top;
   int32_t vocab, entries, value_bf16;
-  float k;            // log2(e) / temperature
-  float inv_temp;     // 1 / temperature
-  float coef;         // grad_scale / temperature
+  float k;                        // log2(e) / temperature
+  float coef;                     // grad_scale / temperature
+  double fine_k, temp, inv_temp;  // log2(e) / temperature, temperature, 1 / temperature
 };
 
 constexpr int kNone = -1;   // an entry that does not count
 
-// A row's entries in LDS, and the bitmap of the tokens that they name.
+// A row's entries in LDS, what they sum to, and the bitmap of the tokens that they name: a byte for
+// each vector of the row, at the place that marks() gives it.
+struct EntrySums {
+  unsigned named_max, teacher_max;   // ordered bits of the largest logits; 0: none
+  int twice;                         // not 0: some token is named more than once
+  double named[16], teacher[16];     // sums of powers, by wave
+};
 struct EntryLds {
   int *token;        // kNone, or the token
-  float *t, *z;      // the teacher's logit over the temperature, the student's logit
-  unsigned *bits;
-  int *twice;        // not 0: some token is named more than once
+  float *t, *z;      // the teacher's logit, the student's logit
+  unsigned char *marks;
 };
-__device__ __forceinline__ EntryLds entry_lds(unsigned *lds, int entries) {
-  return {reinterpret_cast<int *>(lds) + 1, reinterpret_cast<float *>(lds) + 1 + entries,
-          reinterpret_cast<float *>(lds) + 1 + 2 * entries, lds + 1 + 3 * entries, reinterpret_cast<int *>(lds)};
+__device__ __forceinline__ EntryLds entry_lds(u32x4 *lds, size_t mark_bytes, int entries) {
+  float *f = reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + mark_bytes);
+  return {reinterpret_cast<int *>(f), f + entries, f + 2 * entries, reinterpret_cast<unsigned char *>(lds)};
 }
-size_t entry_lds_bytes(int64_t bits, int entries) { return (1 + 3 * (size_t)entries + (size_t)(bits + 31) / 32) * 4; }
+size_t entry_lds_bytes(size_t mark_bytes, int entries) { return mark_bytes + 12 * (size_t)entries; }
 
 __device__ __forceinline__ float entry_value(const DistillParams &p, int64_t at) {
   return p.value_bf16 ? bf16_bits_to_f32(gmem(reinterpret_cast<const unsigned short *>(p.value))[at])
                       : gmem(reinterpret_cast<const float *>(p.value))[at];
 }
+__device__ __forceinline__ unsigned ordered(float x) {
+  const unsigned u = __builtin_bit_cast(unsigned, x);
+  return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+}
+// The reference of a softmax from its largest logit's ordered bits (0 where there is none or it is
+// -inf, whose powers are 0 then).
+__device__ __forceinline__ float ordered_ref(unsigned o) {
+  return o == 0 ? 0.f : ref_of(__builtin_bit_cast(float, o ^ (o >> 31 ? 0x80000000u : 0xffffffffu)));
+}
 
-// Entry j as it counts: each sum over named tokens takes a token once, at its first entry.
-__device__ __forceinline__ bool first_of_token(const EntryLds &e, int j, int token, bool twice) {
-  if (token == kNone) return false;
+// Marks element e of the vector whose byte is at `at`; one that is marked already is named twice.
+__device__ __forceinline__ void mark(unsigned char *marks, int at, int e, EntrySums &sums) {
+  const unsigned bit = 1u << (8 * (at & 3) + e);
+  if (atomicOr(reinterpret_cast<unsigned *>(marks) + (at >> 2), bit) & bit) sums.twice = 1;
+}
+// Whether entry j stands for its token in sums over named tokens: the token's first entry does.
+__device__ __forceinline__ bool first_of_token(const EntryLds &e, int j, bool twice) {
   if (twice)
     for (int i = 0; i < j; ++i)
-      if (e.token[i] == token) return false;
+      if (e.token[i] == e.token[j]) return false;
   return true;
 }
-
-// The bits of a vector's elements; -inf in the place of those that are set.
-template <class T>
-__device__ __forceinline__ unsigned vector_bits(const unsigned *bits, int vec) {
-  const unsigned b = reinterpret_cast<const unsigned char *>(bits)[Vec<T>::N == 8 ? vec : vec >> 1];
-  return Vec<T>::N == 8 ? b : b >> 4 * (vec & 1) & 15u;
-}
+// -inf in the place of the marked elements of a vector.
 template <class T>
 __device__ __forceinline__ void hide(u32x4 &v, unsigned b) {
 #pragma unroll
@@ -84,103 +97,96 @@ __device__ __forceinline__ void hide(u32x4 &v, unsigned b) {
   }
 }
 
-// A softmax in parts: the largest logit (-inf: none) and the sum of powers of the distances to it.
-struct Part {
-  float max, sum;
-};
-__device__ __forceinline__ void add(Part &s, float z, float k) {
-  const float m = __builtin_fmaxf(s.max, z), to = ref_of(m);
-  s.sum = s.sum * pow2(s.max, k, to) + pow2(z, k, to);
-  s.max = m;
-}
-__device__ __forceinline__ Part join(Part a, Part b, float k) {
-  const float m = __builtin_fmaxf(a.max, b.max), to = ref_of(m);
-  return {m, a.sum * pow2(a.max, k, to) + b.sum * pow2(b.max, k, to)};
-}
-__device__ __forceinline__ Part wave_join(Part s, float k) {
-  const float m = wave_max(s.max);
-  return {m, wave_sum(s.sum * pow2(s.max, k, ref_of(m)))};
-}
-// M softmaxes over a block of W waves; lds holds W M entries.
-template <int W, int M>
-__device__ __forceinline__ void block_join(Part (&s)[M], const float (&k)[M], Part *lds) {
+// The rest's softmax of a block of W waves from its threads' largest logits and sums.
+template <int W>
+__device__ __forceinline__ Softmax rest_join(float max, float sum, float k, Softmax *lds) {
   const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    s[i] = wave_join(s[i], k[i]);
-    if (W > 1 && lane == 0) lds[(threadIdx.x >> 6) * M + i] = s[i];
-  }
-  if constexpr (W == 1) return;
+  float m = wave_max(max);
+  sum = wave_sum(sum * pow2(max, k, ref_of(m)));
+  if (lane == 0) lds[threadIdx.x >> 6] = {m, sum};
   lds_barrier();
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    s[i] = {-__builtin_inff(), 0.f};
-    if (lane < W) s[i] = lds[lane * M + i];
-    s[i] = wave_join(s[i], k[i]);
-  }
+  const Softmax s = lds[lane % W];
+  m = wave_max(s.ref);
+  return {m, wave_sum(lane < W ? s.sum * pow2(s.ref, k, ref_of(m)) : 0.f)};
 }
 
 // What a row's gradient and divergence need, the same in every thread.
 struct RowCoefs {
-  bool live;            // the teacher has some probability
-  float ref, inv_sum, log_sum;     // the student's softmax over all tokens
-  float teacher_ref, teacher_inv, teacher_log;
-  float rest_ref, rest_f;          // a token u of the rest: gradient rest_f 2^((z_u - rest_ref) k)
-  float coef;                      // of the row's gradient
-  float rest_kl;                   // the rest's part of the divergence
+  bool live;                         // the teacher has some probability
+  float named_ref, teacher_ref;      // of the entries' powers, and what these are multiplied with to be
+  double named_f, teacher_f;         //   probabilities
+  float ref;                         // the student's softmax over all tokens: the largest logit
+  double sum, teacher_sum;           //   and the sum; the teacher's sum
+  float rest_ref, rest_f;            // a token u of the rest: gradient rest_f 2^((z_u - rest_ref) k)
+  float coef;                        // of the row's gradient
+  float q_rest;
 };
-__device__ __forceinline__ RowCoefs row_coefs(Part rest, Part named, Part teacher, float teacher_rest, float weight,
-                                              const DistillParams &p) {
+__device__ __forceinline__ double power(double z, float ref, const DistillParams &p) {
+  return pow2_exact((z - ref) * p.fine_k);
+}
+
+// rest: the rest's largest logit (-inf: none) and sum; waves: those that left sums of entries;
+// teacher_rest: times the temperature, as the teacher's logits are.
+__device__ __forceinline__ RowCoefs row_coefs(Softmax rest, const EntrySums &sums, int waves, double teacher_rest,
+                                              float weight, const DistillParams &p) {
   RowCoefs r;
-  r.live = !(teacher.max == -__builtin_inff() && teacher.sum == 0.f);
-  const Part all = join(rest, named, p.k);
-  r.ref = ref_of(all.max);
-  r.inv_sum = 1.f / all.sum;
-  r.log_sum = kLn2 * __builtin_amdgcn_logf(all.sum);
-  r.teacher_ref = ref_of(teacher.max);
-  r.teacher_inv = 1.f / teacher.sum;
-  r.teacher_log = kLn2 * __builtin_amdgcn_logf(teacher.sum);
-  const float q = pow2(teacher_rest, (float)kLog2e, r.teacher_ref) * r.teacher_inv;
-  r.rest_ref = ref_of(rest.max);
-  r.coef = weight * p.coef * (teacher.sum == teacher.sum ? 1.f : teacher.sum);
-  float f = pow2(rest.max, p.k, r.ref) * r.inv_sum;
-  r.rest_kl = 0.f;
-  if (!(q <= 0.f)) {
-    f -= rest.sum > 0.f ? q / rest.sum : 0.f;   // (a rest of probability 0 has a gradient of 0 and an infinite divergence)
-    const float lp = rest.sum > 0.f ? (rest.max - r.ref) * p.inv_temp + kLn2 * __builtin_amdgcn_logf(rest.sum) - r.log_sum
-                                    : rest.sum - __builtin_inff();
-    r.rest_kl = q * ((teacher_rest - r.teacher_ref) - r.teacher_log - lp);
+  double named = 0, teacher = 0;
+  for (int i = 0; i < waves; ++i) {
+    named += sums.named[i];
+    teacher += sums.teacher[i];
   }
+  r.live = !(teacher == 0);
+  r.named_ref = ordered_ref(sums.named_max);
+  r.teacher_ref = ordered_ref(sums.teacher_max);
+  r.rest_ref = ref_of(rest.ref);
+  const float named_max = named == 0 ? -__builtin_inff() : r.named_ref;
+  r.ref = ref_of(__builtin_fmaxf(rest.ref, named_max));
+  const double named_scale = power(named_max, r.ref, p), rest_scale = power(rest.ref, r.ref, p);
+  r.sum = named * named_scale + (double)rest.sum * rest_scale;
+  const double inv = 1. / r.sum;
+  r.named_f = named_scale * inv;
+  r.teacher_sum = teacher;
+  r.teacher_f = 1. / teacher;
+  r.q_rest = (float)(power(teacher_rest, r.teacher_ref, p) * r.teacher_f);
+  r.coef = weight * p.coef * (teacher == teacher ? 1.f : (float)teacher);
+  float f = (float)(rest_scale * inv);
+  // (a rest of probability 0 has a gradient of 0 and an infinite divergence)
+  if (!(r.q_rest <= 0.f)) f -= rest.sum > 0.f ? r.q_rest / rest.sum : 0.f;
   r.rest_f = r.coef * f;
   return r;
 }
-__device__ __forceinline__ float entry_q(float t, const RowCoefs &r) {
-  return pow2(t, (float)kLog2e, r.teacher_ref) * r.teacher_inv;
-}
-// One wave: the row's divergence (every lane has it).
-__device__ __forceinline__ float row_kl(const EntryLds &e, const RowCoefs &r, const DistillParams &p) {
-  float kl = 0.f;
+// One wave: the row's divergence (every lane has it).  Its terms are far larger than their sum
+// where the student is near the teacher: fp64.
+__device__ __forceinline__ float row_kl(const EntryLds &e, const RowCoefs &r, Softmax rest, double teacher_rest,
+                                        const DistillParams &p) {
+  const double shift = log(r.sum) - log(r.teacher_sum);
+  double kl = 0;
   for (int j = threadIdx.x & 63; j < p.entries; j += 64) {
     if (e.token[j] == kNone) continue;
-    const float t = e.t[j], q = entry_q(t, r);
-    if (q != 0.f) kl += q * ((t - r.teacher_ref) - r.teacher_log - ((e.z[j] - r.ref) * p.inv_temp - r.log_sum));
+    const double q = power(e.t[j], r.teacher_ref, p) * r.teacher_f;
+    if (q != 0) kl += q * ((((double)e.t[j] - r.teacher_ref) - ((double)e.z[j] - r.ref)) * p.inv_temp + shift);
   }
-  return wave_sum(kl) + r.rest_kl;
+  kl = wave_sum(kl);
+  if (!(r.q_rest <= 0.f)) {
+    const double q = power(teacher_rest, r.teacher_ref, p) * r.teacher_f;
+    kl += q * (((teacher_rest - r.teacher_ref) - ((double)rest.ref - r.ref)) * p.inv_temp + shift - log((double)rest.sum));
+  }
+  return (float)kl;
 }
 // The gradient of entry j's token: the entries of one token write the same value.
 __device__ __forceinline__ float entry_gradient(const EntryLds &e, int j, bool twice, const RowCoefs &r,
                                                 const DistillParams &p) {
   const int token = e.token[j];
-  float q = 0.f;
+  double q = 0;
   if (twice) {
     for (int i = 0; i < p.entries; ++i)
-      if (e.token[i] == token) q += entry_q(e.t[i], r);
+      if (e.token[i] == token) q += power(e.t[i], r.teacher_ref, p);
   } else {
-    q = entry_q(e.t[j], r);
+    q = power(e.t[j], r.teacher_ref, p);
   }
-  return r.coef * (pow2(e.z[j], p.k, r.ref) * r.inv_sum - q);
+  return (float)(r.coef * (power(e.z[j], r.named_ref, p) * r.named_f - q * r.teacher_f));
 }
-// A vector of the rest's gradient, but for the elements that are named.
+// A vector of the rest's gradient, but for the elements that are marked.
 template <class T, bool NT>
 __device__ __forceinline__ void rest_gradient(T *dz, u32x4 v, unsigned b, const RowCoefs &r, float k) {
   constexpr int N = Vec<T>::N;
@@ -199,32 +205,55 @@ __device__ __forceinline__ void rest_gradient(T *dz, u32x4 v, unsigned b, const 
 
 enum { kForward = 0, kGradient = 1, kGradientNT = 2 };
 
+// A row's marks: a byte for each held vector, K a thread side by side, so that a thread has its own
+// with one load; then the other vectors' bits, in order; then a byte for each of the row's last V % N
+// elements.  Where those start, and how many bytes all take (2^20 logits: 152 KB with the entries).
+__host__ __device__ constexpr int tail_marks_of(int64_t vecs, int n, int held) {
+  return held + (int)(((vecs > held ? vecs - held : 0) * n + 7) / 8);
+}
+__host__ __device__ constexpr size_t row_mark_bytes(int64_t vecs, int n, int held) {
+  return ((size_t)tail_marks_of(vecs, n, held) + 8 + 15) / 16 * 16;
+}
+template <class T, int HELD>
+__device__ __forceinline__ unsigned long_marks(const unsigned char *marks, int vec) {
+  const int bit = (vec - HELD) * Vec<T>::N;
+  return Vec<T>::N == 8 ? marks[HELD + (bit >> 3)] : marks[HELD + (bit >> 3)] >> (bit & 7) & 15u;
+}
+
 // One block per row: K vectors of 16 bytes a thread are held in registers between the softmax and
 // the gradient, and where the row is LONG the vectors behind them are read again for the gradient.
+// A forward pass over a LONG row holds none.
 template <typename T, int THR, int K, bool LONG, int OUT>
 __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dlogits, DistillParams p) {
-  constexpr int N = Vec<T>::N;
+  constexpr int N = Vec<T>::N, HELD = THR * K;
   constexpr bool GRAD = OUT != kForward, NT = OUT == kGradientNT;
-  extern __shared__ unsigned lds[];
-  __shared__ Part parts[THR / 64 * 3];
+  extern __shared__ u32x4 lds[];
+  __shared__ EntrySums sums;
+  __shared__ Softmax parts[THR / 64];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, V = p.vocab, vecs = V / N, tail_at = vecs * N + tid;
+  const size_t mark_bytes = row_mark_bytes(LONG ? vecs : 0, N, HELD);
+  const int tail_marks = tail_marks_of(LONG ? vecs : 0, N, HELD);
   const T *z = logits + row * p.ld_logits;
   T *dz = GRAD ? dlogits + row * p.ld_dlogits : nullptr;
-  const EntryLds e = entry_lds(lds, p.entries);
+  const EntryLds e = entry_lds(lds, mark_bytes, p.entries);
   const float w = gmem(p.weight)[row];
-  if (w == 0.f) {
-    if (tid == 0) gmem(p.kl)[row] = 0.f;
-    if constexpr (GRAD) zero_row<T, THR, NT>(dz, V);
-    return;
-  }
-  const float teacher_rest = p.rest ? gmem(p.rest)[row] : -__builtin_inff();
   int64_t token = kNone;   // of the thread's first entry
   float value = 0.f;
   if (tid < p.entries) {
     token = gmem(p.index)[row * p.ld_top + tid];
     value = entry_value(p, row * p.ld_top + tid);
   }
+  const double teacher_rest = p.rest ? gmem(p.rest)[row] * p.temp : -__builtin_inf();
+  for (int i = tid; i < (int)(mark_bytes / 16); i += THR) lds[i] = u32x4{0, 0, 0, 0};
+  if (tid == 0) sums.named_max = sums.teacher_max = sums.twice = 0;
+  if (w == 0.f) {
+    if (tid == 0) gmem(p.kl)[row] = 0.f;
+    if constexpr (GRAD) zero_row<T, THR, NT>(dz, V);
+    return;
+  }
+  bool counts = token >= 0 && token < V;
+  float student = counts ? Vec<T>::load1(z + token) : 0.f;
   u32x4 v[K > 0 ? K : 1];
 #pragma unroll
   for (int i = 0; i < K; ++i) {
@@ -232,38 +261,61 @@ __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dl
     if (LONG || tid + i * THR < vecs) v[i] = Vec<T>::load(z + (tid + i * THR) * N);
   }
   float tail = tail_at < V ? Vec<T>::load1(z + tail_at) : -__builtin_inff();
+  lds_barrier();
 
-  for (int i = tid; i < (V + 31) / 32; i += THR) e.bits[i] = 0;
-  if (tid == 0) *e.twice = 0;
-  lds_barrier();
-  Part sums[3] = {{-__builtin_inff(), 0.f}, {-__builtin_inff(), 0.f}, {-__builtin_inff(), 0.f}};   // rest, named, teacher
-  for (int j = tid; j < p.entries; j += THR) {
-    if (j != tid) {
-      token = gmem(p.index)[row * p.ld_top + j];
-      value = entry_value(p, row * p.ld_top + j);
+  // the entries: what they name is marked, their largest logits are found
+  const int wave = tid >> 6, waves = (p.entries < THR ? p.entries + 63 : THR) >> 6;
+  if (wave < waves) {
+    unsigned top[2] = {0, 0};
+    for (int j = tid; j < p.entries; j += THR) {
+      if (j != tid) {
+        token = gmem(p.index)[row * p.ld_top + j];
+        value = entry_value(p, row * p.ld_top + j);
+        counts = token >= 0 && token < V;
+        student = counts ? Vec<T>::load1(z + token) : 0.f;
+      }
+      e.token[j] = counts ? (int)token : kNone;
+      if (!counts) continue;
+      e.t[j] = value;
+      e.z[j] = student;
+      top[0] = max(top[0], ordered(student));
+      top[1] = max(top[1], ordered(value));
+      const int vec = (int)token / N;
+      if (vec == vecs) mark(e.marks, tail_marks + (int)token % N, 0, sums);
+      else if (vec < HELD) mark(e.marks, vec % THR * K + vec / THR, (int)token % N, sums);
+      else mark(e.marks, HELD + (((int)token - HELD * N) >> 3), ((int)token - HELD * N) & 7, sums);
     }
-    const bool counts = token >= 0 && token < V;
-    e.token[j] = counts ? (int)token : kNone;
-    if (!counts) continue;
-    const float t = value * p.inv_temp;
-    e.t[j] = t;
-    e.z[j] = Vec<T>::load1(z + token);
-    add(sums[2], t, (float)kLog2e);
-    const unsigned bit = 1u << (token & 31);
-    if (atomicOr(&e.bits[token >> 5], bit) & bit) *e.twice = 1;
+    if (tid == 0 && teacher_rest != -__builtin_inf()) top[1] = max(top[1], ordered((float)teacher_rest));
+    top[0] = wave_max(top[0]);
+    top[1] = wave_max(top[1]);
+    if ((tid & 63) == 0) {
+      atomicMax(&sums.named_max, top[0]);
+      atomicMax(&sums.teacher_max, top[1]);
+    }
   }
   lds_barrier();
-  const bool twice = *e.twice != 0;
-  if (tid == 0 && teacher_rest != -__builtin_inff()) add(sums[2], teacher_rest, (float)kLog2e);
-  for (int j = tid; j < p.entries; j += THR)
-    if (first_of_token(e, j, e.token[j], twice)) add(sums[1], e.z[j], p.k);
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    if (!LONG && tid + i * THR >= vecs) continue;
-    const unsigned b = vector_bits<T>(e.bits, tid + i * THR);
-    if (b) hide<T>(v[i], b);
+  const bool twice = sums.twice != 0;
+  if (wave < waves) {
+    const float named_ref = ordered_ref(sums.named_max), teacher_ref = ordered_ref(sums.teacher_max);
+    double named = 0, teacher = tid == 0 ? power(teacher_rest, teacher_ref, p) : 0;
+    for (int j = tid; j < p.entries; j += THR) {
+      if (e.token[j] == kNone) continue;
+      teacher += power(e.t[j], teacher_ref, p);
+      if (first_of_token(e, j, twice)) named += power(e.z[j], named_ref, p);
+    }
+    named = wave_sum(named);
+    teacher = wave_sum(teacher);
+    if ((tid & 63) == 0) {
+      sums.named[wave] = named;
+      sums.teacher[wave] = teacher;
+    }
   }
-  const bool tail_named = tail_at < V && (e.bits[tail_at >> 5] >> (tail_at & 31) & 1);
+  unsigned char marks[K > 0 ? K : 1] = {};
+  if constexpr (K > 0) __builtin_memcpy(marks, __builtin_assume_aligned(e.marks + tid * K, K), K);
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+    if (marks[i]) hide<T>(v[i], marks[i]);
+  const bool tail_named = tail_at < V && e.marks[tail_marks + tid];
   if (tail_named) tail = -__builtin_inff();
 
   float m = tail;
@@ -276,11 +328,11 @@ __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dl
     sum += sum_of<T>(v[i], p.k, ref);
     hold_packed(v[i]);
   }
-  int at = tid + K * THR;
+  int at = tid + HELD;
   if constexpr (LONG) {
     for (; at < vecs; at += THR) {
       u32x4 x = Vec<T>::load(z + (int64_t)at * N);
-      const unsigned b = vector_bits<T>(e.bits, at);
+      const unsigned b = long_marks<T, HELD>(e.marks, at);
       if (b) hide<T>(x, b);
       m = max_of<T>(x, m);
       const float to = ref_of(m);
@@ -288,24 +340,18 @@ __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dl
       ref = to;
     }
   }
-  sums[0] = {m, sum};
-  const float ks[3] = {p.k, p.k, (float)kLog2e};
-  block_join<THR / 64, 3>(sums, ks, parts);
-  const RowCoefs r = row_coefs(sums[0], sums[1], sums[2], teacher_rest, w, p);
+  const Softmax rest = rest_join<THR / 64>(m, sum, p.k, parts);
+  const RowCoefs r = row_coefs(rest, sums, waves, teacher_rest, w, p);
   if (!r.live) {
     if (tid == 0) gmem(p.kl)[row] = 0.f;
     if constexpr (GRAD) zero_row<T, THR, NT>(dz, V);
     return;
   }
-  if (tid < 64) {
-    const float kl = row_kl(e, r, p);
-    if (tid == 0) gmem(p.kl)[row] = kl;
-  }
   if constexpr (GRAD) {
     if constexpr (LONG) {
-      for (at -= THR; at >= K * THR; at -= THR) {
+      for (at -= THR; at >= HELD; at -= THR) {
         u32x4 x = Vec<T>::load(z + (int64_t)at * N);
-        const unsigned b = vector_bits<T>(e.bits, at);
+        const unsigned b = long_marks<T, HELD>(e.marks, at);
         if (b) hide<T>(x, b);
         rest_gradient<T, NT>(dz + (int64_t)at * N, x, b, r, p.k);
       }
@@ -313,11 +359,15 @@ __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dl
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int vec = tid + i * THR;
-      if (LONG || vec < vecs) rest_gradient<T, NT>(dz + vec * N, v[i], vector_bits<T>(e.bits, vec), r, p.k);
+      if (LONG || vec < vecs) rest_gradient<T, NT>(dz + vec * N, v[i], marks[i], r, p.k);
     }
     if (tail_at < V && !tail_named) Vec<T>::store1(dz + tail_at, r.rest_f * pow2(tail, p.k, r.rest_ref));
     for (int j = tid; j < p.entries; j += THR)
       if (e.token[j] != kNone) Vec<T>::store1(dz + e.token[j], entry_gradient(e, j, twice, r, p));
+  }
+  if (wave == THR / 64 - 1) {   // (the last wave: it has the fewest entries)
+    const float kl = row_kl(e, r, rest, teacher_rest, p);
+    if ((tid & 63) == 0) gmem(p.kl)[row] = kl;
   }
 }
 
@@ -353,15 +403,17 @@ __global__ __launch_bounds__(1024) void distill_join_kernel(const float *weight,
 constexpr int kSpanThreads = 256, kSpanK = 4, kSpanVecs = kSpanThreads * kSpanK;
 constexpr int64_t span_count(int64_t vecs) { return vecs < 1 ? 1 : (vecs + kSpanVecs - 1) / kSpanVecs; }
 
-// A span's vectors and the row's last V % N elements, without the named ones, which are marked in
-// the bitmap by their place in the span.
+// A span's vectors and the row's last V % N elements, without the named ones; their marks are K bytes
+// a thread, and a byte for each of the last elements.
 template <typename T>
 struct Span {
-  static constexpr int N = Vec<T>::N, THR = kSpanThreads, kBits = (kSpanVecs + 1) * N;
+  static constexpr int N = Vec<T>::N, THR = kSpanThreads, K = kSpanK, kMarkBytes = kSpanVecs + 16;
   int v0, vecs, first, end, tail_at;   // of the row's vectors and elements
   bool has_tail;
-  u32x4 v[kSpanK];
+  u32x4 v[K];
   float tail;
+  unsigned char marks[K];
+  bool tail_named;
 
   __device__ __forceinline__ Span(const T *z, int V, int spans) {
     const int tid = threadIdx.x;
@@ -372,66 +424,58 @@ struct Span {
     tail_at = vecs * N + tid;
     has_tail = (int)blockIdx.x == spans - 1 && tail_at < V;
 #pragma unroll
-    for (int i = 0; i < kSpanK; ++i) {
+    for (int i = 0; i < K; ++i) {
       const int at = v0 + tid + i * THR;
       v[i] = u32x4{Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest};
       if (at < vecs) v[i] = Vec<T>::load(z + (int64_t)at * N);
     }
     tail = has_tail ? Vec<T>::load1(z + tail_at) : -__builtin_inff();
   }
-  __device__ __forceinline__ void clear(const EntryLds &e) const {
-    for (int i = threadIdx.x; i < (kBits + 31) / 32; i += THR) e.bits[i] = 0;
-    if (threadIdx.x == 0) *e.twice = 0;
+  static __device__ __forceinline__ void clear(u32x4 *lds, EntrySums &sums) {
+    if ((int)threadIdx.x < kMarkBytes / 16) lds[threadIdx.x] = u32x4{0, 0, 0, 0};
+    if (threadIdx.x == 0) sums.named_max = sums.teacher_max = sums.twice = 0;
   }
   __device__ __forceinline__ bool holds(int64_t token) const { return token >= first && token < end; }
-  // Marks token; a token that was marked already is named twice.
-  __device__ __forceinline__ void mark(const EntryLds &e, int token) const {
-    const unsigned bit = 1u << ((token - first) & 31);
-    if (atomicOr(&e.bits[(token - first) >> 5], bit) & bit) *e.twice = 1;
-  }
-  __device__ __forceinline__ unsigned bits_of(const EntryLds &e, int i) const {
-    return vector_bits<T>(e.bits, threadIdx.x + i * THR);
-  }
-  __device__ __forceinline__ bool tail_named(const EntryLds &e) const {
-    return has_tail && (e.bits[(tail_at - first) >> 5] >> ((tail_at - first) & 31) & 1);
+  __device__ __forceinline__ void mark_token(const EntryLds &e, int token, EntrySums &sums) const {
+    const int vec = token / N - v0;
+    if (vec + v0 == vecs) mark(e.marks, kSpanVecs + token % N, 0, sums);
+    else mark(e.marks, vec % THR * K + vec / THR, token % N, sums);
   }
   __device__ __forceinline__ void hide_named(const EntryLds &e) {
+    __builtin_memcpy(marks, __builtin_assume_aligned(e.marks + threadIdx.x * K, K), K);
 #pragma unroll
-    for (int i = 0; i < kSpanK; ++i) {
-      const unsigned b = bits_of(e, i);
-      if (b) hide<T>(v[i], b);
-    }
-    if (tail_named(e)) tail = -__builtin_inff();
+    for (int i = 0; i < K; ++i)
+      if (marks[i]) hide<T>(v[i], marks[i]);
+    tail_named = has_tail && e.marks[kSpanVecs + threadIdx.x];
+    if (tail_named) tail = -__builtin_inff();
   }
 };
 
 template <typename T>
 __global__ __launch_bounds__(kSpanThreads) void distill_span_kernel(const T *logits, DistillParams p) {
   constexpr int THR = kSpanThreads;
-  extern __shared__ unsigned lds[];
-  __shared__ Part parts[THR / 64 * 2];
+  extern __shared__ u32x4 lds[];
+  __shared__ EntrySums sums;
+  __shared__ Softmax parts[THR / 64];
   const int64_t row = blockIdx.y;
   const int tid = threadIdx.x;
   if (blockIdx.x == 0 && row == 0 && tid == 0) *p.ticket = 0;
   if (gmem(p.weight)[row] == 0.f) return;
   const T *z = logits + row * p.ld_logits;
-  const EntryLds e = entry_lds(lds, p.entries);
+  const EntryLds e = entry_lds(lds, Span<T>::kMarkBytes, p.entries);
+  Span<T>::clear(lds, sums);
   Span<T> s(z, p.vocab, gridDim.x);
-  s.clear(e);
   lds_barrier();
   for (int j = tid; j < p.entries; j += THR) {
     const int64_t token = gmem(p.index)[row * p.ld_top + j];
     e.token[j] = s.holds(token) ? (int)token : kNone;
-    if (!s.holds(token)) continue;
-    s.mark(e, (int)token);
-    e.z[j] = Vec<T>::load1(z + token);
-    gmem(p.entry_z)[row * p.entries + j] = e.z[j];
+    if (s.holds(token)) s.mark_token(e, (int)token, sums);
   }
   lds_barrier();
-  Part sums[2] = {{-__builtin_inff(), 0.f}, {-__builtin_inff(), 0.f}};
-  const bool twice = *e.twice != 0;
+  const bool twice = sums.twice != 0;
   for (int j = tid; j < p.entries; j += THR)
-    if (first_of_token(e, j, e.token[j], twice)) add(sums[1], e.z[j], p.k);
+    if (e.token[j] != kNone)
+      gmem(p.entry)[row * p.entries + j] = f32x2{Vec<T>::load1(z + e.token[j]), first_of_token(e, j, twice) ? 1.f : 0.f};
   s.hide_named(e);
   float m = s.tail;
 #pragma unroll
@@ -440,10 +484,8 @@ __global__ __launch_bounds__(kSpanThreads) void distill_span_kernel(const T *log
   float sum = pow2(s.tail, p.k, ref);
 #pragma unroll
   for (int i = 0; i < kSpanK; ++i) sum += sum_of<T>(s.v[i], p.k, ref);
-  sums[0] = {m, sum};
-  const float ks[2] = {p.k, p.k};
-  block_join<THR / 64, 2>(sums, ks, parts);
-  if (tid == 0) gmem(p.spans)[row * gridDim.x + blockIdx.x] = f32x4{sums[0].max, sums[0].sum, sums[1].max, sums[1].sum};
+  const Softmax rest = rest_join<THR / 64>(m, sum, p.k, parts);
+  if (tid == 0) gmem(p.spans)[row * gridDim.x + blockIdx.x] = f32x2{rest.ref, rest.sum};
 }
 
 // (without a gradient the grid has a row's first block alone)
@@ -451,47 +493,72 @@ template <typename T, bool GRAD>
 __global__ __launch_bounds__(kSpanThreads) void distill_span_finish_kernel(const T *logits, T *dlogits, DistillParams p,
                                                                            int32_t spans, float *loss) {
   constexpr int THR = kSpanThreads, N = Vec<T>::N;
-  extern __shared__ unsigned lds[];
-  __shared__ Part parts[THR / 64];
+  extern __shared__ u32x4 lds[];
+  __shared__ EntrySums sums;
   __shared__ bool joins;
   const int64_t row = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63;
   T *dz = GRAD ? dlogits + row * p.ld_dlogits : nullptr;
-  const EntryLds e = entry_lds(lds, p.entries);
+  const EntryLds e = entry_lds(lds, Span<T>::kMarkBytes, p.entries);
   const float w = gmem(p.weight)[row];
   float kl = 0.f;
   if (w != 0.f || GRAD) {
+    Span<T>::clear(lds, sums);
     Span<T> s(logits + row * p.ld_logits, GRAD && w != 0.f ? p.vocab : 0, GRAD ? spans : 0);
     RowCoefs r;
     r.live = false;
     if (w != 0.f) {
-      const float teacher_rest = p.rest ? gmem(p.rest)[row] : -__builtin_inff();
-      s.clear(e);
+      const double teacher_rest = p.rest ? gmem(p.rest)[row] * p.temp : -__builtin_inf();
       lds_barrier();
-      Part teacher[1] = {{-__builtin_inff(), 0.f}};
+      unsigned top[2] = {0, 0};
       for (int j = tid; j < p.entries; j += THR) {
         const int64_t token = gmem(p.index)[row * p.ld_top + j];
         const bool counts = token >= 0 && token < p.vocab;
         e.token[j] = counts ? (int)token : kNone;
         if (!counts) continue;
-        e.t[j] = entry_value(p, row * p.ld_top + j) * p.inv_temp;
-        e.z[j] = gmem(p.entry_z)[row * p.entries + j];
-        add(teacher[0], e.t[j], (float)kLog2e);
-        if (GRAD && s.holds(token)) s.mark(e, (int)token);
+        const f32x2 x = gmem(p.entry)[row * p.entries + j];
+        e.t[j] = entry_value(p, row * p.ld_top + j);
+        e.z[j] = x[0];
+        top[0] = max(top[0], ordered(x[0]));
+        top[1] = max(top[1], ordered(e.t[j]));
+        if (x[1] == 0.f) sums.twice = 1;
+        if (GRAD && s.holds(token)) s.mark_token(e, (int)token, sums);
       }
-      if (tid == 0 && teacher_rest != -__builtin_inff()) add(teacher[0], teacher_rest, (float)kLog2e);
-      Part rest = {-__builtin_inff(), 0.f}, named = rest;
+      if (tid == 0 && teacher_rest != -__builtin_inf()) top[1] = max(top[1], ordered((float)teacher_rest));
+      top[0] = wave_max(top[0]);
+      top[1] = wave_max(top[1]);
+      if (lane == 0) {
+        atomicMax(&sums.named_max, top[0]);
+        atomicMax(&sums.teacher_max, top[1]);
+      }
+      Softmax rest = {-__builtin_inff(), 0.f};
       for (int i = lane; i < spans; i += 64) {
-        const f32x4 x = gmem(p.spans)[row * spans + i];
-        rest = join(rest, {x[0], x[1]}, p.k);
-        named = join(named, {x[2], x[3]}, p.k);
+        const f32x2 x = gmem(p.spans)[row * spans + i];
+        const float m = __builtin_fmaxf(rest.ref, x[0]), to = ref_of(m);
+        rest.sum = rest.sum * pow2(rest.ref, p.k, to) + x[1] * pow2(x[0], p.k, to);
+        rest.ref = m;
       }
-      rest = wave_join(rest, p.k);
-      named = wave_join(named, p.k);
-      const float ks[1] = {(float)kLog2e};
-      block_join<THR / 64, 1>(teacher, ks, parts);
-      r = row_coefs(rest, named, teacher[0], teacher_rest, w, p);
-      if (r.live && blockIdx.x == 0 && tid < 64) kl = row_kl(e, r, p);
+      const float m = wave_max(rest.ref);
+      rest.sum = wave_sum(rest.sum * pow2(rest.ref, p.k, ref_of(m)));
+      rest.ref = m;
+      lds_barrier();
+      const float named_ref = ordered_ref(sums.named_max), teacher_ref = ordered_ref(sums.teacher_max);
+      const bool twice = sums.twice != 0;
+      double named = 0, teacher = tid == 0 ? power(teacher_rest, teacher_ref, p) : 0;
+      for (int j = tid; j < p.entries; j += THR) {
+        if (e.token[j] == kNone) continue;
+        teacher += power(e.t[j], teacher_ref, p);
+        if (first_of_token(e, j, twice)) named += power(e.z[j], named_ref, p);
+      }
+      named = wave_sum(named);
+      teacher = wave_sum(teacher);
+      if (lane == 0) {
+        sums.named[tid >> 6] = named;
+        sums.teacher[tid >> 6] = teacher;
+      }
+      lds_barrier();
+      r = row_coefs(rest, sums, THR / 64, teacher_rest, w, p);
+      if (r.live && blockIdx.x == 0 && tid < 64) kl = row_kl(e, r, rest, teacher_rest, p);
     }
     if constexpr (GRAD) {
       // (the span's own vectors were not read where the row is left out: its bounds are those of the call)
@@ -507,13 +574,13 @@ __global__ __launch_bounds__(kSpanThreads) void distill_span_finish_kernel(const
         if (has_tail) Vec<T>::store1(dz + tail_at, 0.f);
       } else {
         s.hide_named(e);
-        const bool twice = *e.twice != 0;
+        const bool twice = sums.twice != 0;
 #pragma unroll
         for (int i = 0; i < kSpanK; ++i) {
           const int at = v0 + tid + i * THR;
-          if (at < vecs) rest_gradient<T, false>(dz + (int64_t)at * N, s.v[i], s.bits_of(e, i), r, p.k);
+          if (at < vecs) rest_gradient<T, false>(dz + (int64_t)at * N, s.v[i], s.marks[i], r, p.k);
         }
-        if (has_tail && !s.tail_named(e)) Vec<T>::store1(dz + tail_at, r.rest_f * pow2(s.tail, p.k, r.rest_ref));
+        if (has_tail && !s.tail_named) Vec<T>::store1(dz + tail_at, r.rest_f * pow2(s.tail, p.k, r.rest_ref));
         for (int j = tid; j < p.entries; j += THR)
           if (e.token[j] != kNone && s.holds(e.token[j])) Vec<T>::store1(dz + e.token[j], entry_gradient(e, j, twice, r, p));
       }
@@ -539,13 +606,17 @@ bool few_rows(int64_t rows, int64_t vecs) {
 // A gradient that the L2s together (32 MB) cannot hold goes past them.
 constexpr double kL2Bytes = 32e6;
 
+template <typename T, int THR, int K, bool LONG, int OUT>
+void launch_rows(const T *z, T *dz, unsigned rows, const DistillParams &p, hipStream_t stream) {
+  const size_t marks = row_mark_bytes(LONG ? p.vocab / Vec<T>::N : 0, Vec<T>::N, THR * K);
+  hipLaunchKernelGGL((distill_row_kernel<T, THR, K, LONG, OUT>), dim3(rows), dim3(THR), entry_lds_bytes(marks, p.entries),
+                     stream, z, dz, p);
+}
 template <typename T, int THR, int K, bool LONG = false>
 void launch_rows(const T *z, T *dz, unsigned rows, int out, const DistillParams &p, hipStream_t stream) {
-  const dim3 grid(rows), block(THR);
-  const size_t lds = entry_lds_bytes(p.vocab, p.entries);
-  if (out == kForward) hipLaunchKernelGGL((distill_row_kernel<T, THR, LONG ? 0 : K, LONG, kForward>), grid, block, lds, stream, z, dz, p);
-  else if (out == kGradient) hipLaunchKernelGGL((distill_row_kernel<T, THR, K, LONG, kGradient>), grid, block, lds, stream, z, dz, p);
-  else hipLaunchKernelGGL((distill_row_kernel<T, THR, K, LONG, kGradientNT>), grid, block, lds, stream, z, dz, p);
+  if (out == kForward) launch_rows<T, THR, LONG ? 0 : K, LONG, kForward>(z, dz, rows, p, stream);
+  else if (out == kGradient) launch_rows<T, THR, K, LONG, kGradient>(z, dz, rows, p, stream);
+  else launch_rows<T, THR, K, LONG, kGradientNT>(z, dz, rows, p, stream);
 }
 
 template <typename T>
@@ -555,7 +626,7 @@ hipError_t launch_distill_t(const himuon_distill &c, const DistillParams &p, hip
   const int64_t vecs = c.vocab / Vec<T>::N;
   if (few_rows(c.rows, vecs)) {
     const unsigned spans = (unsigned)span_count(vecs), rows = (unsigned)c.rows;
-    const size_t lds = entry_lds_bytes(Span<T>::kBits, c.k);
+    const size_t lds = entry_lds_bytes(Span<T>::kMarkBytes, c.k);
     hipLaunchKernelGGL((distill_span_kernel<T>), dim3(spans, rows), dim3(kSpanThreads), lds, stream, z, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -598,7 +669,7 @@ hipError_t launch_distill_t(const himuon_distill &c, const DistillParams &p, hip
 // The ticket, the spans of few long rows and their entries' logits; other rows need nothing.
 size_t distill_workspace(const himuon_distill &p) {
   const int64_t vecs = p.vocab / (p.dtype == HIMUON_BF16 ? 8 : 4);
-  return few_rows(p.rows, vecs) ? 16 + (size_t)p.rows * (span_count(vecs) * sizeof(f32x4) + p.k * sizeof(float)) : 0;
+  return few_rows(p.rows, vecs) ? 16 + (size_t)p.rows * (span_count(vecs) * sizeof(f32x2) + p.k * sizeof(f32x2)) : 0;
 }
 
 hipError_t launch_distill(const himuon_distill &c, void *workspace, hipStream_t stream) {
@@ -610,8 +681,8 @@ hipError_t launch_distill(const himuon_distill &c, void *workspace, hipStream_t 
   p.kl = c.kl;
   const int64_t vecs = c.vocab / (c.dtype == HIMUON_BF16 ? 8 : 4);
   p.ticket = reinterpret_cast<unsigned *>(workspace);
-  p.spans = reinterpret_cast<f32x4 *>(workspace) + 1;
-  p.entry_z = reinterpret_cast<float *>(p.spans + c.rows * span_count(vecs));
+  p.spans = reinterpret_cast<f32x2 *>(reinterpret_cast<char *>(workspace) + 16);
+  p.entry = reinterpret_cast<f32x2 *>(p.spans + c.rows * span_count(vecs));
   p.ld_logits = c.ld_logits;
   p.ld_dlogits = c.ld_dlogits;
   p.ld_top = c.ld_top;
@@ -619,7 +690,9 @@ hipError_t launch_distill(const himuon_distill &c, void *workspace, hipStream_t 
   p.entries = c.k;
   p.value_bf16 = c.value_dtype == HIMUON_BF16;
   p.k = (float)(kLog2e / c.temperature);
-  p.inv_temp = (float)(1.0 / c.temperature);
+  p.fine_k = kLog2e / c.temperature;
+  p.temp = c.temperature;
+  p.inv_temp = 1.0 / c.temperature;
   p.coef = (float)(c.grad_scale / c.temperature);
   return c.dtype == HIMUON_BF16 ? launch_distill_t<__bf16>(c, p, stream) : launch_distill_t<float>(c, p, stream);
 }

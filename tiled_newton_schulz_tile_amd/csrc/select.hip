@@ -23,25 +23,6 @@ namespace {
 
 typedef unsigned long long u64;
 
-// 2^x for x <= 0 (0 where fp64 underflows; NaN is NaN): a polynomial for 2^f, |f| <= 1/2, that interpolates
-// at the Chebyshev nodes of degree 10, within 4e-16.
-__device__ __forceinline__ double pow2_exact(double x) {
-  x = x < -1100. ? -1100. : x;
-  const double n = __builtin_rint(x), f = x - n;
-  double p = 0x1.e6063f7217bc7p-28;
-  p = __builtin_fma(p, f, 0x1.b675bca4eeebbp-24);
-  p = __builtin_fma(p, f, 0x1.62bfd47773353p-20);
-  p = __builtin_fma(p, f, 0x1.ffcb54062e698p-17);
-  p = __builtin_fma(p, f, 0x1.430913096fd9fp-13);
-  p = __builtin_fma(p, f, 0x1.5d87fe9d7a584p-10);
-  p = __builtin_fma(p, f, 0x1.3b2ab6fba1ddap-7);
-  p = __builtin_fma(p, f, 0x1.c6b08d703ce49p-5);
-  p = __builtin_fma(p, f, 0x1.ebfbdff82c598p-3);
-  p = __builtin_fma(p, f, 0x1.62e42fefa3a19p-1);
-  p = __builtin_fma(p, f, 1.0);
-  return __builtin_amdgcn_ldexp(p, (int)n);
-}
-
 // The bits of a logit as a number that grows from the largest to the smallest (-0 as 0; any NaN
 // before +inf).
 __device__ __forceinline__ unsigned down_key(float z) {
