@@ -85,23 +85,25 @@ struct Softmax {
 __device__ __forceinline__ float ref_of(float max) { return max == -__builtin_inff() ? 0.f : max; }
 __device__ __forceinline__ float pow2(float z, float k, float ref) { return __builtin_amdgcn_exp2f((z - ref) * k); }
 
-// 2^x for x <= 0 (0 where fp64 underflows; NaN is NaN): a polynomial for 2^f, |f| <= 1/2, that interpolates
-// at the Chebyshev nodes of degree 10, within 4e-16.
+// 2^f for |f| <= 1/2: the polynomial of degree 9 that interpolates at the Chebyshev nodes, within
+// 2e-14 of the value.
+__device__ __forceinline__ double pow2_fraction(double f) {
+  double p = 0x1.b6571de2f2351p-24;
+  p = __builtin_fma(p, f, 0x1.63ef969a64d3cp-20);
+  p = __builtin_fma(p, f, 0x1.ffcb76789860fp-17);
+  p = __builtin_fma(p, f, 0x1.43088e257f341p-13);
+  p = __builtin_fma(p, f, 0x1.5d87fe908f88ap-10);
+  p = __builtin_fma(p, f, 0x1.3b2ab72b175eep-7);
+  p = __builtin_fma(p, f, 0x1.c6b08d7044119p-5);
+  p = __builtin_fma(p, f, 0x1.ebfbdff8149f2p-3);
+  p = __builtin_fma(p, f, 0x1.62e42fefa39f7p-1);
+  return __builtin_fma(p, f, 0x1.000000000003dp+0);
+}
+// 2^x for x <= 0 (0 where fp64 underflows; NaN is NaN).
 __device__ __forceinline__ double pow2_exact(double x) {
   x = x < -1100. ? -1100. : x;
-  const double n = __builtin_rint(x), f = x - n;
-  double p = 0x1.e6063f7217bc7p-28;
-  p = __builtin_fma(p, f, 0x1.b675bca4eeebbp-24);
-  p = __builtin_fma(p, f, 0x1.62bfd47773353p-20);
-  p = __builtin_fma(p, f, 0x1.ffcb54062e698p-17);
-  p = __builtin_fma(p, f, 0x1.430913096fd9fp-13);
-  p = __builtin_fma(p, f, 0x1.5d87fe9d7a584p-10);
-  p = __builtin_fma(p, f, 0x1.3b2ab6fba1ddap-7);
-  p = __builtin_fma(p, f, 0x1.c6b08d703ce49p-5);
-  p = __builtin_fma(p, f, 0x1.ebfbdff82c598p-3);
-  p = __builtin_fma(p, f, 0x1.62e42fefa3a19p-1);
-  p = __builtin_fma(p, f, 1.0);
-  return __builtin_amdgcn_ldexp(p, (int)n);
+  const double n = __builtin_rint(x);
+  return __builtin_amdgcn_ldexp(pow2_fraction(x - n), (int)n);
 }
 
 // Joins the threads' softmaxes over a block of W waves; lds holds W entries.
