@@ -5,14 +5,19 @@
 // The order of a row's tokens is from the largest logit to the smallest, and among equal ones by
 // index: a token's rank key is a 64-bit number, its logit's bits mapped to grow downwards above its
 // index, unlike any other of the row.  Every filter keeps a first part of that order, so it is held
-// as the last rank key that it keeps (its border).  A border is found by a descent over the digits
-// of the rank key: a histogram of the elements in the present range, the bin in which the count (or
-// the probability) reaches its target, and that bin as the next range, until one element is left.
+// as the last rank key that it keeps (its border).
 //
-// A block holds its row in registers (up to 256 KB; longer ones are read again for every pass).  What
-// the filters may keep is most often a small part of the row: a bound on the smallest such logit is
-// found first, the elements above it go into lists in LDS, and borders and draw come from those; rows
-// whose lists overflow (flat ones) are read again.
+// A row is read once.  Each of a block's waves goes through a stretch of it on its own: it sums the
+// powers, and it appends to a list in LDS what the filters may keep, which most often is a small part
+// of the row.  What they may keep is all from a bound on, which rises on the way: the k-th largest
+// logit so far, or one below which all tokens together have too little probability to matter.  Borders
+// and draw then come from the lists.  Waves meet once, at the end of the row; with many rows a block is
+// one wave.  Rows whose lists overflow (flat ones) are left to a second launch, which reads them several
+// times.
+//
+// A border is found by a descent over the digits of the rank key: a histogram of the elements in the
+// present range, the bin in which the count (or the probability) reaches its target, and that bin as
+// the next range, until one element is left.
 //
 // A border and a draw decide about whole tokens, and a sum in fp32 that is off by 1e-7 decides
 // wrongly in one row of a hundred where 1e5 tokens share the probability.  Where a token hangs on
@@ -31,221 +36,230 @@ namespace {
 typedef unsigned long long u64;
 
 // The bits of a logit as a number that grows from the largest to the smallest (-0 as 0; any NaN
-// before +inf).
+// before +inf), and back.
 __device__ __forceinline__ unsigned down_key(float z) {
   const unsigned u = __builtin_bit_cast(unsigned, z != z ? __builtin_nanf("") : z + 0.f);
   return u ^ ((unsigned)((int)~u >> 31) >> 1);
 }
-__device__ __forceinline__ u64 rank_key(float z, int index) { return (u64)down_key(z) << 32 | (unsigned)index; }
-
-__device__ __forceinline__ float logit_of(unsigned down) {
+__device__ __forceinline__ float logit_of_key(unsigned down) {
   return __builtin_bit_cast(float, down & 0x80000000u ? down : down ^ 0x7fffffffu);
 }
+// Rank keys: a logit's number (16 bits of it for bf16) above its index.
+constexpr int kIndexBits = 20;
+static_assert(HIMUON_TOP_VOCAB <= 1 << kIndexBits, "an index fits");
+template <class T>
+constexpr int kKeyShift = sizeof(T) == 2 ? 16 : 0;
+template <class T>
+__device__ __forceinline__ u64 rank_key(float z, int index) {
+  return (u64)(down_key(z) >> kKeyShift<T>) << kIndexBits | (unsigned)index;
+}
+template <class T>
+__device__ __forceinline__ float logit_of(u64 r) {
+  unsigned down = (unsigned)(r >> kIndexBits) << kKeyShift<T>;
+  if (kKeyShift<T> && !(down & 0x80000000u)) down |= 0xffffu;
+  return logit_of_key(down);
+}
+__device__ __forceinline__ int index_of(u64 r) { return (int)(r & (((u64)1 << kIndexBits) - 1)); }
+// The first and the last key that a logit can have.
+template <class T>
+__device__ __forceinline__ u64 first_key(float z) { return rank_key<T>(z, 0); }
+template <class T>
+__device__ __forceinline__ u64 last_key(float z) { return rank_key<T>(z, 0) | (((u64)1 << kIndexBits) - 1); }
+
 __device__ __forceinline__ float maximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }   // NaN wins
 
 // Vector `vec` of a row of V elements; -inf stands in for what lies beyond the row.
 template <class T>
 __device__ __forceinline__ u32x4 row_vector(const T *z, int vec, int V) {
   constexpr int N = Vec<T>::N;
-  u32x4 v = {Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest};
   if ((vec + 1) * N <= V) return Vec<T>::load(z + (int64_t)vec * N);
-  if (vec * N >= V) return v;
-  float x[N];
+  u32x4 v = {Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest};
+#pragma unroll 1
+  for (int at = V - 1; at >= vec * N; --at) {   // (from the back, each moving the others up)
+    const unsigned x = __builtin_bit_cast(unsigned, Vec<T>::load1(z + at));
 #pragma unroll
-  for (int e = 0; e < N; ++e) x[e] = vec * N + e < V ? Vec<T>::load1(z + vec * N + e) : -__builtin_inff();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (N == 8) v[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);   // (exact)
-    else v[i] = __builtin_bit_cast(unsigned, x[i]);
+    for (int i = 3; i > 0; --i) v[i] = N == 8 ? v[i] << 16 | v[i - 1] >> 16 : v[i - 1];
+    v[0] = N == 8 ? v[0] << 16 | x >> 16 : x;
   }
   return v;
 }
 
-// Where elements come from: each(f) calls f(index, logit) for all of them, the threads of the block
-// in step.  A row in memory:
-template <class T, int THR>
-struct RowSource {
-  const T *z;
-  int V;
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    constexpr int N = Vec<T>::N;
-    for (int at = threadIdx.x; at * N < V; at += THR) {
+// LDS accesses of one wave's lanes before this are seen by all of its lanes behind it.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+__device__ __forceinline__ u64 wave_scan(u64 x) {   // inclusive
+  return __builtin_bit_cast(u64, dev::wave_scan(__builtin_bit_cast(double, x), 0.0, [](double a, double b) {
+    return __builtin_bit_cast(double, __builtin_bit_cast(u64, a) + __builtin_bit_cast(u64, b));
+  }));
+}
+__device__ __forceinline__ double wave_scan(double x) {
+  return dev::wave_scan(x, 0.0, [](double a, double b) { return a + b; });
+}
+__device__ __forceinline__ int lanes_before(u64 ballot) {
+  return __builtin_amdgcn_mbcnt_hi((unsigned)(ballot >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)ballot, 0));
+}
+__device__ __forceinline__ int lane_of(u64 ballot) { return __builtin_ctzll(ballot); }
+template <class X>
+__device__ __forceinline__ X from_lane(X x, int lane) {   // lane: the same in all lanes
+  if constexpr (sizeof(X) == 4)
+    return __builtin_bit_cast(X, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+  else {
+    const u64 u = __builtin_bit_cast(u64, x);
+    return __builtin_bit_cast(X, (u64)(unsigned)__builtin_amdgcn_readlane((int)(u >> 32), lane) << 32 |
+                                     (unsigned)__builtin_amdgcn_readlane((int)u, lane));
+  }
+}
+
+// A histogram of a descent.
+template <int BINS>
+struct Histogram {
+  u64 mass[BINS];
+  unsigned count[BINS];
+};
+// What is left of a descent's range of rank keys, and what weighs before it.
+struct Range {
+  u64 first, last, before;
+};
+// bin_shift: the keys of a bin of `bits` digits.
+__device__ __forceinline__ int bin_shift(const Range &r, int digits) {
+  const int bits = 64 - __builtin_clzll((r.last - r.first) | 1);
+  return bits > digits ? bits - digits : 0;
+}
+// The bin where the target is reached becomes the range; whether that is the end: one key, or one element.
+__device__ __forceinline__ bool narrow(Range &r, int bin, u64 before, unsigned count, int shift) {
+  r.first += (u64)bin << shift;
+  const u64 width = ((u64)1 << shift) - 1;
+  r.last = r.last - r.first < width ? r.last : r.first + width;
+  r.before = before;
+  return shift == 0 || count == 1;
+}
+
+// The last of n rank keys in LDS (one wave; all between first and last) up to which they weigh the target at
+// least: the first one that reaches it; `last` where all weigh less.  weight(key): all together below 2^64.
+// target_of(total): the target, 1 or more, given what all weigh.  COUNT: each weighs 1.
+constexpr int kWaveBins = 256;
+template <bool COUNT, class WEIGHT, class TARGET>
+__device__ __forceinline__ u64 find_border(const u64 *list, int n, u64 first, u64 last, WEIGHT weight, TARGET target_of,
+                                           Histogram<kWaveBins> &h) {
+  constexpr int B = kWaveBins / 64;   // bins a lane
+  const int lane = threadIdx.x & 63;
+  Range r = {first, last, 0};
+  u64 target = 0;
+  for (bool top = true;; top = false) {
+    const int shift = bin_shift(r, 8);
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (!COUNT) h.mass[lane * B + i] = 0;
+      h.count[lane * B + i] = 0;
+    }
+    wave_sync();
+    for (int j = lane; j < n; j += 64) {
+      const u64 key = list[j];
+      if (key < r.first || key > r.last) continue;
+      const int bin = (int)((key - r.first) >> shift);
+      atomicAdd(&h.count[bin], 1u);
+      if (!COUNT) atomicAdd(&h.mass[bin], weight(key));
+    }
+    wave_sync();
+    u64 w[B], mine = 0;
+#pragma unroll
+    for (int i = 0; i < B; ++i) mine += w[i] = COUNT ? h.count[lane * B + i] : h.mass[lane * B + i];
+    const u64 upto = wave_scan(mine);
+    if (top) target = target_of(from_lane(upto, 63));
+    const u64 hit = __ballot(r.before + upto >= target);
+    if (hit == 0) return last;
+    u64 at = r.before + upto - mine;
+    int bin = 0;
+#pragma unroll
+    for (int i = 0; i < B - 1; ++i)
+      if (bin == i && at + w[i] < target) {
+        at += w[i];
+        bin = i + 1;
+      }
+    const int l = lane_of(hit);
+    bin = l * B + from_lane(bin, l);
+    if (narrow(r, bin, from_lane(at, l), h.count[bin], shift)) return r.last;
+    wave_sync();
+  }
+}
+
+// The same among the elements of a row of V in memory, by the THR threads of a block.  sum (top level alone):
+// what it adds up over all elements.
+template <int THR>
+struct BlockLds {
+  Histogram<4 * THR> h;
+  u64 wave[THR / 64];
+  int bin;
+  u64 before;
+  unsigned count;
+};
+template <class T, int THR, bool COUNT, class WEIGHT, class TARGET>
+__device__ __forceinline__ u64 find_border_in_row(const T *z, int V, u64 first, u64 last, WEIGHT weight, TARGET target_of,
+                                                  BlockLds<THR> &lds) {
+  constexpr int N = Vec<T>::N, B = 4, kDigits = 31 - __builtin_clz(B * THR);
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  Range r = {first, last, 0};
+  u64 target = 0;
+  for (bool top = true;; top = false) {
+    const int shift = bin_shift(r, kDigits);
+    for (int i = tid; i < B * THR; i += THR) {
+      lds.h.mass[i] = 0;
+      lds.h.count[i] = 0;
+    }
+    if (tid == 0) lds.bin = -1;
+    __syncthreads();
+    const float most = logit_of<T>(r.first), least = logit_of<T>(r.last);   // (a NaN is above everything)
+    for (int at = tid; at * N < V; at += THR) {
       float x[N];
       Vec<T>::unpack(row_vector(z, at, V), x);
+      bool in = false;
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (at * N + e < V) f(at * N + e, x[e]);
-    }
-  }
-};
-// A row in registers: K vectors a thread.  Each wave has a stretch of 64 K consecutive vectors, so
-// that elements are in order from wave to wave.
-template <class T, int K>
-struct HeldRow {
-  u32x4 v[K];
-  int first, V;   // the thread's first vector
-
-  __device__ __forceinline__ HeldRow(const T *z, int vocab) {
-    first = (threadIdx.x >> 6) * 64 * K + (threadIdx.x & 63);
-    V = vocab;
+      for (int e = 0; e < N; ++e) in = in || !(x[e] < least || x[e] > most);
+      if (!__any(in)) continue;
 #pragma unroll
-    for (int i = 0; i < K; ++i) v[i] = row_vector(z, first + 64 * i, V);
-  }
-  // f(index of the vector's first element, its elements), one vector after the other: the compiler
-  // may neither keep the unpacked elements of one sweep for the next nor mix the vectors of a sweep
-  // (both would take far more registers than there are).
-  template <class F>
-  __device__ __forceinline__ void vectors(F f) {
-    constexpr int N = Vec<T>::N;
-    int at = first;
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      asm volatile("" : "+v"(v[i]), "+v"(at));
-      float x[N];
-      Vec<T>::unpack(v[i], x);
-      f((at + 64 * i) * N, x);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-};
-// Rank keys in LDS: a list for each wave, in the order of their indices.
-constexpr int kListMost = 512;
-struct ListSource {
-  const u64 *list;   // of this thread's wave
-  int n;
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    for (int j = threadIdx.x & 63; j < n; j += 64) {
-      const u64 r = list[j];
-      f((int)(unsigned)r, logit_of((unsigned)(r >> 32)));
-    }
-  }
-};
-// One logit a thread.
-struct ThreadSource {
-  float z;
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    f((int)threadIdx.x, z);
-  }
-};
-
-// Appends a vector's elements from `least` on to the wave's list of n keys (of which kListMost are
-// kept; n counts on).
-// Whether the wave has any.
-template <int N>
-__device__ __forceinline__ bool append(u64 *list, int &n, int at, const float (&x)[N], float least, int V) {
-  float top = x[0];
-#pragma unroll
-  for (int e = 1; e < N; ++e) top = maximum(top, x[e]);
-  if (!__any(top >= least)) return false;
-  unsigned m = 0;
-#pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (x[e] >= least && at + e < V) m |= 1u << e;
-  const int count = __builtin_popcount(m);
-  int pos = n;
-#pragma unroll
-  for (int b = 0; 1 << b <= N; ++b) {
-    const u64 with = __ballot(count >> b & 1);
-    pos += __builtin_amdgcn_mbcnt_hi((unsigned)(with >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)with, 0)) << b;
-    n += __builtin_popcountll(with) << b;
-  }
-#pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (m >> e & 1) {
-      if (pos < kListMost) list[pos] = rank_key(x[e], at + e);
-      ++pos;
-    }
-  return true;
-}
-
-constexpr int kBins = 1024;
-struct SelectLds {
-  u64 mass[kBins];      // what a bin weighs
-  unsigned count[kBins];
-  u64 wave[16];
-  u64 before;           // the weight before the bin that was found
-  int bin;
-};
-
-template <int THR>
-__device__ __forceinline__ u64 block_scan(u64 mine, u64 *wave, u64 &total) {   // exclusive
-  const int lane = threadIdx.x & 63;
-  u64 s = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const u64 up = __shfl_up(s, d);
-    if (lane >= d) s += up;
-  }
-  if (lane == 63) wave[threadIdx.x >> 6] = s;
-  __syncthreads();
-  u64 base = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < THR / 64; ++w) {
-    if (w < (int)(threadIdx.x >> 6)) base += wave[w];
-    total += wave[w];
-  }
-  __syncthreads();
-  return base + s - mine;
-}
-
-// The last rank key, from first to last, up to which the elements weigh `target` at least: the first
-// one that reaches it.  weight(z): an element's weight (all together below 2^64).  Where all weigh
-// less: last.  target_of(total): the target, at least 1, given what all weigh together.  With LEVELS
-// > 0 the descent ends after so many, at a key that is no smaller.
-template <int THR, int LEVELS = 0, class SOURCE, class WEIGHT, class TARGET>
-__device__ __forceinline__ u64 find_border(SOURCE &src, u64 first, u64 last, WEIGHT weight, TARGET target_of,
-                                           SelectLds &lds) {
-  constexpr int B = kBins / THR > 0 ? kBins / THR : 1;   // bins a thread
-  u64 base = 0, target = 0;
-  const u64 end = last;
-  for (int level = 1;; ++level) {
-    const int bits = 64 - __builtin_clzll((last - first) | 1);
-    const int shift = bits > 10 ? bits - 10 : 0;
-#pragma unroll
-    for (int i = 0; i < kBins; i += THR)
-      if (i + (int)threadIdx.x < kBins) {
-        lds.mass[i + threadIdx.x] = 0;
-        lds.count[i + threadIdx.x] = 0;
+      for (int e = 0; e < N; ++e) {
+        const u64 key = rank_key<T>(x[e], at * N + e);
+        if (key < r.first || key > r.last || at * N + e >= V) continue;
+        const int bin = (int)((key - r.first) >> shift);
+        atomicAdd(&lds.h.count[bin], 1u);
+        if (!COUNT) atomicAdd(&lds.h.mass[bin], weight(x[e]));
       }
-    __syncthreads();
-    src.each([&](int index, float z) {
-      const u64 r = rank_key(z, index);
-      if (r < first || r > last) return;
-      const int bin = (int)((r - first) >> shift);
-      const u64 w = weight(z);
-      atomicAdd(&lds.count[bin], 1u);
-      if (w) atomicAdd(&lds.mass[bin], w);
-    });
-    __syncthreads();
-    u64 w[B], mine = 0, total;
-#pragma unroll
-    for (int i = 0; i < B; ++i) mine += w[i] = (int)threadIdx.x * B + i < kBins ? lds.mass[threadIdx.x * B + i] : 0;
-    u64 before = base + block_scan<THR>(mine, lds.wave, total);
-    if (level == 1) {
-      target = target_of(total);
-      if (total < target) return end;
     }
-    if (before < target && before + mine >= target) {
+    __syncthreads();
+    u64 have[B], mine = 0;
 #pragma unroll
-      for (int i = 0; i < B; ++i) {
-        if (before < target && before + w[i] >= target) {
-          lds.bin = threadIdx.x * B + i;
-          lds.before = before;
+    for (int i = 0; i < B; ++i) mine += have[i] = COUNT ? lds.h.count[tid * B + i] : lds.h.mass[tid * B + i];
+    u64 upto = wave_scan(mine);
+    if (lane == 63) lds.wave[w] = upto;
+    __syncthreads();
+    u64 total = 0;
+    for (int i = 0; i < THR / 64; ++i) {
+      if (i < w) upto += lds.wave[i];
+      total += lds.wave[i];
+    }
+    if (top) target = target_of(total);
+    u64 at = r.before + upto - mine;
+    if (at < target && at + mine >= target) {
+      int bin = 0;
+#pragma unroll
+      for (int i = 0; i < B - 1; ++i)
+        if (bin == i && at + have[i] < target) {
+          at += have[i];
+          bin = i + 1;
         }
-        before += w[i];
-      }
+      lds.bin = tid * B + bin;
+      lds.before = at;
+      lds.count = lds.h.count[tid * B + bin];
     }
     __syncthreads();
-    base = lds.before;
-    first += (u64)lds.bin << shift;
-    last = last - first < ((u64)1 << shift) - 1 ? last : first + (((u64)1 << shift) - 1);
-    const bool done = shift == 0 || lds.count[lds.bin] == 1 || level == LEVELS;
+    const int bin = lds.bin;
+    const u64 before = lds.before;
+    const unsigned count = lds.count;
     __syncthreads();
-    if (done) return last;
+    if (bin < 0) return last;
+    if (narrow(r, bin, before, count, shift)) return r.last;
   }
 }
 
@@ -300,54 +314,62 @@ __device__ __forceinline__ void write_bad(const SampleParams &p, int64_t row) {
   gmem(p.token)[row] = -1;
   gmem(p.logp)[row] = gmem(p.kept)[row] = __builtin_nanf("");
 }
-// top, all, kept: the largest logit, and the sums of powers of the distances to it.
-__device__ __forceinline__ void write_token(const SampleParams &p, int64_t row, const Settings &s, int token, float logit,
-                                            float top, double all, double kept) {
+// Powers 2^(z k) relative to 2^R, R the whole number next to ref k, for logits that are not far above ref
+// (2^100 times its power); 2^-1010 at least: those below kNoPower are none.
+//
+// z k and its fraction come from fused multiply-adds, whose products are exact: the error of a power relative
+// to another is that of k and of the polynomial.  Where |ref| k is past 2^40, logits that differ at all are
+// more than 2^16 octaves apart; a k that makes it 2^40 does no harm then, and keeps the sums exact.
+constexpr double kNoPower = 0x1p-1000;
+struct Powers {
+  double k, shift, low;   // shift: 1.5 2^52 - R, so that z k + shift ends in the power's exponent
+  double unit;            // multiples of 1 / unit in histograms
+  __device__ __forceinline__ void refer_to(float ref, double full_k) {
+    k = full_k;
+    if (__builtin_fabs(ref * k) > 0x1p40) k = 0x1p40 / __builtin_fabs((double)ref);
+    const double R = __builtin_rint(ref * k);
+    shift = 0x1.8p52 - R;
+    low = ref - 1009. * (1.00001 * __builtin_amdgcn_rcp(k));   // (its power is between 2^-1010.1 and 2^-1008.9)
+  }
+  __device__ __forceinline__ double of(float z) const {
+    const double x = __builtin_fmax((double)z, low);
+    const double a = __builtin_fma(x, k, shift), f = __builtin_fma(x, k, shift - a);
+    const u64 p = __builtin_bit_cast(u64, pow2_fraction(f));
+    const unsigned hi = (unsigned)(p >> 32) + ((unsigned)__builtin_bit_cast(u64, a) << 20);
+    return __builtin_bit_cast(double, (u64)hi << 32 | (unsigned)p);
+  }
+  __device__ __forceinline__ u64 mass(float z) const { return (u64)(of(z) * unit + 0.5); }
+  // What powers relative to this have to be multiplied with to be relative to `to`.
+  __device__ __forceinline__ double scale_to(double to_shift) const {
+    const double n = to_shift - shift;   // R - R of `to`
+    return n < -1000. ? 0. : __builtin_amdgcn_ldexp(1., (int)__builtin_fmin(n, 1000.));
+  }
+};
+
+// top: the row's largest logit; all, kept: sums of powers.
+__device__ __forceinline__ void write_token(const SampleParams &p, int64_t row, const Settings &s, const Powers &e, int token,
+                                            float logit, float top, double all, double kept) {
   gmem(p.token)[row] = token;
-  gmem(p.logp)[row] = s.greedy ? 0.f : (float)(((double)logit - top) / s.temp - log(all));
+  gmem(p.logp)[row] = s.greedy ? 0.f : (float)(((double)logit - top) * (s.k * 0.69314718055994530942) - log(all / e.of(top)));
   gmem(p.kept)[row] = s.greedy ? 1.f : (float)(kept / all);
 }
 
-// Powers of the distances to the row's largest logit, 2^-1010 at least: those below kNoPower are none.
-constexpr double kNoPower = 0x1p-1000;
-struct Powers {
-  float top;
-  double k, unit;   // unit: multiples of 1 / unit in histograms
-  __device__ __forceinline__ double of(float z) const {
-    const double magic = 0x1.8p52, d = __builtin_fmax((double)z - top, -1010. / k);
-    const double a = __builtin_fma(d, k, magic), f = __builtin_fma(d, k, magic - a);
-    const u64 p = __builtin_bit_cast(u64, pow2_fraction(f));
-    // (the low bits of a are the exponent)
-    return __builtin_bit_cast(double, p + (__builtin_bit_cast(u64, a) << 52));
-  }
-  __device__ __forceinline__ u64 mass(float z) const { return (u64)(of(z) * unit + 0.5); }
-};
-constexpr u64 kLastKey = (u64)0xff7fffffu << 32 | 0xffffffffu;   // of a finite logit
-
 // What a row's filters keep, once their borders are known.
+template <class T>
 struct Kept {
   u64 border;       // the last rank key of top_k and top_p
   double least;     // the least power of min_p, kNoPower at least
   __device__ __forceinline__ double power(const Powers &e, int index, float z) const {
     const double x = e.of(z);
-    return rank_key(z, index) <= border && x >= least ? x : 0.;
+    return rank_key<T>(z, index) <= border && x >= least ? x : 0.;
   }
 };
 
-// The borders of top_k and top_p together.  all: the sum of the row's powers where top_p needs it (it
-// does not with top_k: then it is that of the first top_k).
-template <int THR, class SOURCE>
-__device__ __forceinline__ u64 filter_border(SOURCE &src, u64 first, u64 last, const Settings &s, const Powers &e, double all,
-                                             SelectLds &lds) {
-  u64 border = last;
-  if (s.by_k)
-    border = find_border<THR>(src, first, last, [](float) { return (u64)1; }, [&](u64) { return (u64)s.top_k; }, lds);
-  if (s.by_p)
-    border = find_border<THR>(src, first, border, [&](float z) { return e.mass(z); }, [&](u64 total) {
-      const double t = __builtin_ceil(s.top_p * (s.by_k ? (double)total : all * e.unit));
-      return t < 1. ? (u64)1 : (u64)t;
-    }, lds);
-  return border;
+// The target of top_p in multiples of 1 / unit: what its first tokens have to reach.  total: of those that top_k
+// keeps, or else all, the sum of the row's powers.
+__device__ __forceinline__ u64 target_of_p(const Settings &s, const Powers &e, u64 total, double all) {
+  const double t = __builtin_ceil(s.top_p * (s.by_k ? (double)total : all * e.unit));
+  return t < 1. ? (u64)1 : (u64)t;
 }
 
 template <int THR>
@@ -361,24 +383,8 @@ __device__ __forceinline__ double block_sum_in_order(double x, double *wave) {
   for (int w = 0; w < THR / 64; ++w) s += wave[w];
   return s;
 }
-template <int THR>
-__device__ __forceinline__ float block_maximum(float x, float *wave) {
-  x = wave_reduce(x, -__builtin_inff(), [](float a, float b) { return maximum(a, b); });
-  if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = x;
-  __syncthreads();
-  x = wave[0];
-#pragma unroll
-  for (int w = 1; w < THR / 64; ++w) x = maximum(x, wave[w]);
-  return x;
-}
-__device__ __forceinline__ double wave_scan(double x) {   // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const double up = __shfl_up(x, d);
-    if (lane >= d) x += up;
-  }
-  return x;
+__device__ __forceinline__ float wave_maximum(float x) {
+  return wave_reduce(x, -__builtin_inff(), [](float a, float b) { return maximum(a, b); });
 }
 
 // One wave: which of n parts (0 or more each, in order) the target falls into: the first one up to
@@ -388,52 +394,445 @@ __device__ __forceinline__ int find_part(int n, double target, PART part, double
   const int lane = threadIdx.x & 63;
   double sum = 0;
   int last = 0;
-  double last_before = 0;
+  before = 0;
   for (int c = 0; c < n; c += 64) {
     const double w = c + lane < n ? part(c + lane) : 0., s = wave_scan(w);
     const u64 hit = __ballot(w > 0. && sum + s > target), some = __ballot(w > 0.);
     if (hit || some) {
-      const int l = hit ? __builtin_ctzll(hit) : 63 - __builtin_clzll(some);
-      const double up = __shfl(s - w, l);
+      const int l = hit ? lane_of(hit) : 63 - __builtin_clzll(some);
       last = c + l;
-      last_before = sum + up;
+      before = sum + from_lane(s - w, l);
       if (hit) break;
     }
-    sum += __shfl(s, 63);
+    sum += from_lane(s, 63);
   }
-  before = last_before;
   return last;
 }
 
-// The token of a row that is read from memory for every pass over it; chunk: LDS, one for each wave
-// and turn over the row's vectors.
+// ---- one wave's stretch of a row
+constexpr int kTurnVecs = 4;                  // vectors a lane has at a time
+constexpr int kTurn = 64 * kTurnVecs;         // vectors a wave has at a time
+constexpr int kTurns = 64;                    // turns of a stretch at most
+constexpr int kListMost = 768;                // keys of a list
+constexpr int kQuota = 224;                   // rank of the logit that the bound follows, at most
+constexpr float kFar = 100.f;                 // octaves
+
+// What a wave's stretch comes to.
+struct Stretch {
+  float top;       // its largest logit (NaN: there is one)
+  float ref;       // the logit that powers followed (-inf: no logit)
+  double shift;    // Powers' of its sums (0: no logit)
+  double sum;      // of the powers of what is not in the list
+  double listed;   // and of what is
+  float bound;     // the largest logit that was left out of the list is below
+  float last_bound;   // sweep()
+  int n;           // keys in the list; kListMost + 1: they did not fit
+};
+
+// What the list of a stretch has to hold, and how its sum is taken.
+struct Wants {
+  int quota;             // 0, or: the quota largest
+  int most;              // keys of the list above which the bound is raised
+  double k, temp;        // log2(e) / temperature, temperature
+  double share_p;        // 0, or: all tokens but some with less than this share of all probability
+  double share_m;        // 0, or: all tokens with at least this share of the largest's probability
+  bool none;             // nothing
+};
+// The bound that comes from the largest logit top, and from what all powers relative to ref sum to at least
+// (with room for errors of 1e-5 of its terms: its logarithms are fp32).
+__device__ __forceinline__ float bound_of(const Wants &want, float top, float ref, double sum, int V) {
+  const auto below = [&](float from, double share) {
+    const float step = (float)want.temp * kLn2 * __builtin_amdgcn_logf((float)share);   // (negative)
+    return __builtin_fmaxf(from + step - 1e-5f * (__builtin_fabsf(from) + __builtin_fabsf(step)), -__FLT_MAX__);
+  };
+  float b = -__FLT_MAX__;
+  if (want.share_p > 0.) b = __builtin_fmaxf(b, below(ref, __builtin_fmin(want.share_p * sum / V, 1e30)));
+  if (want.share_m > 0.) b = __builtin_fmaxf(b, below(top, want.share_m));
+  return __builtin_fminf(b, top);
+}
+
+// A number that `quota` at least of N values a lane are not below, and where ties allow it no more than
+// quota + quota / 8 + 8; -inf where there are not so many above that.  By halves of the values' range, and
+// where that does not converge (a mask among them) of their keys' range.
+template <int N>
+__device__ __forceinline__ float nth_largest(const float (&x)[N], int quota) {
+  float most = x[0], least = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) {
+    most = __builtin_fmaxf(most, x[i]);
+    least = __builtin_fminf(least, x[i]);
+  }
+  const auto count = [&](float t) {
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) c += __builtin_popcountll(__ballot(x[i] >= t));
+    return c;
+  };
+  float hi = wave_max(most), lo = __builtin_fmaxf(-wave_max(-least), -__FLT_MAX__);   // (fewer from hi on, enough from lo on)
+  if (count(hi) >= quota) return hi;
+  if (count(lo) < quota) return -__builtin_inff();
+  for (int turn = 0;; ++turn) {
+    float mid = lo * 0.5f + hi * 0.5f;
+    if (turn >= 16) {
+      const unsigned a = down_key(hi), b = down_key(lo);
+      mid = logit_of_key(a + (b - a) / 2);
+    }
+    if (!(mid > lo && mid < hi)) {
+      if (turn >= 16) return lo;
+      continue;
+    }
+    const int c = count(mid);
+    if (c >= quota) {
+      lo = mid;
+      if (c <= quota + quota / 8 + 8) return lo;
+    } else {
+      hi = mid;
+    }
+  }
+}
+// The same of a list.
+template <class T>
+__device__ __forceinline__ float nth_of_list(const u64 *list, int n, int quota) {
+  float x[kListMost / 64];
+#pragma unroll
+  for (int i = 0; i < kListMost / 64; ++i) {
+    const int j = i * 64 + (threadIdx.x & 63);
+    x[i] = j < n ? logit_of<T>(list[j]) : -__builtin_inff();
+  }
+  return nth_largest(x, quota);
+}
+
+// Appends a vector's elements from `least` on to the wave's list of n keys (of which kListMost are
+// kept; n counts on), in the order of their indices if ORDERED.
+template <class T, bool ORDERED, int N>
+__device__ __forceinline__ void append(u64 *list, int &n, int at, const float (&x)[N], float least, int V) {
+  int pos = n;
+  if constexpr (ORDERED) {
+    unsigned m = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (x[e] >= least && at + e < V) m |= 1u << e;
+    const int count = __builtin_popcount(m);
+#pragma unroll
+    for (int b = 0; 1 << b <= N; ++b) {
+      const u64 with = __ballot(count >> b & 1);
+      pos += lanes_before(with) << b;
+      n += __builtin_popcountll(with) << b;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (m >> e & 1) {
+        if (pos < kListMost) list[pos] = rank_key<T>(x[e], at + e);
+        ++pos;
+      }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const bool in = x[e] >= least && at + e < V;
+      const u64 with = __ballot(in);
+      if (with == 0) continue;
+      pos = n + lanes_before(with);
+      if (in && pos < kListMost) list[pos] = rank_key<T>(x[e], at + e);
+      n += __builtin_popcountll(with);
+    }
+  }
+}
+
+template <class T>
+struct Turn {
+  u32x4 v[kTurnVecs];
+  __device__ __forceinline__ void load(const T *z, int turn, int V) {
+    const int at = turn * kTurn + (threadIdx.x & 63);
+    if ((turn + 1) * kTurn * Vec<T>::N <= V) {
+#pragma unroll
+      for (int i = 0; i < kTurnVecs; ++i) v[i] = Vec<T>::load(z + (int64_t)(at + 64 * i) * Vec<T>::N);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTurnVecs; ++i) v[i] = row_vector(z, at + 64 * i, V);
+    }
+  }
+  // Vector i, the same in all lanes (a choice of registers, so that loops over vectors stay loops).
+  __device__ __forceinline__ u32x4 pick(int i) const {
+    static_assert(kTurnVecs == 4, "four vectors");
+    const bool odd = i & 1, high = i & 2;
+    u32x4 a;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned x = odd ? v[1][j] : v[0][j], y = odd ? v[3][j] : v[2][j];
+      a[j] = high ? y : x;
+    }
+    hold_packed(a);
+    return a;
+  }
+};
+
+// The largest logit of each of a lane's vectors, and of all of them.
+template <class T>
+__device__ __forceinline__ float turn_maximum(Turn<T> &turn, float (&most)[kTurnVecs]) {
+  constexpr int N = Vec<T>::N;
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kTurnVecs; ++i) {
+    hold_packed(turn.v[i]);
+    float x[N];
+    Vec<T>::unpack(turn.v[i], x);
+    most[i] = x[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) most[i] = maximum(most[i], x[j]);
+    top = maximum(top, most[i]);
+    hold_packed(turn.v[i]);
+  }
+  return top;
+}
+// A wave goes through turns [t0, t1) of a row, the first of which is in `now`, with a first logit that
+// powers are relative to and a first bound (which hold for the row).  exact: powers in fp64; else in fp32.
+// They are relative to a logit that follows the largest, and if CEIL (fp32 alone) to one that follows the
+// bound, above which nothing is summed.  turns: nullptr, or what each turn weighs.  last_quota: rank of the
+// logit in the final list that last_bound is not above (0: none).  SMALL: short code rather than few
+// instructions, for calls that are so small that they wait for their code to be fetched.
+template <class T, bool CEIL, bool SMALL>
+__device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0, int t1, const Wants &want, bool exact,
+                                         float ref, float bound, u64 *list, double *turns, int last_quota) {
+  constexpr int N = Vec<T>::N;
+  const int lane = threadIdx.x & 63;
+  const float k32 = (float)want.k, far = (float)(kFar / want.k);
+  // (the second part of k, above 0: the product of -inf with it is -inf, too)
+  const float hi = CEIL ? k32 : __builtin_bit_cast(float, __builtin_bit_cast(unsigned, k32) - 1), lo = (float)(want.k - hi);
+  Stretch out = {-__builtin_inff(), -__builtin_inff(), 0., 0., 0., want.none ? __builtin_inff() : bound, -__FLT_MAX__, 0};
+  float largest = -__builtin_inff();
+  bool stop = false;
+  double sum = 0, part = 0;
+  Powers e;
+  e.unit = 1.;
+  e.refer_to(ref > -__builtin_inff() ? ref : 0.f, want.k);
+  double of_ref = e.of(ref);   // (powers in fp32 are relative to ref's own)
+  const auto refer_to = [&](float to) {
+    const double from = e.shift;
+    const bool none = ref == -__builtin_inff();
+    e.refer_to(to, want.k);
+    Powers last = e;
+    last.shift = from;
+    const double scale = none ? 0. : last.scale_to(e.shift);
+    sum *= scale;
+    part = none ? 0. : part * scale;
+    if (turns) turns[lane] *= scale;
+    ref = to;
+    of_ref = e.of(ref);
+  };
+  const auto logit_at = [&](int j) { return logit_of<T>(list[j]); };
+  // An element is looked at more closely from here on: it belongs to the list, or the powers' reference has to
+  // move (so that none is past 2^100).
+  const auto threshold = [&] { return CEIL ? out.bound : __builtin_fminf(out.bound, ref + far); };
+  float close = threshold();
+  const auto vector = [&](int at, float (&x)[N]) {   // at: the index of its first element
+    float most = x[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) most = maximum(most, x[j]);
+    largest = maximum(largest, most);
+    if (__any(!(most < close))) {
+      if (__any(!(most < (CEIL ? __builtin_inff() : ref + far)))) {
+        const float top = wave_maximum(most);
+        stop = stop || !(top < __builtin_inff());   // NaN or +inf: nothing of the row is needed
+        if (!CEIL && !stop && top > -__builtin_inff()) {
+          refer_to(top);
+          out.bound = __builtin_fmaxf(out.bound, bound_of(want, top, top, 1., V));
+          close = threshold();
+        }
+      }
+      if (__any(most >= out.bound)) {
+        append<T, !CEIL>(list, out.n, at, x, out.bound, V);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = x[j] < out.bound ? x[j] : -__builtin_inff();
+      }
+    }
+    if (!CEIL && exact) {
+      double s[2];
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[j & 1] = j < 2 ? e.of(x[j]) : s[j & 1] + e.of(x[j]);
+      part += s[0] + s[1];
+    } else {
+      // (the difference before the product, which then has an error of its own size; in the sampler k has two parts)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float d = x[j] - ref;
+        x[j] = __builtin_amdgcn_exp2f(CEIL ? d * hi : __builtin_fmaf(d, hi, d * lo));
+      }
+#pragma unroll
+      for (int d = 1; d < N; d *= 2)
+#pragma unroll
+        for (int j = 0; j < N; j += 2 * d) x[j] += x[j + d];
+      part += (double)x[0] * of_ref;
+    }
+  };
+  if (turns) turns[lane] = 0.;
+  for (int t = t0; t < t1; ++t) {
+    part = 0;
+    const bool more = t + 1 < t1;
+    const int first = (t * kTurn + lane) * N;
+    if constexpr (SMALL) {
+      Turn<T> next;
+      if (more) next.load(z, t + 1, V);
+#pragma unroll 1
+      for (int i = 0; i < kTurnVecs; ++i) {
+        float x[N];
+        Vec<T>::unpack(now.pick(i), x);
+        vector(first + i * 64 * N, x);
+      }
+      if (more) now = next;
+    } else {
+      const bool whole = (t + 2) * kTurn * N <= V;   // (the next turn)
+#pragma unroll
+      for (int i = 0; i < kTurnVecs; ++i) {
+        float x[N];
+        Vec<T>::unpack(now.v[i], x);
+        if (more) {   // its place takes the next turn's
+          const int at = (t + 1) * kTurn + 64 * i + lane;
+          now.v[i] = whole ? Vec<T>::load(z + (int64_t)at * N) : row_vector(z, at, V);
+        }
+        vector(first + i * 64 * N, x);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (stop || out.n > kListMost) {
+      out.top = wave_maximum(largest);
+      if (stop) out.n = 0;
+      return out;
+    }
+    if (ref == -__builtin_inff()) part = 0;   // (no logits so far)
+    if (turns) {
+      part = part < 0x1p-980 ? 0. : part;   // (nothing but powers that are none)
+      const double all = wave_sum(part);
+      if (lane == 0) turns[t - t0] = all;
+    }
+    sum += part;
+    part = 0;
+    const bool raise = out.n > want.most, last = !more && last_quota > 0 && out.n >= last_quota;
+    if (!raise && !last) continue;
+    wave_sync();
+    float b = -__FLT_MAX__;
+    if (want.quota > 0) {
+      b = nth_of_list<T>(list, out.n, raise ? want.quota : last_quota);
+    } else {
+      double all = sum;
+      for (int j = lane; j < out.n; j += 64) all += e.of(logit_at(j));
+      b = bound_of(want, wave_maximum(largest), ref, wave_sum(all) / e.of(ref), V);
+    }
+    b = __builtin_fmaxf(out.bound, b);
+    if (!more) out.last_bound = b;
+    if (!raise) continue;
+    // the bound rises, and what is below it is dropped
+    out.bound = b;
+    if (CEIL && b - ref > far) refer_to(b);
+    close = threshold();
+    int n = 0;
+    for (int j = 0; j < out.n; j += 64) {
+      const u64 r = j + lane < out.n ? list[j + lane] : 0;
+      const float x = logit_of<T>(r);
+      const bool in = j + lane < out.n, stays = in && x >= out.bound;
+      const u64 stay = __ballot(stays);
+      if (stays) list[n + lanes_before(stay)] = r;
+      if (in && !stays) sum += e.of(x);
+      n += __builtin_popcountll(stay);
+    }
+    out.n = n;
+    wave_sync();
+    if (n > want.most) {   // (more of them than a list is for)
+      out.n = kListMost + 1;
+      return out;
+    }
+  }
+  out.top = wave_maximum(largest);
+  out.ref = ref;
+  out.shift = ref == -__builtin_inff() ? 0. : e.shift;
+  out.sum = wave_sum(sum);
+  if (CEIL) out.sum /= of_ref;   // (relative to ref)
+  if (!CEIL && out.n > 0) {
+    wave_sync();
+    double all = 0;
+    for (int j = lane; j < out.n; j += 64) all += e.of(logit_at(j));
+    out.listed = wave_sum(all);
+  }
+  return out;
+}
+
+// Keys of a list at which the bound is raised to its quota-th largest (which leaves quota + quota / 8 + 8
+// of them): often while it rises, and with room for those of another turn, some quota in the beginning.
+__device__ __forceinline__ int raise_at(int quota) {
+  const int often = 2 * quota + 64, room = kListMost - 2 * quota - 32;
+  return often < room ? often : room;
+}
+// A row's stretches: W waves, turns [0, turns) of the row in W parts.
+__device__ __forceinline__ int stretch_turn(int turns, int w, int W) { return (int)((int64_t)turns * w / W); }
+template <class T>
+__device__ __forceinline__ int turns_of(int V) {
+  return ((V + Vec<T>::N - 1) / Vec<T>::N + kTurn - 1) / kTurn;
+}
+
+// The token of a row that is read from memory for every pass over it, by the THR threads of a block.  chunk: LDS,
+// one for each 64 vectors of the row (it may be in the histogram's place).
 template <class T, int THR>
-__device__ __forceinline__ void sample_from_memory(const T *z, float top, const Settings &s, const Powers &e, int64_t row,
-                                                   const SampleParams &p, SelectLds &lds, double *wave, double *chunk) {
+__device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s, int64_t row, const SampleParams &p,
+                                                   BlockLds<THR> &lds, double *wave, double *chunk) {
   constexpr int N = Vec<T>::N, W = THR / 64;
   const int tid = threadIdx.x, lane = tid & 63, V = p.vocab, vecs = (V + N - 1) / N;
-  RowSource<T, THR> src = {z, V};
+  float top = -__builtin_inff();
+  for (int at = tid; at < vecs; at += THR) {
+    float x[N];
+    Vec<T>::unpack(row_vector(z, at, V), x);
+#pragma unroll
+    for (int e = 0; e < N; ++e) top = maximum(top, x[e]);
+  }
+  top = wave_maximum(top);
+  __syncthreads();
+  if (lane == 0) wave[tid >> 6] = top;
+  __syncthreads();
+  top = wave_maximum((float)wave[lane % W]);
+  __syncthreads();
+  if (!(__builtin_fabsf(top) < __builtin_inff())) {
+    if (tid == 0) write_bad(p, row);
+    return;
+  }
+  Powers e;
+  e.refer_to(top, s.k);
+  e.unit = __builtin_amdgcn_ldexp(1., p.mass_bits);
   double all = 0;
-  src.each([&](int, float x) { all += e.of(x); });
+  for (int at = tid; at < vecs; at += THR) {
+    float x[N];
+    Vec<T>::unpack(row_vector(z, at, V), x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) all += e.of(x[i]);
+  }
   all = block_sum_in_order<THR>(all, wave);
-  const Kept kept = {s.by_k || s.by_p ? filter_border<THR>(src, (u64)down_key(top) << 32, kLastKey, s, e, all, lds) : ~(u64)0,
-                     __builtin_fmax(s.min_p, kNoPower)};
+  u64 border = last_key<T>(-__FLT_MAX__);
+  if (s.by_k)
+    border = find_border_in_row<T, THR, true>(z, V, first_key<T>(top), border, [](float) { return (u64)1; },
+                                              [&](u64) { return (u64)s.top_k; }, lds);
+  if (s.by_p)
+    border = find_border_in_row<T, THR, false>(z, V, first_key<T>(top), border, [&](float x) { return e.mass(x); },
+                                               [&](u64 total) { return target_of_p(s, e, total, all); }, lds);
+  const Kept<T> kept = {border, __builtin_fmax(s.min_p * e.of(top), kNoPower)};
+  const float edge = logit_of<T>(border);   // (of the last token that is kept)
   const auto weigh = [&](int vec, float (&x)[N]) {
     Vec<T>::unpack(row_vector(z, vec, V), x);
-    double t = 0;
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < N; ++i) t += kept.power(e, vec * N + i, x[i]);
+    for (int i = 0; i < N; ++i) any = any || x[i] >= edge;
+    double t = 0;
+    if (__any(any)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) t += kept.power(e, vec * N + i, x[i]);
+    }
     return t;
   };
-  // the draw: a wave's 64 vectors of a turn are consecutive, so the chunks are in order
-  const int turns = (vecs + THR - 1) / THR, chunks = turns * W;
+  // the draw: a wave's 64 vectors are consecutive, so the chunks are in order
+  const int chunks = (vecs + 63) / 64;
   float x[N];
-  for (int t = 0; t < turns; ++t) {
-    const double sum = wave_sum(weigh(t * THR + tid, x));
-    if (lane == 0) chunk[t * W + (tid >> 6)] = sum;
+  for (int c = tid >> 6; c < chunks; c += W) {
+    const double sum = wave_sum(weigh(c * 64 + lane, x));
+    if (lane == 0) chunk[c] = sum;
   }
   __syncthreads();
-  if (tid >= 64) return;
+  if (tid >= 64) return;   // (they wait for the first wave at the next row)
   double total = 0;
   for (int c = lane; c < chunks; c += 64) total += chunk[c];
   total = wave_sum(total);
@@ -445,168 +844,332 @@ __device__ __forceinline__ void sample_from_memory(const T *z, float top, const 
   const int n = N < V - v * N ? N : V - v * N;
   const float mine = Vec<T>::load1(z + (lane < n ? v * N + lane : V - 1));
   const int i = find_part(n, target - before - more, [&](int j) { return kept.power(e, v * N + j, mine); }, last);
-  if (lane == i) write_token(p, row, s, v * N + i, mine, top, all, total);
+  if (lane == i) write_token(p, row, s, e, v * N + i, mine, top, all, total);
 }
 
-// A row that is held in registers, one block for it.
-template <class T, int THR, int K>
-__global__ __launch_bounds__(THR) void sample_kernel(const T *logits, SampleParams p) {
-  constexpr int N = Vec<T>::N, W = THR / 64;
-  static_assert(64 * K <= THR && K <= kListMost, "a wave's stretch is one vector a thread; its turns fit in its list");
-  __shared__ SelectLds lds;
-  __shared__ u64 lists[W][kListMost];
-  __shared__ double wave[W];
-  __shared__ float wave_top[W];
-  __shared__ int counts[W];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 63, V = p.vocab;
-  const T *z = logits + row * p.ld_logits;
-  const Settings s = settings_of(p, row);
-  HeldRow<T, K> held(z, V);
-  float mine = -__builtin_inff();
-  held.vectors([&](int, const float (&x)[N]) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) mine = maximum(mine, x[e]);
-  });
-  const float top = block_maximum<THR>(mine, wave_top);
-  if (!(__builtin_fabsf(top) < __builtin_inff()) || !s.good) {   // NaN or +inf in the row, nothing but -inf, no such temperature
-    if (tid == 0) write_bad(p, row);
-    return;
-  }
-  const Powers e = {top, s.k, __builtin_amdgcn_ldexp(1., p.mass_bits)};
-  double all = 0;
-  if (s.by_k || s.by_p || s.min_p > 0.) {
-    // a logit that the filters' last token is not below
-    const u64 first = (u64)down_key(top) << 32;
-    const auto below = [&](double b) {   // b, and errors of 1e-6
-      return (float)__builtin_fmax(b - 1e-6 * (__builtin_fabs(b) + __builtin_fabs(top)), -__FLT_MAX__);
-    };
-    float least = -__FLT_MAX__;
-    if (s.greedy) {
-      least = top;
-    } else if (s.by_k && s.top_k <= THR) {
-      // that many threads' largest ones are not below their top_k-th
-      ThreadSource src = {mine};
-      const u64 b = find_border<THR, 2>(src, first, kLastKey, [](float) { return (u64)1; }, [&](u64) { return (u64)s.top_k; }, lds);
-      least = logit_of((unsigned)(b >> 32));
-    } else if (s.by_p && !s.by_k) {
-      // all tokens below it have less than 1 - top_p of what the largest one alone has
-      least = below(top + s.temp * log((1. - s.top_p) / V));
-    }
-    if (s.min_p > 0. && !(s.by_k && s.by_p)) least = __builtin_fmaxf(least, below(top + s.temp * log(s.min_p)));
-    // (without a bound every element goes into the lists: only where they hold a row)
-    int n = least > -__FLT_MAX__ || V <= W * kListMost ? 0 : kListMost + 1;
-    if (n == 0) {
-      if (s.by_p && !s.by_k) {
-        held.vectors([&](int at, const float (&x)[N]) {
-          append(lists[tid >> 6], n, at, x, least, V);
-          double t = 0;
-#pragma unroll
-          for (int i = 0; i < N; ++i) t += e.of(x[i]);
-          all += t;
-        });
-      } else {
-        // the sum is not for a border: below the bound, powers are fp32 with the exponent's product in two parts
-        const float hi = (float)s.k, lo = (float)(s.k - hi);
-        held.vectors([&](int at, const float (&x)[N]) {
-          float y[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i) y[i] = x[i];
-          if (append(lists[tid >> 6], n, at, x, least, V)) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) y[i] = x[i] < least ? x[i] : -__builtin_inff();
-          }
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float d = __builtin_fmaxf(y[i] - top, -__FLT_MAX__);
-            y[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(d, hi, d * lo));
-          }
-#pragma unroll
-          for (int d = 1; d < N; d *= 2)
-#pragma unroll
-            for (int i = 0; i < N; i += 2 * d) y[i] += y[i + d];
-          all += (double)y[0];
-        });
-      }
-    }
-    ListSource src = {lists[tid >> 6], n <= kListMost ? n : 0};
-    if (!(s.by_p && !s.by_k)) src.each([&](int, float x) { all += e.of(x); });
-    if (lane == 0) counts[tid >> 6] = n;
-    all = block_sum_in_order<THR>(all, wave);
-    bool fits = true;
-#pragma unroll
-    for (int w = 0; w < W; ++w) fits = fits && counts[w] <= kListMost;
-    if (!fits) {
-      __syncthreads();
-      sample_from_memory<T, THR>(z, top, s, e, row, p, lds, wave, reinterpret_cast<double *>(&lists[0][0]));
-      return;
-    }
-    const Kept kept = {s.by_k || s.by_p ? filter_border<THR>(src, first, kLastKey, s, e, all, lds) : ~(u64)0,
-                       __builtin_fmax(s.min_p, kNoPower)};
-    // the draw, over the lists in the order of their indices
-    double t = 0;
-    src.each([&](int index, float x) { t += kept.power(e, index, x); });
-    const double total = block_sum_in_order<THR>(t, wave), target = uniform_of(p, row) * total;
-    if (tid >= 64) return;
-    double before, more;
-    const int w = find_part(W, target, [&](int i) { return wave[i]; }, before);
-    const u64 *list = lists[w];
-    const auto at = [&](int j) { return kept.power(e, (int)(unsigned)list[j], logit_of((unsigned)(list[j] >> 32))); };
-    const int j = find_part(counts[w], target - before, at, more);
-    if (lane == 0) write_token(p, row, s, (int)(unsigned)list[j], logit_of((unsigned)(list[j] >> 32)), top, all, total);
-    return;
-  }
+template <int W>
+struct RowLds {
+  static constexpr int kJoined = W == 1 ? 512 : W < 8 ? 1024 : 2048;   // keys of the joined list
+  static constexpr int kRanked = W == 1 ? 192 : 512;    // and those that are ranked by counting
+  union {
+    u64 list[W][kListMost];
+    double turns[W][kTurns];
+  };
+  u64 joined_list[W == 1 ? 1 : kJoined];
+  union {
+    Histogram<kWaveBins> wave;
+    u64 sorted[kRanked];
+  };
+  Stretch out[W];
+  float first_top[W], first_bound[W], bound[W], last_bound[W];
+  double part[W];
+  int count[W];
+  __device__ __forceinline__ u64 *joined() { return W == 1 ? &list[0][0] : joined_list; }
+};
 
-  // all tokens: what each wave's stretch weighs, then the vectors of one stretch
-  held.vectors([&](int, const float (&x)[N]) {
-    double t = 0;
+// The n-th largest of W numbers in LDS, one wave.
+template <int W>
+__device__ __forceinline__ float nth_bound(const float *bound, int n) {
+  if constexpr (W == 1) return bound[0];
+  const int lane = threadIdx.x & 63;
+  const float mine = lane < W ? bound[lane] : -__builtin_inff();
+  int rank = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) t += e.of(x[i]);
-    all += t;
-  });
-  all = block_sum_in_order<THR>(all < 0x1p-980 ? 0. : all, wave);   // (nothing but powers that are none)
-  const Kept kept = {~(u64)0, kNoPower};
-  const double target = uniform_of(p, row) * all;
-  double before;
-  const int w = find_part(W, target, [&](int i) { return wave[i]; }, before);   // (every wave finds the same)
-  float x[N];
-  const int vec = w * 64 * K + tid;
-  Vec<T>::unpack(row_vector(z, tid < 64 * K ? vec : V, V), x);
-  double t = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) t += kept.power(e, vec * N + i, x[i]);
-  double *part = reinterpret_cast<double *>(&lists[0][0]);
-  part[tid] = t;
+  for (int i = 0; i < W; ++i) {
+    const float b = from_lane(mine, i);
+    rank += b > mine || (b == mine && i < lane) ? 1 : 0;
+  }
+  return from_lane(mine, lane_of(__ballot(lane < W && rank == n - 1)));
+}
+
+// How W waves find a bound that is not above the k-th largest logit of all: each takes its quota-th
+// largest (a little more than its share of k), and `ranks` of them have quota logits from their bounds on, k together.
+// More ranks than waves: no bound.
+struct Shares {
+  int quota, ranks;
+};
+template <int W>
+__device__ __forceinline__ Shares shares_of(int k) {
+  if (k <= 0) return {0, 1};
+  int q = W == 1 ? k : (k + k / 4 + W - 1) / W + 1;
+  q = q < kQuota ? q : kQuota;
+  // (a quotient below 2^20 by fp32: half a unit off a whole number before it is cut off)
+  return {q, (int)(((float)(k + q - 1) + 0.5f) * __builtin_amdgcn_rcpf((float)q))};
+}
+
+// What a block knows of a row from its waves' first turns: the largest logit, and a bound for its k
+// largest.  Every wave calls it.
+template <class T, int W>
+__device__ __forceinline__ void first_bounds(Turn<T> &now, Shares share, RowLds<W> &lds, float &top, float &bound) {
+  float most[kTurnVecs];
+  top = wave_maximum(turn_maximum(now, most));
+  bound = -__FLT_MAX__;
+  const bool any = share.quota > 0 && share.ranks <= W;
+  if (any && top < __builtin_inff()) bound = __builtin_fmaxf(bound, nth_largest(most, share.quota));
+  if constexpr (W > 1) {
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      lds.first_top[w] = top;
+      lds.first_bound[w] = bound;
+    }
+    __syncthreads();
+    top = wave_maximum(lds.first_top[(threadIdx.x & 63) < W ? threadIdx.x & 63 : 0]);
+    if (any) bound = nth_bound<W>(lds.first_bound, share.ranks);
+  }
+}
+// What a wave leaves of its stretch for the others; the block waits behind it.
+template <int W>
+__device__ __forceinline__ void leave_stretch(const Stretch &mine, RowLds<W> &lds) {
+  const int w = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) {
+    lds.out[w] = mine;
+    lds.bound[w] = mine.bound;
+    lds.last_bound[w] = mine.last_bound;
+  }
   __syncthreads();
-  if (tid >= 64) return;
-  double more, last;
-  const int v = w * 64 * K + find_part(64 * K, target - before, [&](int i) { return part[i]; }, more);
-  const int n = N < V - v * N ? N : V - v * N;
-  const float own = Vec<T>::load1(z + (lane < n ? v * N + lane : V - 1));
-  const int i = find_part(n, target - before - more, [&](int j) { return kept.power(e, v * N + j, own); }, last);
-  if (lane == i) write_token(p, row, s, v * N + i, own, top, all, all);
+}
+// What the stretches come to together: every wave calls it, lane i has the i-th stretch's shift, sum and sum
+// with what is listed (lanes from W on: none).
+struct Together {
+  float top;
+  bool fits;
+  int listed;
+  double shift, sum, all;
+};
+template <int W>
+__device__ __forceinline__ Together together(const RowLds<W> &lds) {
+  const int lane = threadIdx.x & 63;
+  const Stretch &x = lds.out[lane < W ? lane : 0];
+  const bool in = lane < W;
+  Together t;
+  t.top = wave_maximum(in ? x.top : -__builtin_inff());
+  t.fits = __ballot(in && x.n > kListMost) == 0;
+  t.listed = (int)wave_reduce(in ? (unsigned)x.n : 0u, 0u, [](unsigned a, unsigned b) { return a + b; });
+  t.shift = in ? x.shift : 0.;
+  t.sum = in ? x.sum : 0.;
+  t.all = in ? x.sum + x.listed : 0.;
+  return t;
 }
 
-// A row that is too long for that.
-template <class T, int THR>
-__global__ __launch_bounds__(THR) void sample_long_kernel(const T *logits, SampleParams p) {
-  extern __shared__ double chunk[];
-  __shared__ SelectLds lds;
-  __shared__ double wave[THR / 64];
-  __shared__ float wave_top[THR / 64];
+// The stretches' lists, from bound on, in one, in their order; its length, or kJoined + 1 where it does
+// not fit.  Every wave calls it; the block waits at its end.
+template <class T, int W>
+__device__ __forceinline__ int join_lists(RowLds<W> &lds, float bound) {
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lds.out[w].n;
+  const u64 *list = lds.list[w];
+  int at = 0, total = 0;
+  if constexpr (W > 1) {
+    int mine = 0;
+    for (int j = 0; j < n; j += 64) {
+      const u64 r = j + lane < n ? list[j + lane] : ~(u64)0;
+      mine += __builtin_popcountll(__ballot(j + lane < n && logit_of<T>(r) >= bound));
+    }
+    if (lane == 0) lds.count[w] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (i < w) at += lds.count[i];
+      total += lds.count[i];
+    }
+    if (total > RowLds<W>::kJoined) return RowLds<W>::kJoined + 1;
+  }
+  for (int j = 0; j < n; j += 64) {   // (one wave's list is shortened in its place)
+    const u64 r = j + lane < n ? list[j + lane] : ~(u64)0;
+    const bool in = j + lane < n && logit_of<T>(r) >= bound;
+    const u64 all = __ballot(in);
+    if (in) lds.joined()[at + lanes_before(all)] = r;
+    at += __builtin_popcountll(all);
+  }
+  __syncthreads();
+  if constexpr (W == 1) return at <= RowLds<W>::kJoined ? at : RowLds<W>::kJoined + 1;
+  return total;
+}
+// How many of n keys are below r.
+__device__ __forceinline__ int rank_among(const u64 *keys, int n, u64 r) {
+  int rank = 0, i = 0;
+  for (; i + 8 <= n; i += 8) {   // (eight reads in flight)
+    u64 x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = keys[i + j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rank += x[j] < r ? 1 : 0;
+  }
+  for (; i < n; ++i) rank += keys[i] < r ? 1 : 0;
+  return rank;
+}
+
+// W waves take a row.  later: the rows that they cannot do are marked there for a second launch (a small
+// block is not made for going through a row several times).
+template <class T, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) void sample_kernel(const T *logits, SampleParams p,
+                                                                                            int32_t *later) {
+  constexpr int N = Vec<T>::N;
+  __shared__ RowLds<W> lds;
   const int64_t row = blockIdx.x;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, V = p.vocab, turns = turns_of<T>(V);
   const T *z = logits + row * p.ld_logits;
-  const RowSource<T, THR> src = {z, p.vocab};
+  const int t0 = stretch_turn(turns, w, W), t1 = stretch_turn(turns, w + 1, W);
+  Turn<T> now;
+  now.load(z, t0 < t1 ? t0 : turns, V);
   const Settings s = settings_of(p, row);
-  float mine = -__builtin_inff();
-  src.each([&](int, float x) { mine = maximum(mine, x); });
-  const float top = block_maximum<THR>(mine, wave_top);
-  if (!(__builtin_fabsf(top) < __builtin_inff()) || !s.good) {
+  if (threadIdx.x == 0) gmem(later)[row] = 0;
+  if (!s.good) {
     if (threadIdx.x == 0) write_bad(p, row);
     return;
   }
-  const Powers e = {top, s.k, __builtin_amdgcn_ldexp(1., p.mass_bits)};
-  sample_from_memory<T, THR>(z, top, s, e, row, p, lds, wave, chunk);
+  const bool everything = !s.by_k && !s.by_p && s.min_p == 0., exact = everything || (s.by_p && !s.by_k);
+  const int quota = s.by_k ? s.top_k < kQuota ? s.top_k : kQuota : 0;
+  const Shares share = shares_of<W>(s.by_k ? s.top_k : 0);
+  const Wants want = {quota, quota > 0 ? raise_at(quota) : kListMost - 256, s.k, s.temp,
+                      s.by_p && !s.by_k ? 1. - s.top_p : 0., s.by_k && s.by_p ? 0. : s.min_p, everything};
+  float top, bound;
+  first_bounds<T, W>(now, share, lds, top, bound);
+  if (!(top < __builtin_inff())) {
+    if (threadIdx.x == 0) write_bad(p, row);
+    return;
+  }
+  if (top > -__builtin_inff()) bound = __builtin_fmaxf(bound, bound_of(want, top, top, 1., V));
+  const Stretch mine = sweep<T, false, (W >= 16)>(now, z, V, t0, t1, want, exact, top, bound, lds.list[w],
+                                                  everything ? lds.turns[w] : nullptr,
+                                                  t1 - t0 > 1 && share.ranks <= W ? share.quota : 0);
+  leave_stretch<W>(mine, lds);
+  const Together row_of = together(lds);
+  top = row_of.top;
+  const bool fits = row_of.fits;
+  if (fits && !(__builtin_fabsf(top) < __builtin_inff())) {   // NaN or +inf in the row, nothing but -inf
+    if (threadIdx.x == 0) write_bad(p, row);
+    return;
+  }
+  Powers e;
+    e.refer_to(top, s.k);
+    e.unit = __builtin_amdgcn_ldexp(1., p.mass_bits);
+  // (a stretch's powers to the row's; without logits it has none)
+  Powers own = e;
+  own.shift = row_of.shift;
+  const double relative = row_of.shift == 0. ? 0. : own.scale_to(e.shift);
+  const double part_of_all = row_of.all * relative, all = wave_sum(part_of_all);
+  if (everything) {
+    if (w > 0) return;
+    // what each stretch weighs, then the turns of one, the vectors of one turn, the elements of one vector
+    const Kept<T> kept = {~(u64)0, kNoPower};
+    const double target = uniform_of(p, row) * all;
+    double before, more, last;
+    const int in = find_part(W, target, [&](int) { return part_of_all; }, before);
+    const double scale = from_lane(relative, in);
+    const int s0 = stretch_turn(turns, in, W), s1 = stretch_turn(turns, in + 1, W);
+    const int turn = s0 + find_part(s1 - s0, target - before, [&](int i) { return lds.turns[in][i] * scale; }, more);
+    now.load(z, turn, V);
+    double left = target - before - more, seen_left = 0;
+    int v = -1, seen = 0;
+#pragma unroll 1
+    for (int i = 0; i < kTurnVecs && v < 0; ++i) {
+      float x[N];
+      Vec<T>::unpack(now.pick(i), x);
+      double own = 0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) own += kept.power(e, 0, x[j]);
+      const double total = wave_sum(own);
+      if (total > 0.) {
+        double past;
+        seen = (turn * kTurnVecs + i) * 64 + find_part(64, left, [&](int) { return own; }, past);
+        seen_left = left - past;
+        if (total > left) v = seen;
+      }
+      left -= total;
+    }
+    if (v < 0) v = seen;   // (the target is the whole sum, to within its rounding)
+    const int n = N < V - v * N ? N : V - v * N;
+    const float x = Vec<T>::load1(z + (lane < n ? v * N + lane : V - 1));
+    const int i = find_part(n, seen_left, [&](int) { return kept.power(e, 0, x); }, last);
+    if (lane == i) write_token(p, row, s, e, v * N + i, x, top, all, all);
+    return;
+  }
+  if (fits) {
+    bound = -__FLT_MAX__;
+    if (quota > 0 && share.ranks <= W) bound = nth_bound<W>(lds.last_bound, share.ranks);
+    bound = __builtin_fmaxf(bound, bound_of(want, top, top, all / e.of(top), V));
+    const int n = join_lists<T>(lds, bound);
+    if (n > RowLds<W>::kJoined || (w > 0 && n > RowLds<W>::kRanked)) {
+      if (n > RowLds<W>::kJoined && threadIdx.x == 0) gmem(later)[row] = 1;
+      return;
+    }
+    const u64 *list = lds.joined();
+    if (s.top_k > kQuota && s.by_k) {
+      // (the bound of a stretch followed its kQuota-th largest: the top_k largest are in the lists if that many
+      // are not below the largest bound)
+      const float most = nth_bound<W>(lds.bound, 1);
+      int c = 0;
+      for (int j = 0; j < n; j += 64)
+        c += __builtin_popcountll(__ballot(j + lane < n && logit_of<T>(list[j + lane < n ? j + lane : 0]) >= most));
+      if (c < s.top_k) {
+        if (threadIdx.x == 0) gmem(later)[row] = 1;
+        return;
+      }
+    }
+    u64 border = ~(u64)0;
+    if (n <= RowLds<W>::kRanked && (s.by_k || s.by_p)) {
+      // the keys in their order, and how many of them the filters keep
+      for (int j = threadIdx.x; j < n; j += 64 * W) lds.sorted[rank_among(list, n, list[j])] = list[j];
+      __syncthreads();
+      if (w > 0) return;
+      int keep = s.by_k && s.top_k < n ? s.top_k : n;
+      if (s.by_p) {
+        const auto power = [&](int j) { return j < keep ? e.of(logit_of<T>(lds.sorted[j])) : 0.; };
+        double before = 0, of = all;
+        if (s.by_k) {
+          of = 0;
+          for (int j = lane; j < keep; j += 64) of += power(j);
+          of = wave_sum(of);
+        }
+        const double target = s.top_p * of;   // (the first ones that sum to it)
+        int less = 0;
+        for (int j = 0; j < keep; j += 64) {
+          const double upto = wave_scan(power(j + lane));
+          less += __builtin_popcountll(__ballot(j + lane < keep && before + upto < target));
+          before += from_lane(upto, 63);
+        }
+        keep = less + 1 < keep ? less + 1 : keep;
+      }
+      border = lds.sorted[keep - 1];
+    } else {
+      if (w > 0) return;
+      const u64 first = first_key<T>(top);
+      border = last_key<T>(bound);
+      if (s.by_k)
+        border = find_border<true>(list, n, first, border, [](u64) { return (u64)1; }, [&](u64) { return (u64)s.top_k; }, lds.wave);
+      if (s.by_p)
+        border = find_border<false>(list, n, first, border, [&](u64 r) { return e.mass(logit_of<T>(r)); },
+                                    [&](u64 total) { return target_of_p(s, e, total, all); }, lds.wave);
+    }
+    const Kept<T> kept = {border, __builtin_fmax(s.min_p * e.of(top), kNoPower)};
+    const auto power = [&](int j) { return kept.power(e, index_of(list[j]), logit_of<T>(list[j])); };
+    double t = 0;
+    for (int j = lane; j < n; j += 64) t += power(j);
+    const double total = wave_sum(t);
+    double before;
+    const int j = find_part(n, uniform_of(p, row) * total, power, before);
+    if (lane == 0) write_token(p, row, s, e, index_of(list[j]), logit_of<T>(list[j]), top, all, total);
+    return;
+  }
+  if (threadIdx.x == 0) gmem(later)[row] = 1;
+}
+
+// The rows that were left, in blocks of 1024 threads.
+constexpr int kLaterThreads = 1024, kLaterBlocks = 512;
+template <class T>
+__global__ __launch_bounds__(kLaterThreads) void sample_later_kernel(const T *logits, SampleParams p, const int32_t *later,
+                                                                     int32_t rows) {
+  constexpr int THR = kLaterThreads;
+  __shared__ union {
+    BlockLds<THR> block;
+    double chunk[HIMUON_TOP_VOCAB / (4 * 64)];
+  } lds;
+  __shared__ double wave[THR / 64];
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    if (gmem(later)[row] == 0) continue;
+    sample_from_memory<T, THR>(logits + row * p.ld_logits, settings_of(p, row), row, p, lds.block, wave, lds.chunk);
+    __syncthreads();
+  }
 }
 
 struct TopParams {
@@ -617,6 +1180,7 @@ struct TopParams {
   int32_t vocab, k;
   float k2;         // log2(e) / temperature
   float inv_temp;
+  double k1, temp;  // log2(e) / temperature, temperature
 };
 
 // Sorts n keys (a power of two, 64 at least).
@@ -637,169 +1201,195 @@ __device__ __forceinline__ void sort_keys(u64 *keys, int n) {
 }
 __device__ __forceinline__ int sort_size(int n) { return n <= 64 ? 64 : 1 << (32 - __builtin_clz(n - 1)); }
 
+constexpr int top_most(int W) { return W >= 8 ? HIMUON_TOP_MOST : kQuota * W; }   // k of a block of W waves
 template <int THR>
-struct TopLds {
-  SelectLds select;
-  u64 keys[HIMUON_TOP_MOST];   // the largest, to be sorted
-  Softmax waves[THR / 64];
-  int n;
-};
-
-// The elements of a source up to border (k of them) are sorted and written; the others' sum.
-template <class T, int THR, class SOURCE>
-__device__ __forceinline__ void write_top(SOURCE &src, u64 border, const TopParams &p, int64_t row, TopLds<THR> &lds) {
-  const int n = sort_size(p.k);
-  for (int i = threadIdx.x; i < n; i += THR) lds.keys[i] = ~(u64)0;
-  if (threadIdx.x == 0) lds.n = 0;
-  __syncthreads();
-  src.each([&](int index, float x) {
-    const u64 r = rank_key(x, index);
-    if (r <= border) lds.keys[atomicAdd(&lds.n, 1)] = r;
-  });
-  __syncthreads();
-  sort_keys<THR>(lds.keys, n);
-  for (int i = threadIdx.x; i < p.k; i += THR) {
-    const u64 r = lds.keys[i];
-    gmem(p.index)[row * p.ld_top + i] = (int)(unsigned)r;
-    Vec<T>::store1(reinterpret_cast<T *>(p.value) + row * p.ld_top + i, logit_of((unsigned)(r >> 32)));
-  }
-}
-template <int THR>
-__device__ __forceinline__ void write_rest(float max, float sum, const TopParams &p, int64_t row, TopLds<THR> &lds) {
-  const Softmax s = block_softmax<THR / 64>(max, sum, p.k2, lds.waves);
+__device__ __forceinline__ void write_rest(float max, float sum, const TopParams &p, int64_t row, Softmax *waves) {
+  const Softmax s = block_softmax<THR / 64>(max, sum, p.k2, waves);
   if (threadIdx.x == 0)
     gmem(p.rest)[row] = s.sum == 0.f ? -__builtin_inff() : s.ref * p.inv_temp + kLn2 * __builtin_amdgcn_logf(s.sum);
 }
-// The same from a whole row, by its border.
-template <class T, int THR, class SOURCE>
-__device__ __forceinline__ void top_of_all(SOURCE &src, const TopParams &p, int64_t row, TopLds<THR> &lds) {
-  u64 border = ~(u64)0;
-  if (p.k < p.vocab)
-    border = find_border<THR>(src, 0, ~(u64)0, [](float) { return (u64)1; }, [&](u64) { return (u64)p.k; }, lds.select);
-  write_top<T, THR>(src, border, p, row, lds);
-  float m = -__builtin_inff(), sum = 0.f;
-  src.each([&](int index, float x) {
-    if (rank_key(x, index) > border) m = __builtin_fmaxf(m, x);
-  });
-  const float ref = ref_of(m);
-  src.each([&](int index, float x) {
-    if (rank_key(x, index) > border) sum += pow2(x, p.k2, ref);
-  });
-  write_rest<THR>(m, sum, p, row, lds);
+template <class T>
+__device__ __forceinline__ void write_entry(u64 key, int i, const TopParams &p, int64_t row) {
+  gmem(p.index)[row * p.ld_top + i] = index_of(key);
+  Vec<T>::store1(reinterpret_cast<T *>(p.value) + row * p.ld_top + i, logit_of<T>(key));
 }
 
-template <class T, int THR, int K>
-__global__ __launch_bounds__(THR) void top_kernel(const T *logits, TopParams p) {
-  constexpr int N = Vec<T>::N, W = THR / 64;
-  __shared__ TopLds<THR> lds;
-  __shared__ u64 lists[W][kListMost];
-  __shared__ float wave_top[W];
-  __shared__ int counts[W];
+template <class T, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) void top_kernel(const T *logits, TopParams p,
+                                                                                         int32_t *later) {
+  constexpr int THR = 64 * W;
+  __shared__ RowLds<W> lds;
+  __shared__ Softmax waves[W];
   const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 63, V = p.vocab;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, V = p.vocab, turns = turns_of<T>(V);
   const T *z = logits + row * p.ld_logits;
-  HeldRow<T, K> held(z, V);
-  float mine = -__builtin_inff();
-  held.vectors([&](int, const float (&x)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) mine = maximum(mine, x[i]);
-  });
-  const float top = block_maximum<THR>(mine, wave_top);
-  if (!(__builtin_fabsf(top) < __builtin_inff()) || p.k > THR) {
-    RowSource<T, THR> src = {z, V};
-    top_of_all<T, THR>(src, p, row, lds);
-    return;
-  }
-  // that many threads' largest logits are not below their k-th; no border: fewer threads have any
-  ThreadSource threads = {mine};
-  const u64 bound = find_border<THR, 2>(threads, (u64)down_key(top) << 32, kLastKey, [](float) { return (u64)1; },
-                                        [&](u64) { return (u64)p.k; }, lds.select);
-  const float least = bound == kLastKey ? -__builtin_inff() : logit_of((unsigned)(bound >> 32));
-  int n = 0;
-  float sum = 0.f;
-  const float ref = ref_of(least);
-  held.vectors([&](int at, const float (&x)[N]) {
-    float y[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = x[i];
-    if (append(lists[tid >> 6], n, at, x, least, V)) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = x[i] < least ? x[i] : -__builtin_inff();
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = pow2(y[i], p.k2, ref);
-#pragma unroll
-    for (int d = 1; d < N; d *= 2)
-#pragma unroll
-      for (int i = 0; i < N; i += 2 * d) y[i] += y[i + d];
-    sum += y[0];
-  });
-  if (lane == 0) counts[tid >> 6] = n;
-  const float others = block_softmax<W>(sum > 0.f ? least : -__builtin_inff(), sum, p.k2, lds.waves).sum;
-  bool fits = true;
-#pragma unroll
-  for (int w = 0; w < W; ++w) fits = fits && counts[w] <= kListMost;
+  const int t0 = stretch_turn(turns, w, W), t1 = stretch_turn(turns, w + 1, W);
+  Turn<T> now;
+  now.load(z, t0 < t1 ? t0 : turns, V);
+  const int quota = p.k < kQuota ? p.k : kQuota;
+  const Shares share = shares_of<W>(p.k);
+  const Wants want = {quota, raise_at(quota), p.k1, p.temp, 0., 0., false};
+  float top, bound;
+  first_bounds<T, W>(now, share, lds, top, bound);
+  const Stretch mine = sweep<T, true, (W >= 16)>(now, z, V, t0, t1, want, false, bound, bound, lds.list[w], nullptr,
+                                                 t1 - t0 > 1 && share.ranks <= W ? share.quota : 0);
+  leave_stretch<W>(mine, lds);
+  const Together row_of = together(lds);
+  // (the others' sums, relative to the largest of their references)
+  const float ref = lane < W ? lds.out[lane].ref : -__builtin_inff(), max = wave_max(row_of.sum > 0. ? ref : -__builtin_inff());
+  const double sum = wave_sum(row_of.sum > 0. ? row_of.sum * pow2_exact(((double)ref - max) * p.k1) : 0.);
   // (where the others are so far below that their powers lose bits, they are taken from their own largest)
-  if (!fits || !(others >= 0x1p-60f || least == -__builtin_inff())) {
-    __syncthreads();
-    RowSource<T, THR> src = {z, V};
-    top_of_all<T, THR>(src, p, row, lds);
-    return;
+  bool fits = row_of.fits && __builtin_fabsf(row_of.top) < __builtin_inff() && row_of.listed >= p.k &&
+              (row_of.listed == V || sum >= 0x1p-60);
+  if (fits) {
+    bound = share.ranks <= W ? nth_bound<W>(lds.last_bound, share.ranks) : -__FLT_MAX__;
+    // (what is below the bound is one of the others)
+    float m = sum > 0. ? max : -__builtin_inff();
+    const int own = lds.out[w].n;
+    const u64 *list = lds.list[w];
+    for (int j = lane; j < own; j += 64) {
+      const float x = logit_of<T>(list[j]);
+      if (x < bound) m = __builtin_fmaxf(m, x);
+    }
+    float rest = 0.f;   // of those, relative to m (they are before one wave's list is shortened)
+    {
+      const float to = ref_of(m);
+      for (int j = lane; j < own; j += 64) {
+        const float x = logit_of<T>(list[j]);
+        if (x < bound) rest += pow2(x, p.k2, to);
+      }
+      if (threadIdx.x == 0 && sum > 0.) rest += (float)sum * pow2(max, p.k2, to);
+    }
+    wave_sync();
+    const int n = join_lists<T>(lds, bound);
+    u64 *keys = lds.joined();
+    fits = n <= RowLds<W>::kJoined && n >= p.k;
+    if (fits && p.k > kQuota) {
+      // (the bound of a stretch followed its kQuota-th largest: the k largest are in the lists if that many are not
+      // below the largest bound)
+      const float most = nth_bound<W>(lds.bound, 1);
+      int c = 0;
+      for (int j = 0; j < n; j += 64)
+        c += __builtin_popcountll(__ballot(j + lane < n && logit_of<T>(keys[j + lane < n ? j + lane : 0]) >= most));
+      fits = c >= p.k;
+    }
+    if (fits) {
+      const auto other = [&](u64 r) {
+        const float x = logit_of<T>(r), to = __builtin_fmaxf(m, x);
+        rest = (rest > 0.f ? rest * pow2(m, p.k2, ref_of(to)) : 0.f) + pow2(x, p.k2, ref_of(to));
+        m = to;
+      };
+      if (n <= RowLds<W>::kRanked) {
+        for (int j = threadIdx.x; j < n; j += THR) {
+          const u64 r = keys[j];
+          const int rank = rank_among(keys, n, r);
+          if (rank < p.k) write_entry<T>(r, rank, p, row);
+          else other(r);
+        }
+      } else {
+        const int size = sort_size(n);
+        for (int i = n + threadIdx.x; i < size; i += THR) keys[i] = ~(u64)0;
+        __syncthreads();
+        sort_keys<THR>(keys, size);
+        for (int j = threadIdx.x; j < n; j += THR) {
+          if (j < p.k) write_entry<T>(keys[j], j, p, row);
+          else other(keys[j]);
+        }
+      }
+      write_rest<THR>(m, rest, p, row, waves);
+    }
   }
-  ListSource src = {lists[tid >> 6], n};
-  const u64 border = find_border<THR>(src, (u64)down_key(top) << 32, ~(u64)0, [](float) { return (u64)1; },
-                                      [&](u64) { return (u64)p.k; }, lds.select);
-  write_top<T, THR>(src, border, p, row, lds);
-  float m = sum > 0.f ? least : -__builtin_inff();
-  src.each([&](int index, float x) {
-    if (rank_key(x, index) > border) m = __builtin_fmaxf(m, x);
-  });
-  const float to = ref_of(m);
-  if (sum > 0.f) sum *= pow2(least, p.k2, to);
-  src.each([&](int index, float x) {
-    if (rank_key(x, index) > border) sum += pow2(x, p.k2, to);
-  });
-  write_rest<THR>(m, sum, p, row, lds);
+  if (threadIdx.x == 0) gmem(later)[row] = !fits;
 }
 
-template <class T, int THR>
-__global__ __launch_bounds__(THR) void top_long_kernel(const T *logits, TopParams p) {
-  __shared__ TopLds<THR> lds;
-  RowSource<T, THR> src = {logits + blockIdx.x * p.ld_logits, p.vocab};
-  top_of_all<T, THR>(src, p, blockIdx.x, lds);
+template <class T>
+__global__ __launch_bounds__(kLaterThreads) void top_later_kernel(const T *logits, TopParams p, const int32_t *later,
+                                                                  int32_t rows) {
+  constexpr int THR = kLaterThreads, N = Vec<T>::N;
+  __shared__ BlockLds<THR> block;
+  __shared__ u64 keys[HIMUON_TOP_MOST];
+  __shared__ Softmax waves[THR / 64];
+  __shared__ int found;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    if (gmem(later)[row] == 0) continue;
+    const T *z = logits + row * p.ld_logits;
+    const int V = p.vocab, tid = threadIdx.x;
+    u64 border = ~(u64)0;
+    if (tid == 0) found = 0;
+    if (p.k < V)
+      border = find_border_in_row<T, THR, true>(z, V, 0, last_key<T>(-__builtin_inff()), [](float) { return (u64)1; },
+                                                [&](u64) { return (u64)p.k; }, block);
+    __syncthreads();
+    float m = -__builtin_inff(), sum = 0.f;
+    for (int at = tid; at * N < V; at += THR) {
+      float x[N];
+      Vec<T>::unpack(row_vector(z, at, V), x);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const u64 r = rank_key<T>(x[e], at * N + e);
+        if (at * N + e >= V) continue;
+        if (r <= border) keys[atomicAdd(&found, 1)] = r;
+        else m = __builtin_fmaxf(m, x[e]);
+      }
+    }
+    const int size = sort_size(p.k);
+    for (int i = p.k + tid; i < size; i += THR) keys[i] = ~(u64)0;
+    __syncthreads();
+    sort_keys<THR>(keys, size);
+    for (int i = tid; i < p.k; i += THR) write_entry<T>(keys[i], i, p, row);
+    const float ref = ref_of(m);
+    for (int at = tid; at * N < V; at += THR) {
+      float x[N];
+      Vec<T>::unpack(row_vector(z, at, V), x);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (at * N + e < V && rank_key<T>(x[e], at * N + e) > border) sum += pow2(x[e], p.k2, ref);
+    }
+    write_rest<THR>(m, sum, p, row, waves);
+    __syncthreads();
+  }
 }
 
 constexpr int64_t kLaunchRows = (int64_t)1 << 21;   // a grid holds fewer than 2^32 threads
 
-// A row's vectors by the block that holds them: f(kernel's threads, vectors a thread; 0: too long).
+// Waves for a row: enough of them to fill the chip (256 CUs with 16 each), and as many as its
+// stretches' lengths ask for.
+constexpr int kFillWaves = 4096;
+int waves_of(int64_t rows, int64_t vecs, int least) {
+  const int64_t turns = (vecs + kTurn - 1) / kTurn;
+  int W = 1;
+  while (W < 16 && (W < least || turns > (int64_t)W * kTurns || (rows * W < kFillWaves && W < turns))) W *= 2;
+  return W;
+}
 template <class F>
-void with_shape(int64_t vecs, F f) {
-  if (vecs <= 256) f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
-  else if (vecs <= 256 * 4) f(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
-  else if (vecs <= 512 * 8) f(std::integral_constant<int, 512>(), std::integral_constant<int, 8>());
-  else if (vecs <= 1024 * 8) f(std::integral_constant<int, 1024>(), std::integral_constant<int, 8>());
-  else if (vecs <= 1024 * 16) f(std::integral_constant<int, 1024>(), std::integral_constant<int, 16>());
-  else f(std::integral_constant<int, 1024>(), std::integral_constant<int, 0>());
+void with_waves(int W, F f) {
+  if (W == 1) f(std::integral_constant<int, 1>());
+  else if (W == 2) f(std::integral_constant<int, 2>());
+  else if (W == 4) f(std::integral_constant<int, 4>());
+  else if (W == 8) f(std::integral_constant<int, 8>());
+  else f(std::integral_constant<int, 16>());
 }
 
 template <class T>
-hipError_t launch_sample_t(const himuon_sampling &c, SampleParams p, hipStream_t stream) {
+hipError_t launch_sample_t(const himuon_sampling &c, SampleParams p, int32_t *later, hipStream_t stream) {
   const T *z = reinterpret_cast<const T *>(c.logits);
-  const int64_t vecs = (c.vocab + Vec<T>::N - 1) / Vec<T>::N;
+  // (a stretch's list holds its kQuota largest for certain; settings of each row are not known here)
+  int least = c.row_top_k ? 4 : 1;
+  while (!c.row_top_k && least < 8 && kQuota * least < c.top_k) least *= 2;
+  const int W = waves_of(c.rows, (c.vocab + Vec<T>::N - 1) / Vec<T>::N, least);
   for (int64_t r = 0; r < c.rows; r += kLaunchRows) {
     const unsigned rows = (unsigned)(c.rows - r < kLaunchRows ? c.rows - r : kLaunchRows);
-    with_shape(vecs, [&](auto threads, auto held) {
-      constexpr int THR = decltype(threads)::value, K = decltype(held)::value;
-      const T *at = z + r * c.ld_logits;
-      if constexpr (K > 0) {
-        hipLaunchKernelGGL((sample_kernel<T, THR, K>), dim3(rows), dim3(THR), 0, stream, at, p);
-      } else {
-        const size_t lds = (vecs + THR - 1) / THR * (THR / 64) * sizeof(double);
-        hipLaunchKernelGGL((sample_long_kernel<T, THR>), dim3(rows), dim3(THR), lds, stream, at, p);
-      }
+    with_waves(W, [&](auto waves) {
+      constexpr int kWaves = decltype(waves)::value;
+      hipLaunchKernelGGL((sample_kernel<T, kWaves>), dim3(rows), dim3(64 * kWaves), 0, stream, z + r * c.ld_logits, p, later);
     });
-    const hipError_t e = hipGetLastError();
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((sample_later_kernel<T>), dim3(rows < kLaterBlocks ? rows : kLaterBlocks), dim3(kLaterThreads), 0,
+                       stream, z + r * c.ld_logits, p, later, (int32_t)rows);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    later += rows;
     p.uniform += rows;
     if (p.temperature) p.temperature += rows;
     if (p.top_k) p.top_k += rows;
@@ -813,19 +1403,24 @@ hipError_t launch_sample_t(const himuon_sampling &c, SampleParams p, hipStream_t
 }
 
 template <class T>
-hipError_t launch_top_t(const himuon_top &c, TopParams p, hipStream_t stream) {
+hipError_t launch_top_t(const himuon_top &c, TopParams p, int32_t *later, hipStream_t stream) {
   const T *z = reinterpret_cast<const T *>(c.logits);
-  const int64_t vecs = (c.vocab + Vec<T>::N - 1) / Vec<T>::N;
+  int least = 1;
+  while (top_most(least) < c.k) least *= 2;
+  const int W = waves_of(c.rows, (c.vocab + Vec<T>::N - 1) / Vec<T>::N, least);
   for (int64_t r = 0; r < c.rows; r += kLaunchRows) {
     const unsigned rows = (unsigned)(c.rows - r < kLaunchRows ? c.rows - r : kLaunchRows);
-    with_shape(vecs, [&](auto threads, auto held) {
-      constexpr int THR = decltype(threads)::value, K = decltype(held)::value;
-      const T *at = z + r * c.ld_logits;
-      if constexpr (K > 0) hipLaunchKernelGGL((top_kernel<T, THR, K>), dim3(rows), dim3(THR), 0, stream, at, p);
-      else hipLaunchKernelGGL((top_long_kernel<T, THR>), dim3(rows), dim3(THR), 0, stream, at, p);
+    with_waves(W, [&](auto waves) {
+      constexpr int kWaves = decltype(waves)::value;
+      hipLaunchKernelGGL((top_kernel<T, kWaves>), dim3(rows), dim3(64 * kWaves), 0, stream, z + r * c.ld_logits, p, later);
     });
-    const hipError_t e = hipGetLastError();
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((top_later_kernel<T>), dim3(rows < kLaterBlocks ? rows : kLaterBlocks), dim3(kLaterThreads), 0,
+                       stream, z + r * c.ld_logits, p, later, (int32_t)rows);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    later += rows;
     p.value = reinterpret_cast<T *>(p.value) + rows * p.ld_top;
     p.index += rows * p.ld_top;
     p.rest += rows;
@@ -835,11 +1430,13 @@ hipError_t launch_top_t(const himuon_top &c, TopParams p, hipStream_t stream) {
 
 }  // namespace
 
-size_t sample_workspace(const himuon_sampling &) { return 0; }
-size_t top_workspace(const himuon_top &) { return 0; }
+// A mark for each row that the first launch may leave to the second.
+size_t sample_workspace(const himuon_sampling &c) { return (size_t)(c.rows + 1) / 2 * 8; }
+size_t top_workspace(const himuon_top &c) { return (size_t)(c.rows + 1) / 2 * 8; }
 
-hipError_t launch_sample(const himuon_sampling &c, void *, hipStream_t stream) {
+hipError_t launch_sample(const himuon_sampling &c, void *workspace, hipStream_t stream) {
   SampleParams p{};
+  int32_t *later = reinterpret_cast<int32_t *>(workspace);
   p.uniform = c.uniform;
   p.temperature = c.row_temperature;
   p.top_k = c.row_top_k;
@@ -856,11 +1453,12 @@ hipError_t launch_sample(const himuon_sampling &c, void *, hipStream_t stream) {
   p.T = c.temperature;
   p.p = c.top_p;
   p.m = c.min_p;
-  return c.dtype == HIMUON_BF16 ? launch_sample_t<__bf16>(c, p, stream) : launch_sample_t<float>(c, p, stream);
+  return c.dtype == HIMUON_BF16 ? launch_sample_t<__bf16>(c, p, later, stream) : launch_sample_t<float>(c, p, later, stream);
 }
 
-hipError_t launch_top(const himuon_top &c, void *, hipStream_t stream) {
+hipError_t launch_top(const himuon_top &c, void *workspace, hipStream_t stream) {
   TopParams p{};
+  int32_t *later = reinterpret_cast<int32_t *>(workspace);
   p.value = c.value;
   p.index = c.index;
   p.rest = c.rest;
@@ -870,7 +1468,9 @@ hipError_t launch_top(const himuon_top &c, void *, hipStream_t stream) {
   p.k = c.k;
   p.k2 = (float)(kLog2e / c.temperature);
   p.inv_temp = (float)(1. / c.temperature);
-  return c.dtype == HIMUON_BF16 ? launch_top_t<__bf16>(c, p, stream) : launch_top_t<float>(c, p, stream);
+  p.k1 = kLog2e / c.temperature;
+  p.temp = c.temperature;
+  return c.dtype == HIMUON_BF16 ? launch_top_t<__bf16>(c, p, later, stream) : launch_top_t<float>(c, p, later, stream);
 }
 
 }  // namespace himuon

@@ -33,15 +33,20 @@ __device__ __forceinline__ double last_lane(double x) {
   return __builtin_bit_cast(double, (unsigned long long)last_lane((unsigned)(v >> 32)) << 32 | last_lane((unsigned)v));
 }
 
+// each lane's and all lanes' before it
 template <class T, class OP>
-__device__ __forceinline__ T wave_reduce(T x, T none, OP op) {
+__device__ __forceinline__ T wave_scan(T x, T none, OP op) {
   x = op(x, dpp<0x111, 0xf>(none, x));
   x = op(x, dpp<0x112, 0xf>(none, x));
   x = op(x, dpp<0x114, 0xf>(none, x));
   x = op(x, dpp<0x118, 0xf>(none, x));
   x = op(x, dpp<0x142, 0xa>(none, x));
   x = op(x, dpp<0x143, 0xc>(none, x));
-  return last_lane(x);
+  return x;
+}
+template <class T, class OP>
+__device__ __forceinline__ T wave_reduce(T x, T none, OP op) {
+  return last_lane(wave_scan(x, none, op));
 }
 __device__ __forceinline__ unsigned wave_max(unsigned x) {
   return wave_reduce(x, 0u, [](unsigned a, unsigned b) { return max(a, b); });
