@@ -185,84 +185,6 @@ __device__ __forceinline__ u64 find_border(const u64 *list, int n, u64 first, u6
   }
 }
 
-// The same among the elements of a row of V in memory, by the THR threads of a block.  sum (top level alone):
-// what it adds up over all elements.
-template <int THR>
-struct BlockLds {
-  Histogram<4 * THR> h;
-  u64 wave[THR / 64];
-  int bin;
-  u64 before;
-  unsigned count;
-};
-template <class T, int THR, bool COUNT, class WEIGHT, class TARGET>
-__device__ __forceinline__ u64 find_border_in_row(const T *z, int V, u64 first, u64 last, WEIGHT weight, TARGET target_of,
-                                                  BlockLds<THR> &lds) {
-  constexpr int N = Vec<T>::N, B = 4, kDigits = 31 - __builtin_clz(B * THR);
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  Range r = {first, last, 0};
-  u64 target = 0;
-  for (bool top = true;; top = false) {
-    const int shift = bin_shift(r, kDigits);
-    for (int i = tid; i < B * THR; i += THR) {
-      lds.h.mass[i] = 0;
-      lds.h.count[i] = 0;
-    }
-    if (tid == 0) lds.bin = -1;
-    __syncthreads();
-    const float most = logit_of<T>(r.first), least = logit_of<T>(r.last);   // (a NaN is above everything)
-    for (int at = tid; at * N < V; at += THR) {
-      float x[N];
-      Vec<T>::unpack(row_vector(z, at, V), x);
-      bool in = false;
-#pragma unroll
-      for (int e = 0; e < N; ++e) in = in || !(x[e] < least || x[e] > most);
-      if (!__any(in)) continue;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const u64 key = rank_key<T>(x[e], at * N + e);
-        if (key < r.first || key > r.last || at * N + e >= V) continue;
-        const int bin = (int)((key - r.first) >> shift);
-        atomicAdd(&lds.h.count[bin], 1u);
-        if (!COUNT) atomicAdd(&lds.h.mass[bin], weight(x[e]));
-      }
-    }
-    __syncthreads();
-    u64 have[B], mine = 0;
-#pragma unroll
-    for (int i = 0; i < B; ++i) mine += have[i] = COUNT ? lds.h.count[tid * B + i] : lds.h.mass[tid * B + i];
-    u64 upto = wave_scan(mine);
-    if (lane == 63) lds.wave[w] = upto;
-    __syncthreads();
-    u64 total = 0;
-    for (int i = 0; i < THR / 64; ++i) {
-      if (i < w) upto += lds.wave[i];
-      total += lds.wave[i];
-    }
-    if (top) target = target_of(total);
-    u64 at = r.before + upto - mine;
-    if (at < target && at + mine >= target) {
-      int bin = 0;
-#pragma unroll
-      for (int i = 0; i < B - 1; ++i)
-        if (bin == i && at + have[i] < target) {
-          at += have[i];
-          bin = i + 1;
-        }
-      lds.bin = tid * B + bin;
-      lds.before = at;
-      lds.count = lds.h.count[tid * B + bin];
-    }
-    __syncthreads();
-    const int bin = lds.bin;
-    const u64 before = lds.before;
-    const unsigned count = lds.count;
-    __syncthreads();
-    if (bin < 0) return last;
-    if (narrow(r, bin, before, count, shift)) return r.last;
-  }
-}
-
 struct SampleParams {
   const float *uniform;
   const float *temperature, *top_p, *min_p;   // nullptr: all rows alike, as below
@@ -424,7 +346,7 @@ struct Stretch {
   double shift;    // Powers' of its sums (0: no logit)
   double sum;      // of the powers of what is not in the list
   double listed;   // and of what is
-  float bound;     // the largest logit that was left out of the list is below
+  float raised;    // what quota raised the bound to (-FLT_MAX: it did not)
   float last_bound;   // sweep()
   int n;           // keys in the list; kListMost + 1: they did not fit
 };
@@ -584,6 +506,104 @@ __device__ __forceinline__ float turn_maximum(Turn<T> &turn, float (&most)[kTurn
   }
   return top;
 }
+// f(index of its first vector, its vectors) for the 64 vectors at a time of a row in memory that a wave has of THR threads'.
+template <class T, int THR, class F>
+__device__ __forceinline__ void each_vector(const T *z, int V, F f) {
+  const int lane = threadIdx.x & 63, turns = ((V + Vec<T>::N - 1) / Vec<T>::N + kTurn - 1) / kTurn;
+  for (int t = threadIdx.x >> 6; t < turns; t += THR / 64) {
+    Turn<T> now;
+    now.load(z, t, V);
+#pragma unroll 1
+    for (int i = 0; i < kTurnVecs; ++i) {
+      float x[Vec<T>::N];
+      Vec<T>::unpack(now.pick(i), x);
+      f(t * kTurn + i * 64 + lane, x);
+    }
+  }
+}
+
+// find_border() among the elements of a row of V in memory, by the THR threads of a block.  A bin that is a
+// single logit's (in bf16 mostly all are) has its elements counted, and its mass comes from their number.
+template <int THR>
+struct BlockLds {
+  Histogram<4 * THR> h;
+  u64 wave[THR / 64];
+  int bin;
+  u64 before;
+  unsigned count;
+};
+template <class T, int THR, bool COUNT, class WEIGHT, class TARGET>
+__device__ __forceinline__ u64 find_border_in_row(const T *z, int V, u64 first, u64 last, WEIGHT weight, TARGET target_of,
+                                                  BlockLds<THR> &lds) {
+  constexpr int N = Vec<T>::N, B = 4, kDigits = 31 - __builtin_clz(B * THR);
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  Range r = {first, last, 0};
+  u64 target = 0;
+  for (bool top = true;; top = false) {
+    const int shift = bin_shift(r, kDigits);
+    const bool single = COUNT || (sizeof(T) == 2 && shift <= 20);
+    for (int i = tid; i < B * THR; i += THR) {
+      lds.h.mass[i] = 0;
+      lds.h.count[i] = 0;
+    }
+    if (tid == 0) lds.bin = -1;
+    __syncthreads();
+    const float most = logit_of<T>(r.first), least = logit_of<T>(r.last);   // (a NaN is above everything)
+    each_vector<T, THR>(z, V, [&](int at, float (&x)[N]) {
+      bool in = false;
+#pragma unroll
+      for (int e = 0; e < N; ++e) in = in || !(x[e] < least || x[e] > most);
+      if (!__any(in)) return;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const u64 key = rank_key<T>(x[e], at * N + e);
+        if (key < r.first || key > r.last || at * N + e >= V) continue;
+        const int bin = (int)((key - r.first) >> shift);
+        atomicAdd(&lds.h.count[bin], 1u);
+        if (!single) atomicAdd(&lds.h.mass[bin], weight(x[e]));
+      }
+    });
+    __syncthreads();
+    u64 have[B], mine = 0;
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int bin = tid * B + i;
+      const unsigned n = lds.h.count[bin];
+      have[i] = COUNT ? n : !single ? lds.h.mass[bin] : n > 0 ? n * weight(logit_of<T>(r.first + ((u64)bin << shift))) : 0;
+      mine += have[i];
+    }
+    u64 upto = wave_scan(mine);
+    if (lane == 63) lds.wave[w] = upto;
+    __syncthreads();
+    u64 total = 0;
+    for (int i = 0; i < THR / 64; ++i) {
+      if (i < w) upto += lds.wave[i];
+      total += lds.wave[i];
+    }
+    if (top) target = target_of(total);
+    u64 at = r.before + upto - mine;
+    if (at < target && at + mine >= target) {
+      int bin = 0;
+#pragma unroll
+      for (int i = 0; i < B - 1; ++i)
+        if (bin == i && at + have[i] < target) {
+          at += have[i];
+          bin = i + 1;
+        }
+      lds.bin = tid * B + bin;
+      lds.before = at;
+      lds.count = lds.h.count[tid * B + bin];
+    }
+    __syncthreads();
+    const int bin = lds.bin;
+    const u64 before = lds.before;
+    const unsigned count = lds.count;
+    __syncthreads();
+    if (bin < 0) return last;
+    if (narrow(r, bin, before, count, shift)) return r.last;
+  }
+}
+
 // A wave goes through turns [t0, t1) of a row, the first of which is in `now`, with a first logit that
 // powers are relative to and a first bound (which hold for the row).  exact: powers in fp64; else in fp32.
 // They are relative to a logit that follows the largest, and if CEIL (fp32 alone) to one that follows the
@@ -598,7 +618,8 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
   const float k32 = (float)want.k, far = (float)(kFar / want.k);
   // (the second part of k, above 0: the product of -inf with it is -inf, too)
   const float hi = CEIL ? k32 : __builtin_bit_cast(float, __builtin_bit_cast(unsigned, k32) - 1), lo = (float)(want.k - hi);
-  Stretch out = {-__builtin_inff(), -__builtin_inff(), 0., 0., 0., want.none ? __builtin_inff() : bound, -__FLT_MAX__, 0};
+  Stretch out = {-__builtin_inff(), -__builtin_inff(), 0., 0., 0., -__FLT_MAX__, -__FLT_MAX__, 0};
+  if (want.none) bound = __builtin_inff();
   float largest = -__builtin_inff();
   bool stop = false;
   double sum = 0, part = 0;
@@ -622,7 +643,7 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
   const auto logit_at = [&](int j) { return logit_of<T>(list[j]); };
   // An element is looked at more closely from here on: it belongs to the list, or the powers' reference has to
   // move (so that none is past 2^100).
-  const auto threshold = [&] { return CEIL ? out.bound : __builtin_fminf(out.bound, ref + far); };
+  const auto threshold = [&] { return CEIL ? bound : __builtin_fminf(bound, ref + far); };
   float close = threshold();
   const auto vector = [&](int at, float (&x)[N]) {   // at: the index of its first element
     float most = x[0];
@@ -635,14 +656,14 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
         stop = stop || !(top < __builtin_inff());   // NaN or +inf: nothing of the row is needed
         if (!CEIL && !stop && top > -__builtin_inff()) {
           refer_to(top);
-          out.bound = __builtin_fmaxf(out.bound, bound_of(want, top, top, 1., V));
+          bound = __builtin_fmaxf(bound, bound_of(want, top, top, 1., V));
           close = threshold();
         }
       }
-      if (__any(most >= out.bound)) {
-        append<T, !CEIL>(list, out.n, at, x, out.bound, V);
+      if (__any(most >= bound)) {
+        append<T, !CEIL>(list, out.n, at, x, bound, V);
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = x[j] < out.bound ? x[j] : -__builtin_inff();
+        for (int j = 0; j < N; ++j) x[j] = x[j] < bound ? x[j] : -__builtin_inff();
       }
     }
     if (!CEIL && exact) {
@@ -670,15 +691,13 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
     const bool more = t + 1 < t1;
     const int first = (t * kTurn + lane) * N;
     if constexpr (SMALL) {
-      Turn<T> next;
-      if (more) next.load(z, t + 1, V);
 #pragma unroll 1
       for (int i = 0; i < kTurnVecs; ++i) {
         float x[N];
         Vec<T>::unpack(now.pick(i), x);
         vector(first + i * 64 * N, x);
       }
-      if (more) now = next;
+      if (more) now.load(z, t + 1, V);
     } else {
       const bool whole = (t + 2) * kTurn * N <= V;   // (the next turn)
 #pragma unroll
@@ -706,39 +725,43 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
     }
     sum += part;
     part = 0;
-    const bool raise = out.n > want.most, last = !more && last_quota > 0 && out.n >= last_quota;
-    if (!raise && !last) continue;
-    wave_sync();
-    float b = -__FLT_MAX__;
-    if (want.quota > 0) {
-      b = nth_of_list<T>(list, out.n, raise ? want.quota : last_quota);
-    } else {
-      double all = sum;
-      for (int j = lane; j < out.n; j += 64) all += e.of(logit_at(j));
-      b = bound_of(want, wave_maximum(largest), ref, wave_sum(all) / e.of(ref), V);
-    }
-    b = __builtin_fmaxf(out.bound, b);
-    if (!more) out.last_bound = b;
-    if (!raise) continue;
-    // the bound rises, and what is below it is dropped
-    out.bound = b;
-    if (CEIL && b - ref > far) refer_to(b);
-    close = threshold();
-    int n = 0;
-    for (int j = 0; j < out.n; j += 64) {
-      const u64 r = j + lane < out.n ? list[j + lane] : 0;
-      const float x = logit_of<T>(r);
-      const bool in = j + lane < out.n, stays = in && x >= out.bound;
-      const u64 stay = __ballot(stays);
-      if (stays) list[n + lanes_before(stay)] = r;
-      if (in && !stays) sum += e.of(x);
-      n += __builtin_popcountll(stay);
-    }
-    out.n = n;
-    wave_sync();
-    if (n > want.most) {   // (more of them than a list is for)
-      out.n = kListMost + 1;
-      return out;
+    while (out.n > want.most || (!more && last_quota > 0 && out.n >= last_quota)) {
+      const bool raise = out.n > want.most;
+      wave_sync();
+      float b;
+      if (want.quota > 0) {
+        b = nth_of_list<T>(list, out.n, raise ? want.quota : last_quota);
+      } else {
+        double all = sum;
+        for (int j = lane; j < out.n; j += 64) all += e.of(logit_at(j));
+        b = bound_of(want, wave_maximum(largest), ref, wave_sum(all) / e.of(ref), V);
+      }
+      b = __builtin_fmaxf(bound, b);
+      if (!raise) {
+        out.last_bound = b;
+        break;
+      }
+      // the bound rises, and what is below it is dropped
+      bound = b;
+      if (want.quota > 0) out.raised = b;
+      if (CEIL && b - ref > far) refer_to(b);
+      close = threshold();
+      int n = 0;
+      for (int j = 0; j < out.n; j += 64) {
+        const u64 r = j + lane < out.n ? list[j + lane] : 0;
+        const float x = logit_of<T>(r);
+        const bool in = j + lane < out.n, stays = in && x >= bound;
+        const u64 stay = __ballot(stays);
+        if (stays) list[n + lanes_before(stay)] = r;
+        if (in && !stays) sum += e.of(x);
+        n += __builtin_popcountll(stay);
+      }
+      out.n = n;
+      wave_sync();
+      if (n > want.most) {   // (more of them than a list is for)
+        out.n = kListMost + 1;
+        return out;
+      }
     }
   }
   out.top = wave_maximum(largest);
@@ -768,42 +791,43 @@ __device__ __forceinline__ int turns_of(int V) {
   return ((V + Vec<T>::N - 1) / Vec<T>::N + kTurn - 1) / kTurn;
 }
 
-// The token of a row that is read from memory for every pass over it, by the THR threads of a block.  chunk: LDS,
-// one for each 64 vectors of the row (it may be in the histogram's place).
+// A row's largest logit, by the THR threads of a block, and the sum of all powers, relative to it.  top: NaN or +inf
+// or all of them -inf: no sum.
 template <class T, int THR>
-__device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s, int64_t row, const SampleParams &p,
-                                                   BlockLds<THR> &lds, double *wave, double *chunk) {
+__device__ __forceinline__ double measure_row(const T *z, const Settings &s, const SampleParams &p, float &top, Powers &e,
+                                              double *wave) {
   constexpr int N = Vec<T>::N, W = THR / 64;
-  const int tid = threadIdx.x, lane = tid & 63, V = p.vocab, vecs = (V + N - 1) / N;
-  float top = -__builtin_inff();
-  for (int at = tid; at < vecs; at += THR) {
-    float x[N];
-    Vec<T>::unpack(row_vector(z, at, V), x);
+  const int lane = threadIdx.x & 63;
+  top = -__builtin_inff();
+  each_vector<T, THR>(z, p.vocab, [&](int, float (&x)[N]) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) top = maximum(top, x[e]);
-  }
+    for (int i = 0; i < N; ++i) top = maximum(top, x[i]);
+  });
   top = wave_maximum(top);
   __syncthreads();
-  if (lane == 0) wave[tid >> 6] = top;
+  if (lane == 0) wave[threadIdx.x >> 6] = top;
   __syncthreads();
   top = wave_maximum((float)wave[lane % W]);
-  __syncthreads();
-  if (!(__builtin_fabsf(top) < __builtin_inff())) {
-    if (tid == 0) write_bad(p, row);
-    return;
-  }
-  Powers e;
+  if (!(__builtin_fabsf(top) < __builtin_inff())) return 0.;
   e.refer_to(top, s.k);
-  e.unit = __builtin_amdgcn_ldexp(1., p.mass_bits);
   double all = 0;
-  for (int at = tid; at < vecs; at += THR) {
-    float x[N];
-    Vec<T>::unpack(row_vector(z, at, V), x);
+  each_vector<T, THR>(z, p.vocab, [&](int, float (&x)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) all += e.of(x[i]);
-  }
-  all = block_sum_in_order<THR>(all, wave);
-  u64 border = last_key<T>(-__FLT_MAX__);
+  });
+  return block_sum_in_order<THR>(all, wave);
+}
+
+// The token of a row that is read from memory for every pass over it, by the THR threads of a block.  e: relative to
+// its largest logit top; all: the sum of its powers; bound: what is below it is not kept.  chunk: LDS, one for each
+// 64 vectors of the row (it may be in the histogram's place).
+template <class T, int THR>
+__device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s, int64_t row, const SampleParams &p,
+                                                   const Powers &e, float top, double all, float bound, BlockLds<THR> &lds,
+                                                   double *chunk) {
+  constexpr int N = Vec<T>::N;
+  const int tid = threadIdx.x, lane = tid & 63, V = p.vocab, vecs = (V + N - 1) / N;
+  u64 border = last_key<T>(bound);
   if (s.by_k)
     border = find_border_in_row<T, THR, true>(z, V, first_key<T>(top), border, [](float) { return (u64)1; },
                                               [&](u64) { return (u64)s.top_k; }, lds);
@@ -812,8 +836,7 @@ __device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s
                                                [&](u64 total) { return target_of_p(s, e, total, all); }, lds);
   const Kept<T> kept = {border, __builtin_fmax(s.min_p * e.of(top), kNoPower)};
   const float edge = logit_of<T>(border);   // (of the last token that is kept)
-  const auto weigh = [&](int vec, float (&x)[N]) {
-    Vec<T>::unpack(row_vector(z, vec, V), x);
+  const auto weigh = [&](int vec, const float (&x)[N]) {
     bool any = false;
 #pragma unroll
     for (int i = 0; i < N; ++i) any = any || x[i] >= edge;
@@ -826,11 +849,10 @@ __device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s
   };
   // the draw: a wave's 64 vectors are consecutive, so the chunks are in order
   const int chunks = (vecs + 63) / 64;
-  float x[N];
-  for (int c = tid >> 6; c < chunks; c += W) {
-    const double sum = wave_sum(weigh(c * 64 + lane, x));
-    if (lane == 0) chunk[c] = sum;
-  }
+  each_vector<T, THR>(z, V, [&](int at, float (&x)[N]) {
+    const double sum = wave_sum(weigh(at, x));
+    if (lane == 0 && at < vecs) chunk[at / 64] = sum;
+  });
   __syncthreads();
   if (tid >= 64) return;   // (they wait for the first wave at the next row)
   double total = 0;
@@ -839,6 +861,8 @@ __device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s
   const double target = uniform_of(p, row) * total;
   double before, more, last;
   const int c = find_part(chunks, target, [&](int i) { return chunk[i]; }, before);
+  float x[N];
+  Vec<T>::unpack(row_vector(z, c * 64 + lane, V), x);
   const double own = weigh(c * 64 + lane, x);
   const int v = c * 64 + find_part(64, target - before, [&](int) { return own; }, more);
   const int n = N < V - v * N ? N : V - v * N;
@@ -847,6 +871,10 @@ __device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s
   if (lane == i) write_token(p, row, s, e, v * N + i, mine, top, all, total);
 }
 
+// Whether a block of W waves itself goes through its row again where its lists do not hold what is asked for
+// (others leave it to a second launch).
+constexpr bool again(int W) { return W >= 4; }
+
 template <int W>
 struct RowLds {
   static constexpr int kJoined = W == 1 ? 512 : W < 8 ? 1024 : 2048;   // keys of the joined list
@@ -854,6 +882,8 @@ struct RowLds {
   union {
     u64 list[W][kListMost];
     double turns[W][kTurns];
+    std::conditional_t<again(W), BlockLds<64 * W>, u64> block;
+    double chunk[W][kListMost];
   };
   u64 joined_list[W == 1 ? 1 : kJoined];
   union {
@@ -861,8 +891,9 @@ struct RowLds {
     u64 sorted[kRanked];
   };
   Stretch out[W];
-  float first_top[W], first_bound[W], bound[W], last_bound[W];
+  Settings settings;
   double part[W];
+  float first_top[W], first_bound[W], raised[W], last_bound[W];
   int count[W];
   __device__ __forceinline__ u64 *joined() { return W == 1 ? &list[0][0] : joined_list; }
 };
@@ -923,7 +954,7 @@ __device__ __forceinline__ void leave_stretch(const Stretch &mine, RowLds<W> &ld
   const int w = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0) {
     lds.out[w] = mine;
-    lds.bound[w] = mine.bound;
+    lds.raised[w] = mine.raised;
     lds.last_bound[w] = mine.last_bound;
   }
   __syncthreads();
@@ -984,6 +1015,14 @@ __device__ __forceinline__ int join_lists(RowLds<W> &lds, float bound) {
   if constexpr (W == 1) return at <= RowLds<W>::kJoined ? at : RowLds<W>::kJoined + 1;
   return total;
 }
+// How many of n keys have a logit of `least` or more (one wave).
+template <class T>
+__device__ __forceinline__ int count_from(const u64 *keys, int n, float least) {
+  int c = 0;
+  for (int j = threadIdx.x & 63; j - (int)(threadIdx.x & 63) < n; j += 64)
+    c += __builtin_popcountll(__ballot(j < n && logit_of<T>(keys[j < n ? j : 0]) >= least));
+  return c;
+}
 // How many of n keys are below r.
 __device__ __forceinline__ int rank_among(const u64 *keys, int n, u64 r) {
   int rank = 0, i = 0;
@@ -1011,8 +1050,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
   const int t0 = stretch_turn(turns, w, W), t1 = stretch_turn(turns, w + 1, W);
   Turn<T> now;
   now.load(z, t0 < t1 ? t0 : turns, V);
-  const Settings s = settings_of(p, row);
-  if (threadIdx.x == 0) gmem(later)[row] = 0;
+  Settings s = settings_of(p, row);
+  if (!again(W) && threadIdx.x == 0) gmem(later)[row] = 0;
   if (!s.good) {
     if (threadIdx.x == 0) write_bad(p, row);
     return;
@@ -1029,20 +1068,22 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
     return;
   }
   if (top > -__builtin_inff()) bound = __builtin_fmaxf(bound, bound_of(want, top, top, 1., V));
+  if (threadIdx.x == 0) lds.settings = s;   // (for what follows the sweep, which has no registers to spare)
   const Stretch mine = sweep<T, false, (W >= 16)>(now, z, V, t0, t1, want, exact, top, bound, lds.list[w],
                                                   everything ? lds.turns[w] : nullptr,
-                                                  t1 - t0 > 1 && share.ranks <= W ? share.quota : 0);
+                                                  turns > W && share.ranks <= W ? share.quota : 0);
   leave_stretch<W>(mine, lds);
+  s = lds.settings;
   const Together row_of = together(lds);
   top = row_of.top;
-  const bool fits = row_of.fits;
+  bool fits = row_of.fits;
   if (fits && !(__builtin_fabsf(top) < __builtin_inff())) {   // NaN or +inf in the row, nothing but -inf
     if (threadIdx.x == 0) write_bad(p, row);
     return;
   }
   Powers e;
-    e.refer_to(top, s.k);
-    e.unit = __builtin_amdgcn_ldexp(1., p.mass_bits);
+  e.refer_to(top, s.k);
+  e.unit = __builtin_amdgcn_ldexp(1., p.mass_bits);
   // (a stretch's powers to the row's; without logits it has none)
   Powers own = e;
   own.shift = row_of.shift;
@@ -1084,28 +1125,22 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
     if (lane == i) write_token(p, row, s, e, v * N + i, x, top, all, all);
     return;
   }
+  int n = 0;
+  bound = bound_of(want, top, top, all / e.of(top), V);
   if (fits) {
-    bound = -__FLT_MAX__;
-    if (quota > 0 && share.ranks <= W) bound = nth_bound<W>(lds.last_bound, share.ranks);
-    bound = __builtin_fmaxf(bound, bound_of(want, top, top, all / e.of(top), V));
-    const int n = join_lists<T>(lds, bound);
-    if (n > RowLds<W>::kJoined || (w > 0 && n > RowLds<W>::kRanked)) {
-      if (n > RowLds<W>::kJoined && threadIdx.x == 0) gmem(later)[row] = 1;
-      return;
+    if (quota > 0 && share.ranks <= W) bound = __builtin_fmaxf(bound, nth_bound<W>(lds.last_bound, share.ranks));
+    n = join_lists<T>(lds, bound);
+    fits = n <= RowLds<W>::kJoined;
+    // (where a stretch's list followed its kQuota-th largest, the lists hold what is not below what that raised its bound
+    // to: enough where that is not above the bound for all, or where there are top_k of it)
+    if (fits && s.by_k && s.top_k > kQuota) {
+      const float most = nth_bound<W>(lds.raised, 1);
+      fits = most <= bound || count_from<T>(lds.joined(), n, most) >= s.top_k;
     }
+  }
+  if (fits) {
+    if (w > 0 && n > RowLds<W>::kRanked) return;
     const u64 *list = lds.joined();
-    if (s.top_k > kQuota && s.by_k) {
-      // (the bound of a stretch followed its kQuota-th largest: the top_k largest are in the lists if that many
-      // are not below the largest bound)
-      const float most = nth_bound<W>(lds.bound, 1);
-      int c = 0;
-      for (int j = 0; j < n; j += 64)
-        c += __builtin_popcountll(__ballot(j + lane < n && logit_of<T>(list[j + lane < n ? j + lane : 0]) >= most));
-      if (c < s.top_k) {
-        if (threadIdx.x == 0) gmem(later)[row] = 1;
-        return;
-      }
-    }
     u64 border = ~(u64)0;
     if (n <= RowLds<W>::kRanked && (s.by_k || s.by_p)) {
       // the keys in their order, and how many of them the filters keep
@@ -1151,7 +1186,21 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
     if (lane == 0) write_token(p, row, s, e, index_of(list[j]), logit_of<T>(list[j]), top, all, total);
     return;
   }
-  if (threadIdx.x == 0) gmem(later)[row] = 1;
+  if constexpr (again(W)) {
+    __syncthreads();
+    double sum = all;
+    if (!row_of.fits) {   // (some waves have not gone to their stretches' ends)
+      sum = measure_row<T, 64 * W>(z, s, p, top, e, lds.part);
+      if (!(__builtin_fabsf(top) < __builtin_inff())) {
+        if (threadIdx.x == 0) write_bad(p, row);
+        return;
+      }
+      bound = bound_of(want, top, top, sum / e.of(top), V);
+    }
+    sample_from_memory<T, 64 * W>(z, s, row, p, e, top, sum, bound, lds.block, &lds.chunk[0][0]);
+  } else {
+    if (threadIdx.x == 0) gmem(later)[row] = 1;
+  }
 }
 
 // The rows that were left, in blocks of 1024 threads.
@@ -1159,7 +1208,7 @@ constexpr int kLaterThreads = 1024, kLaterBlocks = 512;
 template <class T>
 __global__ __launch_bounds__(kLaterThreads) void sample_later_kernel(const T *logits, SampleParams p, const int32_t *later,
                                                                      int32_t rows) {
-  constexpr int THR = kLaterThreads;
+  constexpr int THR = kLaterThreads, N = Vec<T>::N;
   __shared__ union {
     BlockLds<THR> block;
     double chunk[HIMUON_TOP_VOCAB / (4 * 64)];
@@ -1167,7 +1216,18 @@ __global__ __launch_bounds__(kLaterThreads) void sample_later_kernel(const T *lo
   __shared__ double wave[THR / 64];
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     if (gmem(later)[row] == 0) continue;
-    sample_from_memory<T, THR>(logits + row * p.ld_logits, settings_of(p, row), row, p, lds.block, wave, lds.chunk);
+    const T *z = logits + row * p.ld_logits;
+    const Settings s = settings_of(p, row);
+    Powers e;
+    e.unit = __builtin_amdgcn_ldexp(1., p.mass_bits);
+    float top;
+    const double all = measure_row<T, THR>(z, s, p, top, e, wave);
+    __syncthreads();
+    if (!(__builtin_fabsf(top) < __builtin_inff())) {
+      if (threadIdx.x == 0) write_bad(p, row);
+      continue;
+    }
+    sample_from_memory<T, THR>(z, s, row, p, e, top, all, -__FLT_MAX__, lds.block, lds.chunk);
     __syncthreads();
   }
 }
@@ -1214,6 +1274,43 @@ __device__ __forceinline__ void write_entry(u64 key, int i, const TopParams &p, 
   Vec<T>::store1(reinterpret_cast<T *>(p.value) + row * p.ld_top + i, logit_of<T>(key));
 }
 
+// A row that is read from memory for every pass over it, by the THR threads of a block; keys: room for
+// sort_size(k) of them, which may be in the histogram's place.
+template <class T, int THR>
+__device__ __forceinline__ void top_from_memory(const T *z, const TopParams &p, int64_t row, BlockLds<THR> &block, u64 *keys,
+                                                Softmax *waves, int &found) {
+  constexpr int N = Vec<T>::N;
+  const int V = p.vocab, tid = threadIdx.x;
+  u64 border = ~(u64)0;
+  if (tid == 0) found = 0;
+  if (p.k < V)
+    border = find_border_in_row<T, THR, true>(z, V, 0, last_key<T>(-__builtin_inff()), [](float) { return (u64)1; },
+                                              [&](u64) { return (u64)p.k; }, block);
+  __syncthreads();
+  float m = -__builtin_inff(), sum = 0.f;
+  each_vector<T, THR>(z, V, [&](int at, float (&x)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const u64 r = rank_key<T>(x[e], at * N + e);
+      if (at * N + e >= V) continue;
+      if (r <= border) keys[atomicAdd(&found, 1)] = r;
+      else m = __builtin_fmaxf(m, x[e]);
+    }
+  });
+  const int size = sort_size(p.k);
+  for (int i = p.k + tid; i < size; i += THR) keys[i] = ~(u64)0;
+  __syncthreads();
+  sort_keys<THR>(keys, size);
+  for (int i = tid; i < p.k; i += THR) write_entry<T>(keys[i], i, p, row);
+  const float ref = ref_of(m);
+  each_vector<T, THR>(z, V, [&](int at, float (&x)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (at * N + e < V && rank_key<T>(x[e], at * N + e) > border) sum += pow2(x[e], p.k2, ref);
+  });
+  write_rest<THR>(m, sum, p, row, waves);
+}
+
 template <class T, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) void top_kernel(const T *logits, TopParams p,
                                                                                          int32_t *later) {
@@ -1232,7 +1329,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
   float top, bound;
   first_bounds<T, W>(now, share, lds, top, bound);
   const Stretch mine = sweep<T, true, (W >= 16)>(now, z, V, t0, t1, want, false, bound, bound, lds.list[w], nullptr,
-                                                 t1 - t0 > 1 && share.ranks <= W ? share.quota : 0);
+                                                 turns > W && share.ranks <= W ? share.quota : 0);
   leave_stretch<W>(mine, lds);
   const Together row_of = together(lds);
   // (the others' sums, relative to the largest of their references)
@@ -1264,14 +1361,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
     const int n = join_lists<T>(lds, bound);
     u64 *keys = lds.joined();
     fits = n <= RowLds<W>::kJoined && n >= p.k;
+    // (where a stretch's list followed its kQuota-th largest, the lists hold what is not below what that raised its bound
+    // to: enough where that is not above the bound for all, or where there are k of it)
     if (fits && p.k > kQuota) {
-      // (the bound of a stretch followed its kQuota-th largest: the k largest are in the lists if that many are not
-      // below the largest bound)
-      const float most = nth_bound<W>(lds.bound, 1);
-      int c = 0;
-      for (int j = 0; j < n; j += 64)
-        c += __builtin_popcountll(__ballot(j + lane < n && logit_of<T>(keys[j + lane < n ? j + lane : 0]) >= most));
-      fits = c >= p.k;
+      const float most = nth_bound<W>(lds.raised, 1);
+      fits = most <= bound || count_from<T>(keys, n, most) >= p.k;
     }
     if (fits) {
       const auto other = [&](u64 r) {
@@ -1299,53 +1393,26 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
       write_rest<THR>(m, rest, p, row, waves);
     }
   }
-  if (threadIdx.x == 0) gmem(later)[row] = !fits;
+  if constexpr (again(W)) {
+    if (fits) return;
+    __syncthreads();
+    top_from_memory<T, THR>(z, p, row, lds.block, lds.joined(), waves, lds.count[0]);
+  } else {
+    if (threadIdx.x == 0) gmem(later)[row] = !fits;
+  }
 }
 
 template <class T>
 __global__ __launch_bounds__(kLaterThreads) void top_later_kernel(const T *logits, TopParams p, const int32_t *later,
                                                                   int32_t rows) {
-  constexpr int THR = kLaterThreads, N = Vec<T>::N;
+  constexpr int THR = kLaterThreads;
   __shared__ BlockLds<THR> block;
   __shared__ u64 keys[HIMUON_TOP_MOST];
   __shared__ Softmax waves[THR / 64];
   __shared__ int found;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     if (gmem(later)[row] == 0) continue;
-    const T *z = logits + row * p.ld_logits;
-    const int V = p.vocab, tid = threadIdx.x;
-    u64 border = ~(u64)0;
-    if (tid == 0) found = 0;
-    if (p.k < V)
-      border = find_border_in_row<T, THR, true>(z, V, 0, last_key<T>(-__builtin_inff()), [](float) { return (u64)1; },
-                                                [&](u64) { return (u64)p.k; }, block);
-    __syncthreads();
-    float m = -__builtin_inff(), sum = 0.f;
-    for (int at = tid; at * N < V; at += THR) {
-      float x[N];
-      Vec<T>::unpack(row_vector(z, at, V), x);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const u64 r = rank_key<T>(x[e], at * N + e);
-        if (at * N + e >= V) continue;
-        if (r <= border) keys[atomicAdd(&found, 1)] = r;
-        else m = __builtin_fmaxf(m, x[e]);
-      }
-    }
-    const int size = sort_size(p.k);
-    for (int i = p.k + tid; i < size; i += THR) keys[i] = ~(u64)0;
-    __syncthreads();
-    sort_keys<THR>(keys, size);
-    for (int i = tid; i < p.k; i += THR) write_entry<T>(keys[i], i, p, row);
-    const float ref = ref_of(m);
-    for (int at = tid; at * N < V; at += THR) {
-      float x[N];
-      Vec<T>::unpack(row_vector(z, at, V), x);
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (at * N + e < V && rank_key<T>(x[e], at * N + e) > border) sum += pow2(x[e], p.k2, ref);
-    }
-    write_rest<THR>(m, sum, p, row, waves);
+    top_from_memory<T, THR>(logits + row * p.ld_logits, p, row, block, keys, waves, found);
     __syncthreads();
   }
 }
@@ -1385,11 +1452,13 @@ hipError_t launch_sample_t(const himuon_sampling &c, SampleParams p, int32_t *la
     });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((sample_later_kernel<T>), dim3(rows < kLaterBlocks ? rows : kLaterBlocks), dim3(kLaterThreads), 0,
-                       stream, z + r * c.ld_logits, p, later, (int32_t)rows);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    later += rows;
+    if (!again(W)) {
+      hipLaunchKernelGGL((sample_later_kernel<T>), dim3(rows < kLaterBlocks ? rows : kLaterBlocks), dim3(kLaterThreads), 0,
+                         stream, z + r * c.ld_logits, p, later, (int32_t)rows);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      later += rows;
+    }
     p.uniform += rows;
     if (p.temperature) p.temperature += rows;
     if (p.top_k) p.top_k += rows;
@@ -1416,11 +1485,13 @@ hipError_t launch_top_t(const himuon_top &c, TopParams p, int32_t *later, hipStr
     });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((top_later_kernel<T>), dim3(rows < kLaterBlocks ? rows : kLaterBlocks), dim3(kLaterThreads), 0,
-                       stream, z + r * c.ld_logits, p, later, (int32_t)rows);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    later += rows;
+    if (!again(W)) {
+      hipLaunchKernelGGL((top_later_kernel<T>), dim3(rows < kLaterBlocks ? rows : kLaterBlocks), dim3(kLaterThreads), 0,
+                         stream, z + r * c.ld_logits, p, later, (int32_t)rows);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      later += rows;
+    }
     p.value = reinterpret_cast<T *>(p.value) + rows * p.ld_top;
     p.index += rows * p.ld_top;
     p.rest += rows;
