@@ -46,14 +46,14 @@ struct EntrySums {
 };
 struct EntryLds {
   int *token;        // kNone, or the token
-  float *t, *z;      // the teacher's logit, the student's logit
+  float *t, *z, *g;  // the teacher's logit, the student's logit, the gradient
   unsigned char *marks;
 };
 __device__ __forceinline__ EntryLds entry_lds(u32x4 *lds, size_t mark_bytes, int entries) {
   float *f = reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + mark_bytes);
-  return {reinterpret_cast<int *>(f), f + entries, f + 2 * entries, reinterpret_cast<unsigned char *>(lds)};
+  return {reinterpret_cast<int *>(f), f + entries, f + 2 * entries, f + 3 * entries, reinterpret_cast<unsigned char *>(lds)};
 }
-size_t entry_lds_bytes(size_t mark_bytes, int entries) { return mark_bytes + 12 * (size_t)entries; }
+size_t entry_lds_bytes(size_t mark_bytes, int entries) { return mark_bytes + 16 * (size_t)entries; }
 
 __device__ __forceinline__ float entry_value(const DistillParams &p, int64_t at) {
   return p.value_bf16 ? bf16_bits_to_f32(gmem(reinterpret_cast<const unsigned short *>(p.value))[at])
@@ -108,6 +108,11 @@ __device__ __forceinline__ Softmax rest_join(float max, float sum, float k, Soft
   const Softmax s = lds[lane % W];
   m = wave_max(s.ref);
   return {m, wave_sum(lane < W ? s.sum * pow2(s.ref, k, ref_of(m)) : 0.f)};
+}
+
+// A number that is the same in all lanes, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
 }
 
 // What a row's gradient and divergence need, the same in every thread.
@@ -186,28 +191,43 @@ __device__ __forceinline__ float entry_gradient(const EntryLds &e, int j, bool t
   }
   return (float)(r.coef * (power(e.z[j], r.named_ref, p) * r.named_f - q * r.teacher_f));
 }
-// A vector of the rest's gradient, but for the elements that are marked.
+// A vector of the rest's gradient.
 template <class T, bool NT>
-__device__ __forceinline__ void rest_gradient(T *dz, u32x4 v, unsigned b, const RowCoefs &r, float k) {
+__device__ __forceinline__ void rest_gradient(T *dz, u32x4 v, float f, float ref, float k) {
   constexpr int N = Vec<T>::N;
   float x[N];
   Vec<T>::unpack(v, x);
 #pragma unroll
-  for (int e = 0; e < N; ++e) x[e] = r.rest_f * pow2(x[e], k, r.rest_ref);
-  if (b == 0) {
-    Vec<T>::template store<NT>(dz, x);
-    return;
+  for (int e = 0; e < N; ++e) x[e] = f * pow2(x[e], k, ref);
+  Vec<T>::template store<NT>(dz, x);
+}
+// The gradients of a row's named tokens, over what stands in their places.  Entry j's is computed by thread j, and
+// stored by the wave that has stored its vector: a wave's stores to one address stay in their order.  (Vectors with
+// holes and named tokens' elements in them afterwards are twice as many stores of parts of lines, which are slow where
+// they go past the L2s: 4096 rows of 128256 bf16, 64 entries, 438 us, and 466 us with holes.)
+// owner: of a vector (the row's last elements are that of one more).  Every thread calls it.
+template <class T, int THR, class OWNER>
+__device__ __forceinline__ void named_gradients(T *dz, const EntryLds &e, bool twice, const RowCoefs &coefs,
+                                                const DistillParams &p, OWNER owner) {
+  if ((int)threadIdx.x < p.entries) {
+    const RowCoefs r = coefs;
+    // (an entry's gradient takes all teacher's logits of its token: it has a place of its own)
+    for (int j = threadIdx.x; j < p.entries; j += THR)
+      if (e.token[j] != kNone) e.g[j] = entry_gradient(e, j, twice, r, p);
   }
-#pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (!(b >> e & 1)) Vec<T>::store1(dz + e, x[e]);
+  lds_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  for (int j = threadIdx.x & 63; j < p.entries; j += 64) {
+    const int token = e.token[j];
+    if (token != kNone && owner(token / Vec<T>::N) == (int)threadIdx.x >> 6) Vec<T>::store1(dz + token, e.g[j]);
+  }
 }
 
 enum { kForward = 0, kGradient = 1, kGradientNT = 2 };
 
 // A row's marks: a byte for each held vector, K a thread side by side, so that a thread has its own
 // with one load; then the other vectors' bits, in order; then a byte for each of the row's last V % N
-// elements.  Where those start, and how many bytes all take (2^20 logits: 152 KB with the entries).
+// elements.  Where those start, and how many bytes all take (2^20 logits: 155 KB with the entries).
 __host__ __device__ constexpr int tail_marks_of(int64_t vecs, int n, int held) {
   return held + (int)(((vecs > held ? vecs - held : 0) * n + 7) / 8);
 }
@@ -229,6 +249,7 @@ __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dl
   constexpr bool GRAD = OUT != kForward, NT = OUT == kGradientNT;
   extern __shared__ u32x4 lds[];
   __shared__ EntrySums sums;
+  __shared__ RowCoefs coefs[THR / 64];
   __shared__ Softmax parts[THR / 64];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, V = p.vocab, vecs = V / N, tail_at = vecs * N + tid;
@@ -315,8 +336,7 @@ __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dl
 #pragma unroll
   for (int i = 0; i < K; ++i)
     if (marks[i]) hide<T>(v[i], marks[i]);
-  const bool tail_named = tail_at < V && e.marks[tail_marks + tid];
-  if (tail_named) tail = -__builtin_inff();
+  if (tail_at < V && e.marks[tail_marks + tid]) tail = -__builtin_inff();
 
   float m = tail;
 #pragma unroll
@@ -341,8 +361,19 @@ __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dl
     }
   }
   const Softmax rest = rest_join<THR / 64>(m, sum, p.k, parts);
-  const RowCoefs r = row_coefs(rest, sums, waves, teacher_rest, w, p);
-  if (!r.live) {
+  // (in LDS for later: the registers are full of the row)
+  float rest_f, rest_ref;
+  bool live;
+  {
+    const RowCoefs r = row_coefs(rest, sums, waves, teacher_rest, w, p);
+    if ((tid & 63) == 0 && (wave < waves || wave == THR / 64 - 1)) coefs[wave] = r;
+    rest_f = uniform(r.rest_f);
+    rest_ref = uniform(r.rest_ref);
+    live = r.live;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  if (!live) {
     if (tid == 0) gmem(p.kl)[row] = 0.f;
     if constexpr (GRAD) zero_row<T, THR, NT>(dz, V);
     return;
@@ -351,22 +382,19 @@ __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dl
     if constexpr (LONG) {
       for (at -= THR; at >= HELD; at -= THR) {
         u32x4 x = Vec<T>::load(z + (int64_t)at * N);
-        const unsigned b = long_marks<T, HELD>(e.marks, at);
-        if (b) hide<T>(x, b);
-        rest_gradient<T, NT>(dz + (int64_t)at * N, x, b, r, p.k);
+        rest_gradient<T, NT>(dz + (int64_t)at * N, x, rest_f, rest_ref, p.k);
       }
     }
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int vec = tid + i * THR;
-      if (LONG || vec < vecs) rest_gradient<T, NT>(dz + vec * N, v[i], marks[i], r, p.k);
+      if (LONG || vec < vecs) rest_gradient<T, NT>(dz + vec * N, v[i], rest_f, rest_ref, p.k);
     }
-    if (tail_at < V && !tail_named) Vec<T>::store1(dz + tail_at, r.rest_f * pow2(tail, p.k, r.rest_ref));
-    for (int j = tid; j < p.entries; j += THR)
-      if (e.token[j] != kNone) Vec<T>::store1(dz + e.token[j], entry_gradient(e, j, twice, r, p));
+    if (tail_at < V) Vec<T>::store1(dz + tail_at, rest_f * pow2(tail, p.k, rest_ref));
+    named_gradients<T, THR>(dz, e, twice, coefs[wave], p, [&](int vec) { return vec == vecs ? 0 : vec % THR / 64; });
   }
   if (wave == THR / 64 - 1) {   // (the last wave: it has the fewest entries)
-    const float kl = row_kl(e, r, rest, teacher_rest, p);
+    const float kl = row_kl(e, coefs[wave], rest, teacher_rest, p);
     if ((tid & 63) == 0) gmem(p.kl)[row] = kl;
   }
 }
@@ -413,7 +441,6 @@ struct Span {
   u32x4 v[K];
   float tail;
   unsigned char marks[K];
-  bool tail_named;
 
   __device__ __forceinline__ Span(const T *z, int V, int spans) {
     const int tid = threadIdx.x;
@@ -446,8 +473,7 @@ struct Span {
 #pragma unroll
     for (int i = 0; i < K; ++i)
       if (marks[i]) hide<T>(v[i], marks[i]);
-    tail_named = has_tail && e.marks[kSpanVecs + threadIdx.x];
-    if (tail_named) tail = -__builtin_inff();
+    if (has_tail && e.marks[kSpanVecs + threadIdx.x]) tail = -__builtin_inff();
   }
 };
 
@@ -495,6 +521,7 @@ __global__ __launch_bounds__(kSpanThreads) void distill_span_finish_kernel(const
   constexpr int THR = kSpanThreads, N = Vec<T>::N;
   extern __shared__ u32x4 lds[];
   __shared__ EntrySums sums;
+  __shared__ RowCoefs coefs;
   __shared__ bool joins;
   const int64_t row = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -522,7 +549,6 @@ __global__ __launch_bounds__(kSpanThreads) void distill_span_finish_kernel(const
         top[0] = max(top[0], ordered(x[0]));
         top[1] = max(top[1], ordered(e.t[j]));
         if (x[1] == 0.f) sums.twice = 1;
-        if (GRAD && s.holds(token)) s.mark_token(e, (int)token, sums);
       }
       if (tid == 0 && teacher_rest != -__builtin_inf()) top[1] = max(top[1], ordered((float)teacher_rest));
       top[0] = wave_max(top[0]);
@@ -563,7 +589,7 @@ __global__ __launch_bounds__(kSpanThreads) void distill_span_finish_kernel(const
     if constexpr (GRAD) {
       // (the span's own vectors were not read where the row is left out: its bounds are those of the call)
       const int v0 = blockIdx.x * kSpanVecs, vecs = p.vocab / N, tail_at = vecs * N + tid;
-      const bool has_tail = (int)blockIdx.x == spans - 1 && tail_at < p.vocab;
+      const bool has_last = (int)blockIdx.x == spans - 1, has_tail = has_last && tail_at < p.vocab;
       if (!r.live) {
         const float zero[N] = {};
 #pragma unroll
@@ -573,16 +599,18 @@ __global__ __launch_bounds__(kSpanThreads) void distill_span_finish_kernel(const
         }
         if (has_tail) Vec<T>::store1(dz + tail_at, 0.f);
       } else {
-        s.hide_named(e);
         const bool twice = sums.twice != 0;
 #pragma unroll
         for (int i = 0; i < kSpanK; ++i) {
           const int at = v0 + tid + i * THR;
-          if (at < vecs) rest_gradient<T, false>(dz + (int64_t)at * N, s.v[i], s.marks[i], r, p.k);
+          if (at < vecs) rest_gradient<T, false>(dz + (int64_t)at * N, s.v[i], r.rest_f, r.rest_ref, p.k);
         }
-        if (has_tail && !s.tail_named) Vec<T>::store1(dz + tail_at, r.rest_f * pow2(s.tail, p.k, r.rest_ref));
-        for (int j = tid; j < p.entries; j += THR)
-          if (e.token[j] != kNone && s.holds(e.token[j])) Vec<T>::store1(dz + e.token[j], entry_gradient(e, j, twice, r, p));
+        if (has_tail) Vec<T>::store1(dz + tail_at, r.rest_f * pow2(s.tail, p.k, r.rest_ref));
+        if (tid == 0) coefs = r;
+        lds_barrier();
+        named_gradients<T, THR>(dz, e, twice, coefs, p, [&](int vec) {
+          return vec == vecs ? (has_last ? 0 : -1) : vec < v0 || vec >= v0 + kSpanVecs ? -1 : (vec - v0) % THR / 64;
+        });
       }
     }
   }
