@@ -3,9 +3,10 @@
     python examples/policy_finetune.py [--steps 60] [--state-bits 8]
 
 A two-layer network over a window of tokens learns by reward alone to continue sequences
-by a fixed rule: it samples answers, scores them, and takes a few steps of the clipped
-policy loss with a KL term to the starting policy on each batch (policy_loss gives the
-gradient of the logits, torch the rest of the backward pass).  The gradient's norm and clip
+by a fixed rule: it samples answers (sample gives them with their log probabilities), scores
+them, and takes a few steps of the clipped policy loss with a KL term to the starting policy
+on each batch (policy_loss gives the gradient of the logits, torch the rest of the backward
+pass).  The gradient's norm and clip
 factor stay on the device (GradNorm); the matrices are updated by HiMuon and everything else
 (embedding, gains, biases) by the library's AdamW.  Synthetic data, random weights.
 """
@@ -21,6 +22,7 @@ import tiled_newton_schulz_tile_amd as hm  # noqa: E402
 from tiled_newton_schulz_tile_amd.adamw import GradNorm  # noqa: E402
 from tiled_newton_schulz_tile_amd.optim import AdamWOptimizer, HiMuonOptimizer  # noqa: E402
 from tiled_newton_schulz_tile_amd.policy import policy_loss  # noqa: E402
+from tiled_newton_schulz_tile_amd.sampling import sample  # noqa: E402
 
 VOCAB, WINDOW, WIDTH = 509, 3, 256
 
@@ -58,14 +60,13 @@ def train(steps=60, state_bits=8, rows=2048, epochs=2, seed=0, log=print):
         window = torch.randint(0, VOCAB, (rows, WINDOW), device="cuda")
         with torch.no_grad():
             logits = model(window)
-            token = torch.distributions.Categorical(logits=logits).sample()
+            token, old, _ = sample(logits, torch.rand(rows, device="cuda"))
             # a dense reward: how near the answer is to the rule's
             gap = (token - rule(window)).abs().float() / VOCAB
             reward = torch.exp(-8 * gap)
             rewards.append(reward.mean())
             advantage = (reward - reward.mean()) / (reward.std() + 1e-6)
             weight = torch.full((rows,), 1.0 / rows, device="cuda")
-            old = policy_loss(logits, token, weight, advantage, dlogits=False).logp
             ref = policy_loss(reference(window), token, weight, advantage, dlogits=False).logp
         for _ in range(epochs):
             logits = model(window)
