@@ -412,16 +412,21 @@ __device__ __forceinline__ float nth_largest(const float (&x)[N], int quota) {
     }
   }
 }
-// The same of a list.
-template <class T>
-__device__ __forceinline__ float nth_of_list(const u64 *list, int n, int quota) {
-  float x[kListMost / 64];
+// The same of a list.  SHORT: of a short one in fewer steps.
+template <class T, int N>
+__device__ __forceinline__ float nth_of_keys(const u64 *list, int n, int quota) {
+  float x[N];
 #pragma unroll
-  for (int i = 0; i < kListMost / 64; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int j = i * 64 + (threadIdx.x & 63);
     x[i] = j < n ? logit_of<T>(list[j]) : -__builtin_inff();
   }
   return nth_largest(x, quota);
+}
+template <class T, bool SHORT>
+__device__ __forceinline__ float nth_of_list(const u64 *list, int n, int quota) {
+  if (SHORT && n <= 320) return nth_of_keys<T, 5>(list, n, quota);
+  return nth_of_keys<T, kListMost / 64>(list, n, quota);
 }
 
 // x[e], e a lane's own.
@@ -438,7 +443,7 @@ __device__ __forceinline__ float pick_element(const float (&x)[N], int e) {
 }
 // Appends a vector's elements from `least` on (finite: the vectors behind a row are -inf) to the wave's list of n keys
 // (of which kListMost are kept; n counts on), in the order of their indices.  A lane mostly has one at most: one turn
-// of the loop.  4096 x 128256 bf16, k = 64: 310 us, and 335 us with a step for each of a vector's elements.
+// of the loop.  4096 x 128256 bf16, k = 64: 295 us; it was 310 us, and 335 us with a step for each of a vector's elements.
 template <class T, int N>
 __device__ __forceinline__ void append(u64 *list, int &n, int at, const float (&x)[N], float least) {
   unsigned m = 0;
@@ -667,7 +672,7 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
       if (__any(most >= bound)) {
         append<T>(list, out.n, at, x, bound);
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = x[j] < bound ? x[j] : -__builtin_inff();
+        for (int j = 0; j < N; ++j) x[j] = x[j] >= bound ? -__builtin_inff() : x[j];
       }
     }
     if (!CEIL && exact) {
@@ -734,7 +739,7 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
       wave_sync();
       float b;
       if (want.quota > 0) {
-        b = nth_of_list<T>(list, out.n, raise ? want.quota : last_quota);
+        b = nth_of_list<T, !SMALL>(list, out.n, raise ? want.quota : last_quota);
       } else {
         double all = sum;
         for (int j = lane; j < out.n; j += 64) all += e.of(logit_at(j));
