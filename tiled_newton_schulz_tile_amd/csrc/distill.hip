@@ -626,12 +626,18 @@ __global__ __launch_bounds__(kSpanThreads) void distill_span_finish_kernel(const
   write_loss<THR / 64, true>(p.weight, p.kl, gridDim.y, loss);
 }
 
-constexpr int kFewRows = 128;
-bool few_rows(int64_t rows, int64_t vecs) {
-  return rows > 0 && ((rows <= 64 && vecs >= 256) || (rows <= kFewRows && vecs >= 2048));
+// Whether rows are cut into spans.  Gradient in spans and by rows, us: 8 x 32000 bf16 12.4 and 11.4, 1 x 128256 11.3
+// and 21.7, 32 x 128256 17.0 and 23.3, 128 x 128256 55.5 and 24.8, 32 x 262144 22.3 and 40.0, 100 x 262144 59.4 and 44.0,
+// 8 x 50257 fp32 11.8 and 13.9.  Forward alone: 32 x 128256 11.0 and 16.4, 128 x 128256 17.6 and 18.0, 128 x 50257 fp32
+// 14.3 and 12.6.
+constexpr int kFewRows = 32, kFewRowsForward = 64, kFewVecs = 8192;
+bool few_rows(const himuon_distill &p) {
+  const int64_t vecs = p.vocab / (p.dtype == HIMUON_BF16 ? 8 : 4);
+  return p.rows > 0 && vecs > kFewVecs && p.rows <= (p.dlogits ? kFewRows : kFewRowsForward);
 }
 
-// A gradient that the L2s together (32 MB) cannot hold goes past them.
+// A gradient that the L2s together (32 MB) cannot hold goes past them (4096 x 128256 bf16 without left-out rows 503 us,
+// 530 through them; 1000 x 50257 fp32 84 and 102; below that no difference).
 constexpr double kL2Bytes = 32e6;
 
 template <typename T, int THR, int K, bool LONG, int OUT>
@@ -652,7 +658,7 @@ hipError_t launch_distill_t(const himuon_distill &c, const DistillParams &p, hip
   const T *z = reinterpret_cast<const T *>(c.logits);
   T *dz = reinterpret_cast<T *>(c.dlogits);
   const int64_t vecs = c.vocab / Vec<T>::N;
-  if (few_rows(c.rows, vecs)) {
+  if (few_rows(c)) {
     const unsigned spans = (unsigned)span_count(vecs), rows = (unsigned)c.rows;
     const size_t lds = entry_lds_bytes(Span<T>::kMarkBytes, c.k);
     hipLaunchKernelGGL((distill_span_kernel<T>), dim3(spans, rows), dim3(kSpanThreads), lds, stream, z, p);
@@ -697,7 +703,7 @@ hipError_t launch_distill_t(const himuon_distill &c, const DistillParams &p, hip
 // The ticket, the spans of few long rows and their entries' logits; other rows need nothing.
 size_t distill_workspace(const himuon_distill &p) {
   const int64_t vecs = p.vocab / (p.dtype == HIMUON_BF16 ? 8 : 4);
-  return few_rows(p.rows, vecs) ? 16 + (size_t)p.rows * (span_count(vecs) * sizeof(f32x2) + p.k * sizeof(f32x2)) : 0;
+  return few_rows(p) ? 16 + (size_t)p.rows * (span_count(vecs) * sizeof(f32x2) + p.k * sizeof(f32x2)) : 0;
 }
 
 hipError_t launch_distill(const himuon_distill &c, void *workspace, hipStream_t stream) {

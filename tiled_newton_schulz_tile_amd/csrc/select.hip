@@ -12,8 +12,8 @@
 // of the row.  What they may keep is all from a bound on, which rises on the way: the k-th largest
 // logit so far, or one below which all tokens together have too little probability to matter.  Borders
 // and draw then come from the lists.  Waves meet once, at the end of the row; with many rows a block is
-// one wave.  Rows whose lists overflow (flat ones) are left to a second launch, which reads them several
-// times.
+// one wave.  Rows whose lists overflow (flat ones) are read again several times: by blocks of 4 waves or more
+// at once, for smaller ones by a second launch.
 //
 // A border is found by a descent over the digits of the rank key: a histogram of the elements in the
 // present range, the bin in which the count (or the probability) reaches its target, and that bin as
@@ -412,7 +412,7 @@ __device__ __forceinline__ float nth_largest(const float (&x)[N], int quota) {
     }
   }
 }
-// The same of a list.  SHORT: of a short one in fewer steps.
+// The same of a list, of a short one in fewer steps (4096 x 128256 bf16, k = 64: 295 us, 310 us without).
 template <class T, int N>
 __device__ __forceinline__ float nth_of_keys(const u64 *list, int n, int quota) {
   float x[N];
@@ -423,9 +423,9 @@ __device__ __forceinline__ float nth_of_keys(const u64 *list, int n, int quota) 
   }
   return nth_largest(x, quota);
 }
-template <class T, bool SHORT>
+template <class T>
 __device__ __forceinline__ float nth_of_list(const u64 *list, int n, int quota) {
-  if (SHORT && n <= 320) return nth_of_keys<T, 5>(list, n, quota);
+  if (n <= 320) return nth_of_keys<T, 5>(list, n, quota);
   return nth_of_keys<T, kListMost / 64>(list, n, quota);
 }
 
@@ -443,7 +443,7 @@ __device__ __forceinline__ float pick_element(const float (&x)[N], int e) {
 }
 // Appends a vector's elements from `least` on (finite: the vectors behind a row are -inf) to the wave's list of n keys
 // (of which kListMost are kept; n counts on), in the order of their indices.  A lane mostly has one at most: one turn
-// of the loop.  4096 x 128256 bf16, k = 64: 295 us; it was 310 us, and 335 us with a step for each of a vector's elements.
+// of the loop (4096 x 128256 bf16, k = 64: 310 us then, and 335 us with a step for each of a vector's elements).
 template <class T, int N>
 __device__ __forceinline__ void append(u64 *list, int &n, int at, const float (&x)[N], float least) {
   unsigned m = 0;
@@ -617,9 +617,8 @@ __device__ __forceinline__ u64 find_border_in_row(const T *z, int V, u64 first, 
 // powers are relative to and a first bound (which hold for the row).  exact: powers in fp64; else in fp32.
 // They are relative to a logit that follows the largest, and if CEIL (fp32 alone) to one that follows the
 // bound, above which nothing is summed.  turns: nullptr, or what each turn weighs.  last_quota: rank of the
-// logit in the final list that last_bound is not above (0: none).  SMALL: short code rather than few
-// instructions, for calls that are so small that they wait for their code to be fetched.
-template <class T, bool CEIL, bool SMALL>
+// logit in the final list that last_bound is not above (0: none).
+template <class T, bool CEIL>
 __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0, int t1, const Wants &want, bool exact,
                                          float ref, float bound, u64 *list, double *turns, int last_quota) {
   constexpr int N = Vec<T>::N;
@@ -699,27 +698,17 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
     part = 0;
     const bool more = t + 1 < t1;
     const int first = (t * kTurn + lane) * N;
-    if constexpr (SMALL) {
-#pragma unroll 1
-      for (int i = 0; i < kTurnVecs; ++i) {
-        float x[N];
-        Vec<T>::unpack(now.pick(i), x);
-        vector(first + i * 64 * N, x);
-      }
-      if (more) now.load(z, t + 1, V);
-    } else {
-      const bool whole = (t + 2) * kTurn * N <= V;   // (the next turn)
+    const bool whole = (t + 2) * kTurn * N <= V;   // (the next turn)
 #pragma unroll
-      for (int i = 0; i < kTurnVecs; ++i) {
-        float x[N];
-        Vec<T>::unpack(now.v[i], x);
-        if (more) {   // its place takes the next turn's
-          const int at = (t + 1) * kTurn + 64 * i + lane;
-          now.v[i] = whole ? Vec<T>::load(z + (int64_t)at * N) : row_vector(z, at, V);
-        }
-        vector(first + i * 64 * N, x);
-        __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < kTurnVecs; ++i) {
+      float x[N];
+      Vec<T>::unpack(now.v[i], x);
+      if (more) {   // its place takes the next turn's
+        const int at = (t + 1) * kTurn + 64 * i + lane;
+        now.v[i] = whole ? Vec<T>::load(z + (int64_t)at * N) : row_vector(z, at, V);
       }
+      vector(first + i * 64 * N, x);
+      __builtin_amdgcn_sched_barrier(0);
     }
     if (stop || out.n > kListMost) {
       out.top = wave_maximum(largest);
@@ -739,7 +728,7 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
       wave_sync();
       float b;
       if (want.quota > 0) {
-        b = nth_of_list<T, !SMALL>(list, out.n, raise ? want.quota : last_quota);
+        b = nth_of_list<T>(list, out.n, raise ? want.quota : last_quota);
       } else {
         double all = sum;
         for (int j = lane; j < out.n; j += 64) all += e.of(logit_at(j));
@@ -880,8 +869,10 @@ __device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s
   if (lane == i) write_token(p, row, s, e, v * N + i, mine, top, all, total);
 }
 
-// Whether a block of W waves itself goes through its row again where its lists do not hold what is asked for
-// (others leave it to a second launch).
+// Whether a block of W waves itself goes through its row again where its lists do not hold what is asked for.  Others
+// leave it to a second launch, which costs every call some microseconds (bf16: one row of 32000 24.7 us, 29.0 with two
+// launches; 2000 x 32000, top_p 88 us, 100), but blocks of 16 waves: where one row of 4096 x 32000 is flat, top_k is 240
+// us, and 361 where its one wave goes on with it.
 constexpr bool again(int W) { return W >= 4; }
 
 template <int W>
@@ -1046,10 +1037,9 @@ __device__ __forceinline__ int rank_among(const u64 *keys, int n, u64 r) {
   return rank;
 }
 
-// W waves take a row.  later: the rows that they cannot do are marked there for a second launch (a small
-// block is not made for going through a row several times).
+// W waves take a row.  later: the rows that small blocks cannot do are marked there for the second launch.
 template <class T, int W>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) void sample_kernel(const T *logits, SampleParams p,
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W == 2 ? 3 : 4))) void sample_kernel(const T *logits, SampleParams p,
                                                                                             int32_t *later) {
   constexpr int N = Vec<T>::N;
   __shared__ RowLds<W> lds;
@@ -1078,7 +1068,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
   }
   if (top > -__builtin_inff()) bound = __builtin_fmaxf(bound, bound_of(want, top, top, 1., V));
   if (threadIdx.x == 0) lds.settings = s;   // (for what follows the sweep, which has no registers to spare)
-  const Stretch mine = sweep<T, false, (W >= 16)>(now, z, V, t0, t1, want, exact, top, bound, lds.list[w],
+  const Stretch mine = sweep<T, false>(now, z, V, t0, t1, want, exact, top, bound, lds.list[w],
                                                   everything ? lds.turns[w] : nullptr,
                                                   turns > W && share.ranks <= W ? share.quota : 0);
   leave_stretch<W>(mine, lds);
@@ -1214,17 +1204,34 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
 
 // The rows that were left, in blocks of 1024 threads.
 constexpr int kLaterThreads = 1024, kLaterBlocks = 512;
+// f(row) for the marked rows that are this block's: the marks of THR of its rows are read at once.
+template <int THR, class F>
+__device__ __forceinline__ void marked_rows(const int32_t *later, int32_t rows, F f) {
+  __shared__ u64 marks[THR / 64];
+  const int64_t step = gridDim.x;
+  for (int64_t base = blockIdx.x; base < rows; base += THR * step) {
+    const int64_t row = base + threadIdx.x * step;
+    const u64 mine = __ballot(row < rows && gmem(later)[row < rows ? row : 0] != 0);
+    if ((threadIdx.x & 63) == 0) marks[threadIdx.x >> 6] = mine;
+    __syncthreads();
+    for (int w = 0; w < THR / 64; ++w)
+      for (u64 m = marks[w]; m != 0; m &= m - 1) {
+        f(base + (w * 64 + lane_of(m)) * step);
+        __syncthreads();
+      }
+    __syncthreads();
+  }
+}
 template <class T>
 __global__ __launch_bounds__(kLaterThreads) void sample_later_kernel(const T *logits, SampleParams p, const int32_t *later,
                                                                      int32_t rows) {
-  constexpr int THR = kLaterThreads, N = Vec<T>::N;
+  constexpr int THR = kLaterThreads;
   __shared__ union {
     BlockLds<THR> block;
     double chunk[HIMUON_TOP_VOCAB / (4 * 64)];
   } lds;
   __shared__ double wave[THR / 64];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    if (gmem(later)[row] == 0) continue;
+  marked_rows<THR>(later, rows, [&](int64_t row) {
     const T *z = logits + row * p.ld_logits;
     const Settings s = settings_of(p, row);
     Powers e;
@@ -1234,11 +1241,10 @@ __global__ __launch_bounds__(kLaterThreads) void sample_later_kernel(const T *lo
     __syncthreads();
     if (!(__builtin_fabsf(top) < __builtin_inff())) {
       if (threadIdx.x == 0) write_bad(p, row);
-      continue;
+      return;
     }
     sample_from_memory<T, THR>(z, s, row, p, e, top, all, -__FLT_MAX__, lds.block, lds.chunk);
-    __syncthreads();
-  }
+  });
 }
 
 struct TopParams {
@@ -1321,7 +1327,7 @@ __device__ __forceinline__ void top_from_memory(const T *z, const TopParams &p, 
 }
 
 template <class T, int W>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) void top_kernel(const T *logits, TopParams p,
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W == 2 ? 3 : 4))) void top_kernel(const T *logits, TopParams p,
                                                                                          int32_t *later) {
   constexpr int THR = 64 * W;
   __shared__ RowLds<W> lds;
@@ -1337,7 +1343,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
   const Wants want = {quota, raise_at(quota), p.k1, p.temp, 0., 0., false};
   float top, bound;
   first_bounds<T, W>(now, share, lds, top, bound);
-  const Stretch mine = sweep<T, true, (W >= 16)>(now, z, V, t0, t1, want, false, bound, bound, lds.list[w], nullptr,
+  const Stretch mine = sweep<T, true>(now, z, V, t0, t1, want, false, bound, bound, lds.list[w], nullptr,
                                                  turns > W && share.ranks <= W ? share.quota : 0);
   leave_stretch<W>(mine, lds);
   const Together row_of = together(lds);
@@ -1419,22 +1425,22 @@ __global__ __launch_bounds__(kLaterThreads) void top_later_kernel(const T *logit
   __shared__ u64 keys[HIMUON_TOP_MOST];
   __shared__ Softmax waves[THR / 64];
   __shared__ int found;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    if (gmem(later)[row] == 0) continue;
+  marked_rows<THR>(later, rows, [&](int64_t row) {
     top_from_memory<T, THR>(logits + row * p.ld_logits, p, row, block, keys, waves, found);
-    __syncthreads();
-  }
+  });
 }
 
 constexpr int64_t kLaunchRows = (int64_t)1 << 21;   // a grid holds fewer than 2^32 threads
 
-// Waves for a row: enough of them to fill the chip (256 CUs with 16 each), and as many as its
-// stretches' lengths ask for.
+// Waves for a row: enough of them to fill the chip (256 CUs with 16 each; with half of that 1024 x 128256 bf16 draws take
+// 146 us and not 121, with twice that the top 100 of 1023 x 50257 fp32 147 us and not 87), and as many as its stretches'
+// lengths ask for.  A block of 16 waves has a CU for itself, so 16 only where all blocks run at once (500 x 50257 fp32,
+// top_p: 45.8 us with 8, 56.9 with 16).
 constexpr int kFillWaves = 4096;
 int waves_of(int64_t rows, int64_t vecs, int least) {
   const int64_t turns = (vecs + kTurn - 1) / kTurn;
   int W = 1;
-  while (W < 16 && (W < least || turns > (int64_t)W * kTurns || (rows * W < kFillWaves && W < turns))) W *= 2;
+  while (W < 16 && (W < least || turns > (int64_t)W * kTurns || (rows * W < (W < 8 ? kFillWaves : kFillWaves / 2) && W < turns))) W *= 2;
   return W;
 }
 template <class F>
@@ -1449,9 +1455,13 @@ void with_waves(int W, F f) {
 template <class T>
 hipError_t launch_sample_t(const himuon_sampling &c, SampleParams p, int32_t *later, hipStream_t stream) {
   const T *z = reinterpret_cast<const T *>(c.logits);
-  // (a stretch's list holds its kQuota largest for certain; settings of each row are not known here)
-  int least = c.row_top_k ? 4 : 1;
+  // (a stretch's list holds its kQuota largest for certain; settings of each row are not known here; what top_p alone
+  // keeps often takes more than a list or two: 4096 x 128256 bf16, 0.9: 553 us with 4 waves, 744 with 2, 923 with 1)
+  const bool by_p = c.row_top_p || c.top_p < 1.;
+  int least = c.row_top_k || (by_p && !c.top_k) ? 4 : 1;
   while (!c.row_top_k && least < 8 && kQuota * least < c.top_k) least *= 2;
+  // (without filters, temperature 0 among them, no row has a list)
+  const bool lists = c.row_top_k || c.top_k || by_p || c.row_min_p || c.min_p > 0. || c.row_temperature || c.temperature == 0.;
   const int W = waves_of(c.rows, (c.vocab + Vec<T>::N - 1) / Vec<T>::N, least);
   for (int64_t r = 0; r < c.rows; r += kLaunchRows) {
     const unsigned rows = (unsigned)(c.rows - r < kLaunchRows ? c.rows - r : kLaunchRows);
@@ -1461,7 +1471,7 @@ hipError_t launch_sample_t(const himuon_sampling &c, SampleParams p, int32_t *la
     });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (!again(W)) {
+    if (!again(W) && lists) {
       hipLaunchKernelGGL((sample_later_kernel<T>), dim3(rows < kLaterBlocks ? rows : kLaterBlocks), dim3(kLaterThreads), 0,
                          stream, z + r * c.ld_logits, p, later, (int32_t)rows);
       e = hipGetLastError();
