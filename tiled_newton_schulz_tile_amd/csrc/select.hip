@@ -336,6 +336,7 @@ constexpr int kTurnVecs = 4;                  // vectors a lane has at a time
 constexpr int kTurn = 64 * kTurnVecs;         // vectors a wave has at a time
 constexpr int kTurns = 64;                    // turns of a stretch at most
 constexpr int kListMost = 768;                // keys of a list
+constexpr int kFirstTurns = 4;
 constexpr int kQuota = 224;                   // rank of the logit that the bound follows, at most
 constexpr float kFar = 100.f;                 // octaves
 
@@ -354,7 +355,7 @@ struct Stretch {
 // What the list of a stretch has to hold, and how its sum is taken.
 struct Wants {
   int quota;             // 0, or: the quota largest
-  int most;              // keys of the list above which the bound is raised
+  int most, then;        // keys of the list above which the bound is raised: in the first kFirstTurns, and then
   double k, temp;        // log2(e) / temperature, temperature
   double share_p;        // 0, or: all tokens but some with less than this share of all probability
   double share_m;        // 0, or: all tokens with at least this share of the largest's probability
@@ -723,8 +724,9 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
     }
     sum += part;
     part = 0;
-    while (out.n > want.most || (!more && last_quota > 0 && out.n >= last_quota)) {
-      const bool raise = out.n > want.most;
+    const int most = t - t0 < kFirstTurns ? want.most : want.then;
+    while (out.n > most || (!more && last_quota > 0 && out.n >= last_quota)) {
+      const bool raise = out.n > most;
       wave_sync();
       float b;
       if (want.quota > 0) {
@@ -756,7 +758,7 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
       }
       out.n = n;
       wave_sync();
-      if (n > want.most) {   // (more of them than a list is for)
+      if (n > most) {   // (more of them than a list is for)
         out.n = kListMost + 1;
         return out;
       }
@@ -777,9 +779,11 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
 }
 
 // Keys of a list at which the bound is raised to its quota-th largest (which leaves quota + quota / 8 + 8
-// of them): often while it rises, and with room for those of another turn, some quota in the beginning.
-__device__ __forceinline__ int raise_at(int quota) {
-  const int often = 2 * quota + 64, room = kListMost - 2 * quota - 32;
+// of them): often while it rises, and with room for those of another turn, some quota in the beginning and a
+// quarter of the list at most after kFirstTurns (with the first room all along the top 449 of 4096 x 128256 bf16 take
+// 847 us, and not 686: the bound is raised every 28 keys).
+__device__ __forceinline__ int raise_at(int quota, bool first) {
+  const int often = 2 * quota + 64, room = first ? kListMost - 2 * quota - 32 : kListMost * 3 / 4;
   return often < room ? often : room;
 }
 // A row's stretches: W waves, turns [0, turns) of the row in W parts.
@@ -1058,7 +1062,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W == 2 ?
   const bool everything = !s.by_k && !s.by_p && s.min_p == 0., exact = everything || (s.by_p && !s.by_k);
   const int quota = s.by_k ? s.top_k < kQuota ? s.top_k : kQuota : 0;
   const Shares share = shares_of<W>(s.by_k ? s.top_k : 0);
-  const Wants want = {quota, quota > 0 ? raise_at(quota) : kListMost - 256, s.k, s.temp,
+  const Wants want = {quota, quota > 0 ? raise_at(quota, true) : kListMost - 256, quota > 0 ? raise_at(quota, false) : kListMost - 256, s.k, s.temp,
                       s.by_p && !s.by_k ? 1. - s.top_p : 0., s.by_k && s.by_p ? 0. : s.min_p, everything};
   float top, bound;
   first_bounds<T, W>(now, share, lds, top, bound);
@@ -1276,7 +1280,6 @@ __device__ __forceinline__ void sort_keys(u64 *keys, int n) {
 }
 __device__ __forceinline__ int sort_size(int n) { return n <= 64 ? 64 : 1 << (32 - __builtin_clz(n - 1)); }
 
-constexpr int top_most(int W) { return W >= 8 ? HIMUON_TOP_MOST : kQuota * W; }   // k of a block of W waves
 template <int THR>
 __device__ __forceinline__ void write_rest(float max, float sum, const TopParams &p, int64_t row, Softmax *waves) {
   const Softmax s = block_softmax<THR / 64>(max, sum, p.k2, waves);
@@ -1340,7 +1343,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W == 2 ?
   now.load(z, t0 < t1 ? t0 : turns, V);
   const int quota = p.k < kQuota ? p.k : kQuota;
   const Shares share = shares_of<W>(p.k);
-  const Wants want = {quota, raise_at(quota), p.k1, p.temp, 0., 0., false};
+  const Wants want = {quota, raise_at(quota, true), raise_at(quota, false), p.k1, p.temp, 0., 0., false};
   float top, bound;
   first_bounds<T, W>(now, share, lds, top, bound);
   const Stretch mine = sweep<T, true>(now, z, V, t0, t1, want, false, bound, bound, lds.list[w], nullptr,
@@ -1437,6 +1440,10 @@ constexpr int64_t kLaunchRows = (int64_t)1 << 21;   // a grid holds fewer than 2
 // lengths ask for.  A block of 16 waves has a CU for itself, so 16 only where all blocks run at once (500 x 50257 fp32,
 // top_p: 45.8 us with 8, 56.9 with 16).
 constexpr int kFillWaves = 4096;
+// The k up to which W waves take a row: the joined list of 4 has room for little more than 640 (top 700 of 4096 x
+// 128256 bf16 1532 us with 4 waves, 1028 with 8), two lists are little for more than one holds (top 440 1404 us with 2
+// waves, 682 with 4), and one wave sorts up to 256 keys well (top 224 864 us with one, top 225 579 with 4).
+constexpr int most_of(int W) { return W >= 8 ? HIMUON_TOP_MOST : W == 4 ? 640 : 216; }
 int waves_of(int64_t rows, int64_t vecs, int least) {
   const int64_t turns = (vecs + kTurn - 1) / kTurn;
   int W = 1;
@@ -1459,7 +1466,7 @@ hipError_t launch_sample_t(const himuon_sampling &c, SampleParams p, int32_t *la
   // keeps often takes more than a list or two: 4096 x 128256 bf16, 0.9: 553 us with 4 waves, 744 with 2, 923 with 1)
   const bool by_p = c.row_top_p || c.top_p < 1.;
   int least = c.row_top_k || (by_p && !c.top_k) ? 4 : 1;
-  while (!c.row_top_k && least < 8 && kQuota * least < c.top_k) least *= 2;
+  while (!c.row_top_k && least < 8 && most_of(least) < c.top_k) least *= 2;
   // (without filters, temperature 0 among them, no row has a list)
   const bool lists = c.row_top_k || c.top_k || by_p || c.row_min_p || c.min_p > 0. || c.row_temperature || c.temperature == 0.;
   const int W = waves_of(c.rows, (c.vocab + Vec<T>::N - 1) / Vec<T>::N, least);
@@ -1494,7 +1501,7 @@ template <class T>
 hipError_t launch_top_t(const himuon_top &c, TopParams p, int32_t *later, hipStream_t stream) {
   const T *z = reinterpret_cast<const T *>(c.logits);
   int least = 1;
-  while (top_most(least) < c.k) least *= 2;
+  while (most_of(least) < c.k) least *= 2;
   const int W = waves_of(c.rows, (c.vocab + Vec<T>::N - 1) / Vec<T>::N, least);
   for (int64_t r = 0; r < c.rows; r += kLaunchRows) {
     const unsigned rows = (unsigned)(c.rows - r < kLaunchRows ? c.rows - r : kLaunchRows);
