@@ -387,3 +387,30 @@ def test_select_wrapper_refusals():
             top_logits(z, **bad)
     with pytest.raises(ValueError):
         top_logits(z.t(), 1)
+
+
+@pytest.mark.parametrize("N", [3, 300, 2100, 4200])
+@pytest.mark.parametrize("k", [1, 50, 216, 217, 640, 641, 1024])
+@pytest.mark.parametrize("way", ["up", "down", "mixed"])
+def test_ordered_rows(N, k, way):
+    """Rows that rise, fall or do neither, for every number of waves a row: rising ones raise a list's bound all the
+    way, and in ordered ones a single stretch has all that is kept.  Logits are all different in fp32, so torch's top k is the
+    only right one.  rest: each power is within 2^-23 (1 + ln 2 |x|) of itself, x below 30 octaves where it counts, so
+    the sum within 2^-18 and three levels of 2^-24, its logarithm by as much, and that is rounded."""
+    _need_gpu()
+    V = 9001
+    g = torch.Generator().manual_seed(k)
+    z = (torch.randperm(V, generator=g).double() / V * 20 - 10).float().expand(N, V).contiguous().cuda()
+    if way != "mixed":
+        z = z.sort(1, descending=way == "down").values.contiguous()
+    z += (torch.arange(N) % 7).float()[:, None].cuda()   # (rounds, but an order of steps of 2e-3 stays)
+    got = top_logits(z, k, temperature=0.9)
+    want = z.topk(k, 1)
+    assert torch.equal(got.value, want.values) and torch.equal(got.index, want.indices)
+    rest = (z.double().scatter(1, want.indices, -INF) / 0.9).logsumexp(1)
+    assert ((got.rest - rest).abs() <= 2.0 ** -17 + 2.0 ** -23 * rest.abs()).all()
+    u = torch.rand(N, generator=g).cuda()
+    for kw in (dict(top_k=k), dict(top_p=0.9), dict(min_p=0.05), dict(top_k=k, top_p=0.5, min_p=1e-4, temperature=3.0)):
+        drawn = sample(z, u, **kw)
+        some = torch.arange(0, N, max(1, N // 5))
+        assert check_sample(z[some], u[some], [x[some] for x in drawn], **kw) == len(some)

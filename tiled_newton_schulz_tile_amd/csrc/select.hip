@@ -516,7 +516,7 @@ __device__ __forceinline__ float turn_maximum(Turn<T> &turn, float (&most)[kTurn
   }
   return top;
 }
-// f(index of its first vector, its vectors) for the 64 vectors at a time of a row in memory that a wave has of THR threads'.
+// f(a lane's vector, its elements) for all vectors of a row in memory, 64 consecutive ones a wave and call.
 template <class T, int THR, class F>
 __device__ __forceinline__ void each_vector(const T *z, int V, F f) {
   const int lane = threadIdx.x & 63, turns = ((V + Vec<T>::N - 1) / Vec<T>::N + kTurn - 1) / kTurn;
@@ -1043,8 +1043,8 @@ __device__ __forceinline__ int rank_among(const u64 *keys, int n, u64 r) {
 
 // W waves take a row.  later: the rows that small blocks cannot do are marked there for the second launch.
 template <class T, int W>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W == 2 ? 3 : 4))) void sample_kernel(const T *logits, SampleParams p,
-                                                                                            int32_t *later) {
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W == 2 ? 3 : 4)))
+void sample_kernel(const T *logits, SampleParams p, int32_t *later) {
   constexpr int N = Vec<T>::N;
   __shared__ RowLds<W> lds;
   const int64_t row = blockIdx.x;
@@ -1062,7 +1062,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W == 2 ?
   const bool everything = !s.by_k && !s.by_p && s.min_p == 0., exact = everything || (s.by_p && !s.by_k);
   const int quota = s.by_k ? s.top_k < kQuota ? s.top_k : kQuota : 0;
   const Shares share = shares_of<W>(s.by_k ? s.top_k : 0);
-  const Wants want = {quota, quota > 0 ? raise_at(quota, true) : kListMost - 256, quota > 0 ? raise_at(quota, false) : kListMost - 256, s.k, s.temp,
+  const int full = kListMost - 256;
+  const Wants want = {quota, quota > 0 ? raise_at(quota, true) : full, quota > 0 ? raise_at(quota, false) : full, s.k, s.temp,
                       s.by_p && !s.by_k ? 1. - s.top_p : 0., s.by_k && s.by_p ? 0. : s.min_p, everything};
   float top, bound;
   first_bounds<T, W>(now, share, lds, top, bound);
@@ -1330,8 +1331,8 @@ __device__ __forceinline__ void top_from_memory(const T *z, const TopParams &p, 
 }
 
 template <class T, int W>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W == 2 ? 3 : 4))) void top_kernel(const T *logits, TopParams p,
-                                                                                         int32_t *later) {
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W == 2 ? 3 : 4)))
+void top_kernel(const T *logits, TopParams p, int32_t *later) {
   constexpr int THR = 64 * W;
   __shared__ RowLds<W> lds;
   __shared__ Softmax waves[W];
