@@ -236,35 +236,34 @@ __device__ __forceinline__ void write_bad(const SampleParams &p, int64_t row) {
   gmem(p.token)[row] = -1;
   gmem(p.logp)[row] = gmem(p.kept)[row] = __builtin_nanf("");
 }
-// Powers 2^(z k) relative to 2^R, R the whole number next to ref k, for logits that are not far above ref
-// (2^100 times its power); 2^-1010 at least: those below kNoPower are none.
+// Powers 2^((z - ref) k) for logits that are not far above ref (2^100 times its power); 2^-1010 at least: those
+// below kNoPower are none.
 //
-// z k and its fraction come from fused multiply-adds, whose products are exact: the error of a power relative
-// to another is that of k and of the polynomial.  Where |ref| k is past 2^40, logits that differ at all are
-// more than 2^16 octaves apart; a k that makes it 2^40 does no harm then, and keeps the sums exact.
+// The distance to ref is taken in fp64, first of all: powers and sums relative to references of any size are what
+// these are apart.  The product and its fraction come from fused multiply-adds, so the error of a power is that of k and of
+// the polynomial.
 constexpr double kNoPower = 0x1p-1000;
 struct Powers {
-  double k, shift, low;   // shift: 1.5 2^52 - R, so that z k + shift ends in the power's exponent
-  double unit;            // multiples of 1 / unit in histograms
-  __device__ __forceinline__ void refer_to(float ref, double full_k) {
-    k = full_k;
-    if (__builtin_fabs(ref * k) > 0x1p40) k = 0x1p40 / __builtin_fabs((double)ref);
-    const double R = __builtin_rint(ref * k);
-    shift = 0x1.8p52 - R;
-    low = ref - 1009. * (1.00001 * __builtin_amdgcn_rcp(k));   // (its power is between 2^-1010.1 and 2^-1008.9)
+  double k, ref, low;   // low: the least distance
+  double unit;          // multiples of 1 / unit in histograms
+  __device__ __forceinline__ void refer_to(float to, double to_k) {
+    k = to_k;
+    ref = to;
+    low = -1009. * (1.00001 * __builtin_amdgcn_rcp(k));   // (its power is between 2^-1010.1 and 2^-1008.9)
   }
   __device__ __forceinline__ double of(float z) const {
-    const double x = __builtin_fmax((double)z, low);
-    const double a = __builtin_fma(x, k, shift), f = __builtin_fma(x, k, shift - a);
+    constexpr double kWhole = 0x1.8p52;   // (a sum with it ends in a whole number, the power's exponent)
+    const double d = __builtin_fmax((double)z - ref, low);
+    const double a = __builtin_fma(d, k, kWhole), f = __builtin_fma(d, k, kWhole - a);
     const u64 p = __builtin_bit_cast(u64, pow2_fraction(f));
     const unsigned hi = (unsigned)(p >> 32) + ((unsigned)__builtin_bit_cast(u64, a) << 20);
     return __builtin_bit_cast(double, (u64)hi << 32 | (unsigned)p);
   }
   __device__ __forceinline__ u64 mass(float z) const { return (u64)(of(z) * unit + 0.5); }
-  // What powers relative to this have to be multiplied with to be relative to `to`.
-  __device__ __forceinline__ double scale_to(double to_shift) const {
-    const double n = to_shift - shift;   // R - R of `to`
-    return n < -1000. ? 0. : __builtin_amdgcn_ldexp(1., (int)__builtin_fmin(n, 1000.));
+  // What powers relative to `from`, a logit that is not above ref, have to be multiplied with to be relative to ref.
+  __device__ __forceinline__ double scale_from(float from) const {
+    const double x = of(from);
+    return x < kNoPower ? 0. : x;
   }
 };
 
@@ -343,8 +342,7 @@ constexpr float kFar = 100.f;                 // octaves
 // What a wave's stretch comes to.
 struct Stretch {
   float top;       // its largest logit (NaN: there is one)
-  float ref;       // the logit that powers followed (-inf: no logit)
-  double shift;    // Powers' of its sums (0: no logit)
+  float ref;       // the logit that its sums are relative to (-inf: no logit)
   double sum;      // of the powers of what is not in the list
   double listed;   // and of what is
   float raised;    // what quota raised the bound to (-FLT_MAX: it did not)
@@ -627,7 +625,7 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
   const float k32 = (float)want.k, far = (float)(kFar / want.k);
   // (the second part of k, above 0: the product of -inf with it is -inf, too)
   const float hi = CEIL ? k32 : __builtin_bit_cast(float, __builtin_bit_cast(unsigned, k32) - 1), lo = (float)(want.k - hi);
-  Stretch out = {-__builtin_inff(), -__builtin_inff(), 0., 0., 0., -__FLT_MAX__, -__FLT_MAX__, 0};
+  Stretch out = {-__builtin_inff(), -__builtin_inff(), 0., 0., -__FLT_MAX__, -__FLT_MAX__, 0};
   if (want.none) bound = __builtin_inff();
   float largest = -__builtin_inff();
   bool stop = false;
@@ -637,12 +635,9 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
   e.refer_to(ref > -__builtin_inff() ? ref : 0.f, want.k);
   double of_ref = e.of(ref);   // (powers in fp32 are relative to ref's own)
   const auto refer_to = [&](float to) {
-    const double from = e.shift;
     const bool none = ref == -__builtin_inff();
     e.refer_to(to, want.k);
-    Powers last = e;
-    last.shift = from;
-    const double scale = none ? 0. : last.scale_to(e.shift);
+    const double scale = none ? 0. : e.scale_from(ref);
     sum *= scale;
     part = none ? 0. : part * scale;
     if (turns) turns[lane] *= scale;
@@ -766,7 +761,6 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
   }
   out.top = wave_maximum(largest);
   out.ref = ref;
-  out.shift = ref == -__builtin_inff() ? 0. : e.shift;
   out.sum = wave_sum(sum);
   if (CEIL) out.sum /= of_ref;   // (relative to ref)
   if (!CEIL && out.n > 0) {
@@ -963,13 +957,14 @@ __device__ __forceinline__ void leave_stretch(const Stretch &mine, RowLds<W> &ld
   }
   __syncthreads();
 }
-// What the stretches come to together: every wave calls it, lane i has the i-th stretch's shift, sum and sum
-// with what is listed (lanes from W on: none).
+// What the stretches come to together: every wave calls it, lane i has the i-th stretch's reference, sum and
+// sum with what is listed (lanes from W on: none).
 struct Together {
   float top;
   bool fits;
   int listed;
-  double shift, sum, all;
+  float ref;
+  double sum, all;
 };
 template <int W>
 __device__ __forceinline__ Together together(const RowLds<W> &lds) {
@@ -980,7 +975,7 @@ __device__ __forceinline__ Together together(const RowLds<W> &lds) {
   t.top = wave_maximum(in ? x.top : -__builtin_inff());
   t.fits = __ballot(in && x.n > kListMost) == 0;
   t.listed = (int)wave_reduce(in ? (unsigned)x.n : 0u, 0u, [](unsigned a, unsigned b) { return a + b; });
-  t.shift = in ? x.shift : 0.;
+  t.ref = in ? x.ref : -__builtin_inff();
   t.sum = in ? x.sum : 0.;
   t.all = in ? x.sum + x.listed : 0.;
   return t;
@@ -1088,10 +1083,7 @@ void sample_kernel(const T *logits, SampleParams p, int32_t *later) {
   Powers e;
   e.refer_to(top, s.k);
   e.unit = __builtin_amdgcn_ldexp(1., p.mass_bits);
-  // (a stretch's powers to the row's; without logits it has none)
-  Powers own = e;
-  own.shift = row_of.shift;
-  const double relative = row_of.shift == 0. ? 0. : own.scale_to(e.shift);
+  const double relative = e.scale_from(row_of.ref);   // (a stretch's powers to the row's; 0 without logits)
   const double part_of_all = row_of.all * relative, all = wave_sum(part_of_all);
   if (everything) {
     if (w > 0) return;
