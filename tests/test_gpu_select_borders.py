@@ -1,5 +1,5 @@
 """Where himuon_sample's borders hang on more than ordinary rows show (MI355X only): logits so large that
-their powers have no common scale."""
+their powers have no common scale, and equal logits with borders that fall between two of them exactly."""
 import pytest
 import torch
 
@@ -10,6 +10,7 @@ hm = pytest.importorskip("tiled_newton_schulz_tile_amd")
 from tiled_newton_schulz_tile_amd.sampling import sample  # noqa: E402
 
 DEV = "cuda"
+INF = float("inf")
 # rows and tokens (fp32) for every number of waves a row, where the sweep's stretches have more than one turn
 SIZES = [(3, 40003), (300, 9001), (1100, 9001), (2100, 9001), (4200, 9001)]
 
@@ -42,3 +43,31 @@ def test_two_huge_logits(N, V, least, most, T, dtype):
         some = some_of(N)
         assert check_sample(logits[some], uniform[some], [x[some] for x in got], **kw) == len(some)
         assert (got.token >= V - 700).all()
+
+
+@pytest.mark.parametrize("N,V", [(3, 40960), (300, 9216), (1100, 9216), (2100, 9216), (4200, 9216), (4200, 512), (300, 512)])
+@pytest.mark.parametrize("value,T", [(0.0, 1.0), (3.671875, 0.3), (-1e30, 1.0), (17.5, 1e4)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_equal_logits_part_exactly(N, V, value, T, dtype):
+    """Of n equal logits, every sum of powers is a whole number: top_p keeps its share of them to the token, and a
+    uniform on a border takes the token behind it.  A second row in four has masked tokens of no probability (-inf), a
+    third one of so little (1e-130) that they do not move a sum in 64 bits, behind the equal ones."""
+    _need_gpu()
+    logits = torch.full((N, V), value, dtype=dtype, device=DEV)
+    half = V // 2
+    logits[1::4, :half] = -INF
+    if value > -1e29:
+        logits[2::4, half:] = value - 300 * T
+    first, count = torch.zeros(N, dtype=torch.int64), torch.full((N,), V)
+    first[1::4] = count[1::4] = half
+    if value > -1e29:
+        count[2::4] = half
+    uniform = (torch.arange(N) * 37 % 128).float() / 128
+    for kw, share in ((dict(), 1.0), (dict(top_p=0.5), 0.5), (dict(top_p=0.75), 0.75), (dict(top_k=half), None),
+                      (dict(top_k=V // 4, top_p=0.5), None), (dict(min_p=1.0), 1.0), (dict(top_p=0.25, min_p=0.9), 0.25)):
+        n = (count * share).long() if share else torch.full((N,), half if len(kw) == 1 else V // 8)
+        got = sample(logits, uniform.to(DEV), temperature=T, **kw)
+        want = first + (uniform.double() * n).long()
+        assert torch.equal(got.token.cpu(), want), (kw, (got.token.cpu() != want).nonzero()[:3])
+        assert torch.equal(got.kept.cpu(), (n.double() / count).float()), kw
+        assert ((got.logp.cpu().double() + count.double().log()).abs() <= 2.0 ** -23 * count.double().log()).all()

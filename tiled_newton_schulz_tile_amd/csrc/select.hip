@@ -240,8 +240,9 @@ __device__ __forceinline__ void write_bad(const SampleParams &p, int64_t row) {
 // below kNoPower are none.
 //
 // The distance to ref is taken in fp64, first of all: powers and sums relative to references of any size are what
-// these are apart.  The product and its fraction come from fused multiply-adds, so the error of a power is that of k and of
-// the polynomial.
+// these are apart.  The product and its fraction come from fused multiply-adds, so the error of a power is that of k
+// and of the polynomial.  ref's own power is 1 exactly, and sums over logits that equal it are whole numbers: a border
+// that falls between two of them does so here.
 constexpr double kNoPower = 0x1p-1000;
 struct Powers {
   double k, ref, low;   // low: the least distance
@@ -267,11 +268,11 @@ struct Powers {
   }
 };
 
-// top: the row's largest logit; all, kept: sums of powers.
-__device__ __forceinline__ void write_token(const SampleParams &p, int64_t row, const Settings &s, const Powers &e, int token,
-                                            float logit, float top, double all, double kept) {
+// top: the row's largest logit; all, kept: sums of powers relative to it.
+__device__ __forceinline__ void write_token(const SampleParams &p, int64_t row, const Settings &s, int token, float logit,
+                                            float top, double all, double kept) {
   gmem(p.token)[row] = token;
-  gmem(p.logp)[row] = s.greedy ? 0.f : (float)(((double)logit - top) * (s.k * 0.69314718055994530942) - log(all / e.of(top)));
+  gmem(p.logp)[row] = s.greedy ? 0.f : (float)(((double)logit - top) * (s.k * 0.69314718055994530942) - log(all));
   gmem(p.kept)[row] = s.greedy ? 1.f : (float)(kept / all);
 }
 
@@ -633,7 +634,6 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
   Powers e;
   e.unit = 1.;
   e.refer_to(ref > -__builtin_inff() ? ref : 0.f, want.k);
-  double of_ref = e.of(ref);   // (powers in fp32 are relative to ref's own)
   const auto refer_to = [&](float to) {
     const bool none = ref == -__builtin_inff();
     e.refer_to(to, want.k);
@@ -642,7 +642,6 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
     part = none ? 0. : part * scale;
     if (turns) turns[lane] *= scale;
     ref = to;
-    of_ref = e.of(ref);
   };
   const auto logit_at = [&](int j) { return logit_of<T>(list[j]); };
   // An element is looked at more closely from here on: it belongs to the list, or the powers' reference has to
@@ -686,7 +685,7 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
       for (int d = 1; d < N; d *= 2)
 #pragma unroll
         for (int j = 0; j < N; j += 2 * d) x[j] += x[j + d];
-      part += (double)x[0] * of_ref;
+      part += (double)x[0];
     }
   };
   if (turns) turns[lane] = 0.;
@@ -729,7 +728,7 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
       } else {
         double all = sum;
         for (int j = lane; j < out.n; j += 64) all += e.of(logit_at(j));
-        b = bound_of(want, wave_maximum(largest), ref, wave_sum(all) / e.of(ref), V);
+        b = bound_of(want, wave_maximum(largest), ref, wave_sum(all), V);
       }
       b = __builtin_fmaxf(bound, b);
       if (!raise) {
@@ -762,7 +761,6 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
   out.top = wave_maximum(largest);
   out.ref = ref;
   out.sum = wave_sum(sum);
-  if (CEIL) out.sum /= of_ref;   // (relative to ref)
   if (!CEIL && out.n > 0) {
     wave_sync();
     double all = 0;
@@ -830,7 +828,7 @@ __device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s
   if (s.by_p)
     border = find_border_in_row<T, THR, false>(z, V, first_key<T>(top), border, [&](float x) { return e.mass(x); },
                                                [&](u64 total) { return target_of_p(s, e, total, all); }, lds);
-  const Kept<T> kept = {border, __builtin_fmax(s.min_p * e.of(top), kNoPower)};
+  const Kept<T> kept = {border, __builtin_fmax(s.min_p, kNoPower)};
   const float edge = logit_of<T>(border);   // (of the last token that is kept)
   const auto weigh = [&](int vec, const float (&x)[N]) {
     bool any = false;
@@ -864,7 +862,7 @@ __device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s
   const int n = N < V - v * N ? N : V - v * N;
   const float mine = Vec<T>::load1(z + (lane < n ? v * N + lane : V - 1));
   const int i = find_part(n, target - before - more, [&](int j) { return kept.power(e, v * N + j, mine); }, last);
-  if (lane == i) write_token(p, row, s, e, v * N + i, mine, top, all, total);
+  if (lane == i) write_token(p, row, s, v * N + i, mine, top, all, total);
 }
 
 // Whether a block of W waves itself goes through its row again where its lists do not hold what is asked for.  Others
@@ -1118,11 +1116,11 @@ void sample_kernel(const T *logits, SampleParams p, int32_t *later) {
     const int n = N < V - v * N ? N : V - v * N;
     const float x = Vec<T>::load1(z + (lane < n ? v * N + lane : V - 1));
     const int i = find_part(n, seen_left, [&](int) { return kept.power(e, 0, x); }, last);
-    if (lane == i) write_token(p, row, s, e, v * N + i, x, top, all, all);
+    if (lane == i) write_token(p, row, s, v * N + i, x, top, all, all);
     return;
   }
   int n = 0;
-  bound = bound_of(want, top, top, all / e.of(top), V);
+  bound = bound_of(want, top, top, all, V);
   if (fits) {
     if (quota > 0 && share.ranks <= W) bound = __builtin_fmaxf(bound, nth_bound<W>(lds.last_bound, share.ranks));
     n = join_lists<T>(lds, bound);
@@ -1172,14 +1170,14 @@ void sample_kernel(const T *logits, SampleParams p, int32_t *later) {
         border = find_border<false>(list, n, first, border, [&](u64 r) { return e.mass(logit_of<T>(r)); },
                                     [&](u64 total) { return target_of_p(s, e, total, all); }, lds.wave);
     }
-    const Kept<T> kept = {border, __builtin_fmax(s.min_p * e.of(top), kNoPower)};
+    const Kept<T> kept = {border, __builtin_fmax(s.min_p, kNoPower)};
     const auto power = [&](int j) { return kept.power(e, index_of(list[j]), logit_of<T>(list[j])); };
     double t = 0;
     for (int j = lane; j < n; j += 64) t += power(j);
     const double total = wave_sum(t);
     double before;
     const int j = find_part(n, uniform_of(p, row) * total, power, before);
-    if (lane == 0) write_token(p, row, s, e, index_of(list[j]), logit_of<T>(list[j]), top, all, total);
+    if (lane == 0) write_token(p, row, s, index_of(list[j]), logit_of<T>(list[j]), top, all, total);
     return;
   }
   if constexpr (again(W)) {
@@ -1191,7 +1189,7 @@ void sample_kernel(const T *logits, SampleParams p, int32_t *later) {
         if (threadIdx.x == 0) write_bad(p, row);
         return;
       }
-      bound = bound_of(want, top, top, sum / e.of(top), V);
+      bound = bound_of(want, top, top, sum, V);
     }
     sample_from_memory<T, 64 * W>(z, s, row, p, e, top, sum, bound, lds.block, &lds.chunk[0][0]);
   } else {
