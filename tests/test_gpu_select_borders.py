@@ -1,5 +1,9 @@
 """Where himuon_sample's borders hang on more than ordinary rows show (MI355X only): logits so large that
-their powers have no common scale, and equal logits with borders that fall between two of them exactly."""
+their powers have no common scale, equal logits with borders that fall between two of them exactly, and min_p
+near one."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
@@ -71,3 +75,39 @@ def test_equal_logits_part_exactly(N, V, value, T, dtype):
         assert torch.equal(got.token.cpu(), want), (kw, (got.token.cpu() != want).nonzero()[:3])
         assert torch.equal(got.kept.cpu(), (n.double() / count).float()), kw
         assert ((got.logp.cpu().double() + count.double().log()).abs() <= 2.0 ** -23 * count.double().log()).all()
+
+
+@pytest.mark.parametrize("N,V", [(3, 100003), (3, 600), (300, 600), (4200, 600)])
+@pytest.mark.parametrize("scale,min_p,T", [(1e-8, 0.99999999, 1.0), (2.5, 0.999992, 2.0 ** 20), (2.5, 1 - 1e-7, 2.0 ** 20),
+                                           (2.5, 0.9999, 1e5), (1.0, 0.999, 2.0 ** -20), (1.0, 0.999, 1.0)])
+def test_min_p_near_one(N, V, scale, min_p, T):
+    """Edges a small part of T below a largest logit of 0 or near it."""
+    _need_gpu()
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn(N, V, generator=g) * scale
+    z = torch.where(torch.arange(N)[:, None] % 2 == 0, z - z.amax(1, keepdim=True), z)
+    logits, uniform = z.to(DEV), torch.rand(N, generator=g).to(DEV)
+    got = sample(logits, uniform, temperature=T, min_p=min_p)
+    some = some_of(N)
+    assert check_sample(logits[some], uniform[some], [x[some] for x in got], temperature=T, min_p=min_p) == len(some)
+
+
+@pytest.mark.parametrize("N", [1, 300, 4200])
+@pytest.mark.parametrize("T", [2.0 ** -20, 1.0, 700.0, 2.0 ** 20])
+def test_min_p_keeps_the_logit_at_its_edge(N, T):
+    """The first fp32 number from T log(min_p) on is kept and the one below it is not, also with top_k."""
+    _need_gpu()
+    for min_p in (1 - 2.9e-8, 1 - 1e-6, 0.999, 0.9, 0.5, 0.3, 1e-3):
+        edge = T * math.log(min_p)
+        on = np.float32(edge)
+        on = on if float(on) >= edge else np.nextafter(on, np.float32(0))
+        below = np.nextafter(on, np.float32(-np.inf))
+        z = torch.full((N, 500), -60 * T)
+        z[:, 7], z[:, 100], z[:, 300] = 0.0, float(below), float(on)
+        logits, uniform = z.to(DEV), torch.full((N,), 0.9, device=DEV)
+        for more in (dict(), dict(top_k=40)):
+            got = sample(logits, uniform, temperature=T, min_p=min_p, **more)
+            p, q = math.exp(float(on) / T), math.exp(float(below) / T)
+            token = 7 if float(np.float32(0.9)) * (1 + p) < 1 else 300   # (the first one's power is 1)
+            assert (got.token == token).all(), (min_p, more)
+            assert ((got.kept.double() - (1 + p) / (1 + p + q)).abs() <= 2.0 ** -21).all(), (min_p, more)

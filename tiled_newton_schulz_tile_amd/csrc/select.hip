@@ -360,12 +360,14 @@ struct Wants {
   double share_m;        // 0, or: all tokens with at least this share of the largest's probability
   bool none;             // nothing
 };
-// The bound that comes from the largest logit top, and from what all powers relative to ref sum to at least
-// (with room for errors of 1e-5 of its terms: its logarithms are fp32).
+// The bound that comes from the largest logit top, and from what all powers relative to ref sum to at least.  Below
+// what the formulas give: the share and its logarithm are fp32, which is 2^-22 of a temperature together where the share
+// is near 1 and its logarithm near 0, and 2^-22 of the step elsewhere; sums and products are off by 2^-23 of their terms.
 __device__ __forceinline__ float bound_of(const Wants &want, float top, float ref, double sum, int V) {
   const auto below = [&](float from, double share) {
-    const float step = (float)want.temp * kLn2 * __builtin_amdgcn_logf((float)share);   // (negative)
-    return __builtin_fmaxf(from + step - 1e-5f * (__builtin_fabsf(from) + __builtin_fabsf(step)), -__FLT_MAX__);
+    const float temp = (float)want.temp, step = temp * kLn2 * __builtin_amdgcn_logf((float)share);   // (negative)
+    const float room = 1e-5f * (__builtin_fabsf(from) + __builtin_fabsf(step)) + 0x1p-20f * temp;
+    return __builtin_fmaxf(from + step - room, -__FLT_MAX__);
   };
   float b = -__FLT_MAX__;
   if (want.share_p > 0.) b = __builtin_fmaxf(b, below(ref, __builtin_fmin(want.share_p * sum / V, 1e30)));
