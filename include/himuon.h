@@ -346,10 +346,11 @@ HIMUON_API himuon_status himuon_policy_loss(const himuon_policy *p, void *worksp
      logp = log of the token's probability under softmax(logits / T), filters aside: old_logp of
             himuon_policy_loss with that temperature,
      kept = the probability that all kept tokens have there.
-   T = 0 takes the first of the largest logits (logp 0, kept 1).  Tokens of -inf are never taken; a
-   row with NaN or +inf among its logits or with nothing but -inf, and a row_temperature that is
-   neither 0 nor in [2^-20, 2^20], give token -1 and NaN.  Borders are decided as 64-bit sums of the
-   formulas above decide them. */
+   T = 0 takes the first of the largest logits (logp 0, kept 1).  Tokens of -inf are never taken (and
+   a uniform of 0 passes over tokens with e_i below 2^-1000, and may from 2^-960 down); a row with
+   NaN or +inf among its logits or with nothing but -inf, and a row_temperature that is neither 0
+   nor in [2^-20, 2^20], give token -1 and NaN.  Borders are decided as 64-bit sums of the formulas
+   above decide them. */
 typedef struct {
   int64_t rows, vocab;           /* >= 0, in [1, HIMUON_TOP_VOCAB]                      */
   int64_t ld_logits;             /* leading dimension in elements, >= vocab             */

@@ -1,6 +1,6 @@
 """Where himuon_sample's borders hang on more than ordinary rows show (MI355X only): logits so large that
-their powers have no common scale, equal logits with borders that fall between two of them exactly, and min_p
-near one."""
+their powers have no common scale, equal logits with borders that fall between two of them exactly, min_p near
+one, and tokens too improbable to be taken."""
 import math
 
 import numpy as np
@@ -111,3 +111,19 @@ def test_min_p_keeps_the_logit_at_its_edge(N, T):
             token = 7 if float(np.float32(0.9)) * (1 + p) < 1 else 300   # (the first one's power is 1)
             assert (got.token == token).all(), (min_p, more)
             assert ((got.kept.double() - (1 + p) / (1 + p + q)).abs() <= 2.0 ** -21).all(), (min_p, more)
+
+
+@pytest.mark.parametrize("N,V", [(3, 40003), (2100, 9001), (4200, 9001)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_uniform_of_zero_takes_a_token_that_can_be_taken(N, V, dtype):
+    """Not one of -inf, nor one of about 2^-1000 of the largest's probability, also where such ones are all that a wave
+    reads at first."""
+    _need_gpu()
+    for far in (-700.0, -720.0, -740.0, -5000.0):
+        logits = torch.full((N, V), far, dtype=dtype, device=DEV)
+        logits[:, 0] = -INF
+        logits[:, V - 300:] = 0.0
+        logits[1::2, 5] = far + 12
+        got = sample(logits, torch.zeros(N, device=DEV))
+        assert (got.token == V - 300).all(), far
+        assert ((got.logp + math.log(300)).abs() <= 2.0 ** -20).all() and (got.kept == 1).all()

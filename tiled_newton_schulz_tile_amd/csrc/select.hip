@@ -1087,14 +1087,17 @@ void sample_kernel(const T *logits, SampleParams p, int32_t *later) {
   const double part_of_all = row_of.all * relative, all = wave_sum(part_of_all);
   if (everything) {
     if (w > 0) return;
-    // what each stretch weighs, then the turns of one, the vectors of one turn, the elements of one vector
+    // what each stretch weighs, then the turns of one, the vectors of one turn, the elements of one vector.  A stretch
+    // (64 turns) or turn (2^11 elements) that weighs too little to be sure of a turn or an element with a power is none
+    const auto some = [](double w, double least) { return w < least ? 0. : w; };
     const Kept<T> kept = {~(u64)0, kNoPower};
     const double target = uniform_of(p, row) * all;
     double before, more, last;
-    const int in = find_part(W, target, [&](int) { return part_of_all; }, before);
+    const int in = find_part(W, target, [&](int) { return some(part_of_all, 0x1p-970); }, before);
     const double scale = from_lane(relative, in);
     const int s0 = stretch_turn(turns, in, W), s1 = stretch_turn(turns, in + 1, W);
-    const int turn = s0 + find_part(s1 - s0, target - before, [&](int i) { return lds.turns[in][i] * scale; }, more);
+    const int turn =
+        s0 + find_part(s1 - s0, target - before, [&](int i) { return some(lds.turns[in][i] * scale, 0x1p-980); }, more);
     now.load(z, turn, V);
     double left = target - before - more, seen_left = 0;
     int v = -1, seen = 0;
