@@ -40,7 +40,7 @@ constexpr int kNone = -1;   // an entry that does not count
 // A row's entries in LDS, what they sum to, and the bitmap of the tokens that they name: a byte for
 // each vector of the row, at the place that marks() gives it.
 struct EntrySums {
-  unsigned named_max, teacher_max;   // ordered bits of the largest logits; 0: none
+  unsigned named_max, teacher_max;   // ordered bits of the entries' largest logits; 0: none
   int twice;                         // not 0: some token is named more than once
   double named[16], teacher[16];     // sums of powers, by wave
 };
@@ -63,10 +63,17 @@ __device__ __forceinline__ unsigned ordered(float x) {
   const unsigned u = __builtin_bit_cast(unsigned, x);
   return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float of_ordered(unsigned o) {
+  return __builtin_bit_cast(float, o ^ (o >> 31 ? 0x80000000u : 0xffffffffu));
+}
 // The reference of a softmax from its largest logit's ordered bits (0 where there is none or it is
 // -inf, whose powers are 0 then).
-__device__ __forceinline__ float ordered_ref(unsigned o) {
-  return o == 0 ? 0.f : ref_of(__builtin_bit_cast(float, o ^ (o >> 31 ? 0x80000000u : 0xffffffffu)));
+__device__ __forceinline__ float ordered_ref(unsigned o) { return o == 0 ? 0.f : ref_of(of_ordered(o)); }
+// The teacher's, from its entries and its rest times the temperature.  That is fp64: its fp32 value may be thousands
+// of octaves away, and beyond fp32's range.  (A NaN is in the sums.)
+__device__ __forceinline__ double teacher_ref_of(unsigned o, double teacher_rest) {
+  const double m = __builtin_fmax(o == 0 ? -__builtin_inf() : (double)of_ordered(o), teacher_rest);
+  return m == -__builtin_inf() ? 0. : m;
 }
 
 // Marks element e of the vector whose byte is at `at`; one that is marked already is named twice.
@@ -118,7 +125,8 @@ __device__ __forceinline__ float uniform(float x) {
 // What a row's gradient and divergence need, the same in every thread.
 struct RowCoefs {
   bool live;                         // the teacher has some probability
-  float named_ref, teacher_ref;      // of the entries' powers, and what these are multiplied with to be
+  float named_ref;                   // of the entries' powers,
+  double teacher_ref;                //   of the teacher's, and what these are multiplied with to be
   double named_f, teacher_f;         //   probabilities
   float ref;                         // the student's softmax over all tokens: the largest logit
   double sum, teacher_sum;           //   and the sum; the teacher's sum
@@ -126,7 +134,7 @@ struct RowCoefs {
   float coef;                        // of the row's gradient
   float q_rest;
 };
-__device__ __forceinline__ double power(double z, float ref, const DistillParams &p) {
+__device__ __forceinline__ double power(double z, double ref, const DistillParams &p) {
   return pow2_exact((z - ref) * p.fine_k);
 }
 
@@ -142,7 +150,7 @@ __device__ __forceinline__ RowCoefs row_coefs(Softmax rest, const EntrySums &sum
   }
   r.live = !(teacher == 0);
   r.named_ref = ordered_ref(sums.named_max);
-  r.teacher_ref = ordered_ref(sums.teacher_max);
+  r.teacher_ref = teacher_ref_of(sums.teacher_max, teacher_rest);
   r.rest_ref = ref_of(rest.ref);
   const float named_max = named == 0 ? -__builtin_inff() : r.named_ref;
   r.ref = ref_of(__builtin_fmaxf(rest.ref, named_max));
@@ -169,7 +177,7 @@ __device__ __forceinline__ float row_kl(const EntryLds &e, const RowCoefs &r, So
   for (int j = threadIdx.x & 63; j < p.entries; j += 64) {
     if (e.token[j] == kNone) continue;
     const double q = power(e.t[j], r.teacher_ref, p) * r.teacher_f;
-    if (q != 0) kl += q * ((((double)e.t[j] - r.teacher_ref) - ((double)e.z[j] - r.ref)) * p.inv_temp + shift);
+    if (q != 0) kl += q * (((e.t[j] - r.teacher_ref) - ((double)e.z[j] - r.ref)) * p.inv_temp + shift);
   }
   kl = wave_sum(kl);
   if (!(r.q_rest <= 0.f)) {
@@ -306,7 +314,6 @@ __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dl
       else if (vec < HELD) mark(e.marks, vec % THR * K + vec / THR, (int)token % N, sums);
       else mark(e.marks, HELD + (((int)token - HELD * N) >> 3), ((int)token - HELD * N) & 7, sums);
     }
-    if (tid == 0 && teacher_rest != -__builtin_inf()) top[1] = max(top[1], ordered((float)teacher_rest));
     top[0] = wave_max(top[0]);
     top[1] = wave_max(top[1]);
     if ((tid & 63) == 0) {
@@ -317,7 +324,8 @@ __global__ __launch_bounds__(THR) void distill_row_kernel(const T *logits, T *dl
   lds_barrier();
   const bool twice = sums.twice != 0;
   if (wave < waves) {
-    const float named_ref = ordered_ref(sums.named_max), teacher_ref = ordered_ref(sums.teacher_max);
+    const float named_ref = ordered_ref(sums.named_max);
+    const double teacher_ref = teacher_ref_of(sums.teacher_max, teacher_rest);
     double named = 0, teacher = tid == 0 ? power(teacher_rest, teacher_ref, p) : 0;
     for (int j = tid; j < p.entries; j += THR) {
       if (e.token[j] == kNone) continue;
@@ -550,7 +558,6 @@ __global__ __launch_bounds__(kSpanThreads) void distill_span_finish_kernel(const
         top[1] = max(top[1], ordered(e.t[j]));
         if (x[1] == 0.f) sums.twice = 1;
       }
-      if (tid == 0 && teacher_rest != -__builtin_inf()) top[1] = max(top[1], ordered((float)teacher_rest));
       top[0] = wave_max(top[0]);
       top[1] = wave_max(top[1]);
       if (lane == 0) {
@@ -568,7 +575,8 @@ __global__ __launch_bounds__(kSpanThreads) void distill_span_finish_kernel(const
       rest.sum = wave_sum(rest.sum * pow2(rest.ref, p.k, ref_of(m)));
       rest.ref = m;
       lds_barrier();
-      const float named_ref = ordered_ref(sums.named_max), teacher_ref = ordered_ref(sums.teacher_max);
+      const float named_ref = ordered_ref(sums.named_max);
+      const double teacher_ref = teacher_ref_of(sums.teacher_max, teacher_rest);
       const bool twice = sums.twice != 0;
       double named = 0, teacher = tid == 0 ? power(teacher_rest, teacher_ref, p) : 0;
       for (int j = tid; j < p.entries; j += THR) {
