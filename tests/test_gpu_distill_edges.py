@@ -55,3 +55,23 @@ def test_a_rest_alone(N, V, rest, temperature, dtype):
     size = (p + p / p_rest) / temperature
     error = np.abs(got.dlogits.double().cpu().numpy() - grad)[:live]
     assert (error <= 2 * tol * size + half * np.abs(grad[:live]) + 1e-37).all()
+
+
+@pytest.mark.parametrize("N,V", SIZES)
+@pytest.mark.parametrize("below", [60.0, 110.0, 600.0])
+def test_a_small_rest_where_the_student_has_none(N, V, below):
+    """A rest of any probability that is a number in 64 bits has an infinite divergence from a student without one, as a
+    named token has; the gradient is finite.  One of no probability has none."""
+    _need_gpu()
+    logits, value, index, weight, r = make(N, V, 12, torch.float32, 9, masked=0.0)
+    named = torch.zeros(N, V, dtype=torch.bool, device="cuda").scatter_(1, index, True)
+    logits.masked_fill_(~named, -INF)
+    value[:, 11] = value[:, 0] - below
+    r[:] = value[:, 0] - below
+    r[2] = -INF
+    for grad in (True, False):
+        got = distill_loss(logits, value, index, weight, rest=r, dlogits=grad)
+        assert (got.kl[:2] == INF).all() and torch.isfinite(got.kl[2])
+        assert (got.kl[3:] == INF).all() and (not grad or torch.isfinite(got.dlogits).all())
+    logits[0, index[0, 11]], r[0] = -INF, -INF    # (the named one)
+    assert distill_loss(logits, value, index, weight, rest=r).kl[0] == INF

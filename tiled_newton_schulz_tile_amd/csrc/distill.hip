@@ -132,7 +132,7 @@ struct RowCoefs {
   double sum, teacher_sum;           //   and the sum; the teacher's sum
   float rest_ref, rest_f;            // a token u of the rest: gradient rest_f 2^((z_u - rest_ref) k)
   float coef;                        // of the row's gradient
-  float q_rest;
+  bool rest_counts;                  // the teacher's rest has some probability
 };
 __device__ __forceinline__ double power(double z, double ref, const DistillParams &p) {
   return pow2_exact((z - ref) * p.fine_k);
@@ -160,11 +160,12 @@ __device__ __forceinline__ RowCoefs row_coefs(Softmax rest, const EntrySums &sum
   r.named_f = named_scale * inv;
   r.teacher_sum = teacher;
   r.teacher_f = 1. / teacher;
-  r.q_rest = (float)(power(teacher_rest, r.teacher_ref, p) * r.teacher_f);
+  const double q_rest = power(teacher_rest, r.teacher_ref, p) * r.teacher_f;
+  r.rest_counts = !(q_rest <= 0);   // (NaN does)
   r.coef = weight * p.coef * (teacher == teacher ? 1.f : (float)teacher);
   float f = (float)(rest_scale * inv);
   // (a rest of probability 0 has a gradient of 0 and an infinite divergence)
-  if (!(r.q_rest <= 0.f)) f -= rest.sum > 0.f ? r.q_rest / rest.sum : 0.f;
+  if (r.rest_counts) f -= rest.sum > 0.f ? (float)q_rest / rest.sum : 0.f;
   r.rest_f = r.coef * f;
   return r;
 }
@@ -180,7 +181,7 @@ __device__ __forceinline__ float row_kl(const EntryLds &e, const RowCoefs &r, So
     if (q != 0) kl += q * (((e.t[j] - r.teacher_ref) - ((double)e.z[j] - r.ref)) * p.inv_temp + shift);
   }
   kl = wave_sum(kl);
-  if (!(r.q_rest <= 0.f)) {
+  if (r.rest_counts) {
     const double q = power(teacher_rest, r.teacher_ref, p) * r.teacher_f;
     kl += q * (((teacher_rest - r.teacher_ref) - ((double)rest.ref - r.ref)) * p.inv_temp + shift - log((double)rest.sum));
   }
