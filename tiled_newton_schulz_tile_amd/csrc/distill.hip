@@ -53,7 +53,7 @@ __device__ __forceinline__ EntryLds entry_lds(u32x4 *lds, size_t mark_bytes, int
   float *f = reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + mark_bytes);
   return {reinterpret_cast<int *>(f), f + entries, f + 2 * entries, f + 3 * entries, reinterpret_cast<unsigned char *>(lds)};
 }
-size_t entry_lds_bytes(size_t mark_bytes, int entries) { return mark_bytes + 16 * (size_t)entries; }
+constexpr size_t entry_lds_bytes(size_t mark_bytes, int entries) { return mark_bytes + 16 * (size_t)entries; }
 
 __device__ __forceinline__ float entry_value(const DistillParams &p, int64_t at) {
   return p.value_bf16 ? bf16_bits_to_f32(gmem(reinterpret_cast<const unsigned short *>(p.value))[at])
@@ -243,6 +243,13 @@ __host__ __device__ constexpr int tail_marks_of(int64_t vecs, int n, int held) {
 __host__ __device__ constexpr size_t row_mark_bytes(int64_t vecs, int n, int held) {
   return ((size_t)tail_marks_of(vecs, n, held) + 8 + 15) / 16 * 16;
 }
+// The largest launch fits a CU's LDS: rows of the most tokens in fp32, held by 1024 threads with 16 vectors each or not
+// held at all, with the most entries.
+constexpr size_t largest_lds(int held) {
+  return entry_lds_bytes(row_mark_bytes(HIMUON_TOP_VOCAB / Vec<float>::N, Vec<float>::N, held), HIMUON_TOP_MOST) +
+         sizeof(EntrySums) + 16 * (sizeof(RowCoefs) + sizeof(Softmax));
+}
+static_assert(largest_lds(0) <= 160 << 10 && largest_lds(1024 * 16) <= 160 << 10, "LDS of the largest rows");
 template <class T, int HELD>
 __device__ __forceinline__ unsigned long_marks(const unsigned char *marks, int vec) {
   const int bit = (vec - HELD) * Vec<T>::N;
