@@ -867,10 +867,13 @@ __device__ __forceinline__ void sample_from_memory(const T *z, const Settings &s
   if (lane == i) write_token(p, row, s, v * N + i, mine, top, all, total);
 }
 
-// Whether a block of W waves itself goes through its row again where its lists do not hold what is asked for.  Others
-// leave it to a second launch, which costs every call some microseconds (bf16: one row of 32000 24.7 us, 29.0 with two
-// launches; 2000 x 32000, top_p 88 us, 100), but blocks of 16 waves: where one row of 4096 x 32000 is flat, top_k is 240
-// us, and 361 where its one wave goes on with it.
+// Whether a block of W waves reads its row again itself where the row's lists do not hold what is asked for.  The
+// alternative is a second launch, in blocks of 16 waves, that finds the rows that the first one marked; every call pays
+// for it, with such a row or without.
+//   Blocks of 4 waves on read again: 1 x 32000 bf16, top_k 23.0 us, and 29.9 with a second launch; 2000 x 32000, top_p 82
+//   and 99.
+//   Blocks of 1 and 2 waves leave it to the second launch, since one wave takes long over a row: 4096 x 32000, top_k with
+//   one flat row 227 us, and 321 where its wave reads again (without a flat row 133 and 115).
 constexpr bool again(int W) { return W >= 4; }
 
 template <int W>
@@ -1431,14 +1434,22 @@ __global__ __launch_bounds__(kLaterThreads) void top_later_kernel(const T *logit
 
 constexpr int64_t kLaunchRows = (int64_t)1 << 21;   // a grid holds fewer than 2^32 threads
 
-// Waves for a row: enough of them to fill the chip (256 CUs with 16 each; with half of that 1024 x 128256 bf16 draws take
-// 146 us and not 121, with twice that the top 100 of 1023 x 50257 fp32 147 us and not 87), and as many as its stretches'
-// lengths ask for.  A block of 16 waves has a CU for itself, so 16 only where all blocks run at once (500 x 50257 fp32,
-// top_p: 45.8 us with 8, 56.9 with 16).
+// Waves for a row: enough of them to fill the chip (256 CUs with 16 each: draws of 1024 x 128256 bf16 take 115 us with 4
+// waves a row, 122 with 2 and 180 with 1; the top 100 of 1023 x 50257 fp32 82 us with 8, 89 with 4 and 127 with 16), and as
+// many as its stretches' lengths ask for.  A block of 16 waves has a CU for itself, so 16 only where all blocks run at once
+// (500 x 50257 fp32, top_p: 44.5 us with 8, 52.6 with 16).
 constexpr int kFillWaves = 4096;
-// The k up to which W waves take a row: the joined list of 4 has room for little more than 640 (top 700 of 4096 x
-// 128256 bf16 1532 us with 4 waves, 1028 with 8), two lists are little for more than one holds (top 440 1404 us with 2
-// waves, 682 with 4), and one wave sorts up to 256 keys well (top 224 864 us with one, top 225 579 with 4).
+// The k up to which W waves take a row.  Top k of 4096 rows, us:
+//                            k =    64   150   180   216   224   300   440   640   700  1024
+//   128256 bf16 tokens, 1 wave     295   367   580   522   697  1528  1578  1689  1708  1800
+//                       2 waves    416   520   558   626   641   710  1148  1704  1721  1814
+//                       4 waves    376   470   494   560   574   641   682  1024  1723  1483
+//                       8 waves    387   441   469   514   513   650   802   943  1022  1126
+//   50257 fp32 tokens,  1 wave     220   283         343         804         902         929
+//                       4 waves    264   350         424         506         771         742
+//                       8 waves    281   323         373         482         769         917
+// One wave leads up to 150 and with fp32 to 216 (in between it depends on how often its list's bound is raised); 4 waves
+// follow as long as their joined list of 1024 keys has room, which ends between 640 and 700.
 constexpr int most_of(int W) { return W >= 8 ? HIMUON_TOP_MOST : W == 4 ? 640 : 216; }
 int waves_of(int64_t rows, int64_t vecs, int least) {
   const int64_t turns = (vecs + kTurn - 1) / kTurn;
@@ -1459,7 +1470,9 @@ template <class T>
 hipError_t launch_sample_t(const himuon_sampling &c, SampleParams p, int32_t *later, hipStream_t stream) {
   const T *z = reinterpret_cast<const T *>(c.logits);
   // (a stretch's list holds its kQuota largest for certain; settings of each row are not known here; what top_p alone
-  // keeps often takes more than a list or two: 4096 x 128256 bf16, 0.9: 553 us with 4 waves, 744 with 2, 923 with 1)
+  // keeps often takes more than a list or two: 4096 x 128256 bf16, 0.9: 522 us with 4 waves, 724 with 2, 918 with 1.
+  // Rows that keep more than the lists hold are read again: a top_k of a row's own from some 700 on with 4 waves (4096 x
+  // 128256 bf16: 934 us for 641, 1790 for 880), one for all rows above 1024 with 8 (1057 us for 1024, 2049 for 1500))
   const bool by_p = c.row_top_p || c.top_p < 1.;
   int least = c.row_top_k || (by_p && !c.top_k) ? 4 : 1;
   while (!c.row_top_k && least < 8 && most_of(least) < c.top_k) least *= 2;
