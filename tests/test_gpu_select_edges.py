@@ -147,3 +147,29 @@ def test_strides_compare_their_rows(N, V, pad, offset, dtype):
         got = sample(masked, uniform, **kw)
         assert check_sample(masked[:9], uniform[:9], [x[:9] for x in got], **kw) >= 8
         assert (got.token < V // 3).all()
+
+
+@pytest.mark.parametrize("N,V", [(12, 40000), (300, 9001), (1100, 9001), (2100, 9001), (4200, 9001), (300, 600)])
+@pytest.mark.parametrize("low", [-60.0, -20.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rest_of_rows_whose_largest_come_late(N, V, low, dtype):
+    """Every wave begins with logits far below the others'.  The rest's own largest is about as large as the row's, so its
+    powers have no distance to speak of: rounding it over T, a thread's V / 256 terms (at least) and a join of ten levels
+    are all."""
+    _need_gpu()
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn(N, V, generator=g)
+    turn = 256 * (4 if dtype is torch.float32 else 8)
+    z[:, (torch.arange(V) // turn) % 5 != 4] += low
+    z[:, -V // 8:] -= torch.where(z[:, -V // 8:] < low / 2, low, 0.0)
+    logits = z.to(dtype).to(DEV)
+    z = logits.double().cpu().sort(1, descending=True).values
+    for T in (1.0, 0.5):
+        for k in (1, 5, 60):
+            got = top_logits(logits, k, temperature=T)
+            want = (z[:, k:] / T).logsumexp(1)
+            tol = 2.0 ** -22 * (z[:, k].abs() / T + 2 + math.log(V)) + 2.0 ** -24 * (V / 256 + 24)
+            tol += 3 * 2.0 ** -24 * (z[:, 0] - z[:, k]) / T
+            error = (got.rest.double().cpu() - want).abs()
+            assert (error <= tol).all(), (T, k, float((error / tol).max()))
+            assert torch.equal(got.value.double().cpu(), z[:, :k])

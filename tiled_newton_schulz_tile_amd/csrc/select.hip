@@ -617,8 +617,8 @@ __device__ __forceinline__ u64 find_border_in_row(const T *z, int V, u64 first, 
 
 // A wave goes through turns [t0, t1) of a row, the first of which is in `now`, with a first logit that
 // powers are relative to and a first bound (which hold for the row).  exact: powers in fp64; else in fp32.
-// They are relative to a logit that follows the largest, and if CEIL (fp32 alone) to one that follows the
-// bound, above which nothing is summed.  turns: nullptr, or what each turn weighs.  last_quota: rank of the
+// They are relative to a logit that follows the largest by kFar, and if CEIL (fp32 alone) to the bound, above which
+// nothing is summed.  turns: nullptr, or what each turn weighs.  last_quota: rank of the
 // logit in the final list that last_bound is not above (0: none).
 template <class T, bool CEIL>
 __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0, int t1, const Wants &want, bool exact,
@@ -740,7 +740,7 @@ __device__ __forceinline__ Stretch sweep(Turn<T> &now, const T *z, int V, int t0
       // the bound rises, and what is below it is dropped
       bound = b;
       if (want.quota > 0) out.raised = b;
-      if (CEIL && b - ref > far) refer_to(b);
+      if (CEIL && b > ref) refer_to(b);   // (an fp32 power loses 2^-22 by each octave that it is away)
       close = threshold();
       int n = 0;
       for (int j = 0; j < out.n; j += 64) {
