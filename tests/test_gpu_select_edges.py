@@ -173,3 +173,37 @@ def test_rest_of_rows_whose_largest_come_late(N, V, low, dtype):
             error = (got.rest.double().cpu() - want).abs()
             assert (error <= tol).all(), (T, k, float((error / tol).max()))
             assert torch.equal(got.value.double().cpu(), z[:, :k])
+
+
+@pytest.mark.parametrize("N,V", [(12, 40000), (300, 9001), (1100, 9001), (2100, 9001), (4200, 9001), (300, 600)])
+@pytest.mark.parametrize("low", [-60.0, -20.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_log_probabilities_of_rows_whose_largest_come_late(N, V, low, dtype):
+    """Every wave begins with logits far below the others'; the tolerances are those of other rows."""
+    _need_gpu()
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn(N, V, generator=g)
+    turn = 256 * (4 if dtype is torch.float32 else 8)
+    z[:, (torch.arange(V) // turn) % 5 != 4] += low
+    z[:, -V // 8:] -= torch.where(z[:, -V // 8:] < low / 2, low, 0.0)
+    logits, uniform = z.to(dtype).to(DEV), torch.rand(N, generator=g).to(DEV)
+    some = torch.arange(0, N, N // 12 + 1)
+    for kw in (dict(top_k=1), dict(top_k=5), dict(top_k=60), dict(min_p=0.9), dict(min_p=0.5), dict(top_k=40, top_p=0.8)):
+        got = sample(logits, uniform, **kw)
+        assert check_sample(logits[some], uniform[some], [x[some] for x in got], **kw) >= len(some) - 1
+
+
+@pytest.mark.parametrize("N,V", [(12, 40000), (300, 9001), (1100, 9001), (2100, 9001), (4200, 9001)])
+@pytest.mark.parametrize("low", [-60.0, -30.0])
+def test_log_probabilities_beside_a_few_late_logits(N, V, low):
+    """The same with four large logits at the row's end, one of which is kept: the others' powers are nearly all that
+    the log probability has besides."""
+    _need_gpu()
+    g = torch.Generator().manual_seed(N)
+    z = torch.randn(N, V, generator=g) + low
+    z[:, [V - 700, V - 300, V - 9, V - 2]] = torch.rand(N, 4, generator=g)
+    logits, uniform = z.to(DEV), torch.rand(N, generator=g).to(DEV)
+    some = torch.arange(0, N, N // 100 + 1)
+    for kw in (dict(top_k=1), dict(top_k=2), dict(min_p=0.95)):
+        got = sample(logits, uniform, **kw)
+        assert check_sample(logits[some], uniform[some], [x[some] for x in got], **kw) >= len(some) - 1
